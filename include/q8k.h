@@ -77,9 +77,17 @@ typedef enum {
     Q8K_Q5_K = 4         /* GGUF Q5_K: 176-byte blocks, row-major block order   */
 } q8k_qtype;
 
+typedef enum {
+    Q8K_F32 = 0, /* activations of the serving operators: fp32, what the       */
+    Q8K_F16 = 1, /* projections above write and read, or 16-bit types          */
+    Q8K_BF16 = 2
+} q8k_dtype;
+
 #define Q8K_QK 256         /* values per K-quant super-block / q8_K block       */
 #define Q8K_COLS_MAX 8     /* most activation columns qmatvec_batched serves    */
 #define Q8K_MOE_MAX_TOKENS 256 /* most tokens qmatvec_moe serves per call       */
+#define Q8K_KV_PAGE 64     /* tokens in a page of the key/value cache           */
+#define Q8K_TOP_MAX 32     /* most alternatives qlogprobs returns a row         */
 #define Q8K_MOE_MAX_TOPK 64    /* most experts per token qmatvec_moe serves     */
 
 /* ---------------------------------------------------------------- sizing --
@@ -239,6 +247,119 @@ int qmatmul_prefill_moe(int qtype, const void* w, int64_t E, int64_t rows, int64
 #define Q8K_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 int qmatmul_prefill_moe_noalloc(int qtype, const void* w, int64_t E, int64_t rows, int64_t K, const void* xq,
                                 int64_t T, const int32_t* ids, const float* rw, int32_t topk, float* y, void* stream);
+
+/* ------------------------------------------- between the projections --
+ * What a serving step needs besides its projections: a paged key/value cache
+ * held in 8 bits, the attention that reads it, and the log probabilities of
+ * the output head's logits.  Activations are fp32 (as qmatvec* and
+ * qmatmul_prefill* write and q8k_pack reads them), fp16 or bf16 (dtype, a
+ * q8k_dtype); every sum, softmax statistic and accumulator is fp32.
+ *
+ * The cache (the page layout is the library's; other code reads it with
+ * q8k_kv_read): `pages` pages of Q8K_KV_PAGE tokens, q8k_kv_bytes(...) bytes.
+ * For each token and key/value head it holds the key's and the value's
+ * head_dim int8 codes and one fp32 scale each, by q8k_pack's rule with the
+ * head's row as the block (scale = amax/127, code = round-half-even(x *
+ * (127/amax)) clamped to [-127, 127]).  For each (page, head), one after
+ * another by page and then head, a record of 128 * head_dim + 512 bytes:
+ *   key codes   [head_dim/64][64 tokens][64]   planes of 64 of the values
+ *   value codes [head_dim][64 places]          token t at place
+ *       (t>>2 & 3) << 4 | (t>>5) << 3 | (t>>4 & 1) << 2 | (t & 3)
+ *   fp32 key scales [64 tokens], fp32 value scales [64 tokens].
+ * A fresh cache may hold anything.
+ * head_dim: 64, 128 or 256.  kv_heads <= 4096; pages <= 2^24. */
+typedef struct {
+    void* data; /* 16-byte aligned */
+    int64_t pages;
+    int32_t kv_heads;
+    int32_t head_dim;
+} q8k_kv_cache;
+
+/* Position rotation: row p of `table` (fp32 [positions][dim], 16-byte
+ * aligned) holds the cosines of position p's dim/2 angles, then their sines.
+ * The first `dim` values of a head (a multiple of 8, at most head_dim) turn in
+ * pairs, (a, b) -> (a cos - b sin, a sin + b cos): pair i is values
+ * (i, i + dim/2) for Q8K_ROPE_HALF, (2i, 2i + 1) for Q8K_ROPE_ADJACENT. */
+typedef enum { Q8K_ROPE_HALF = 0, Q8K_ROPE_ADJACENT = 1 } q8k_rope_pairs;
+typedef struct {
+    const float* table;
+    int64_t positions;
+    int32_t dim;
+    int32_t pairs;
+} q8k_rope;
+
+size_t q8k_kv_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim); /* 0 on a bad shape */
+
+/* q8k_kv_append: turn T tokens' keys by their positions, bring keys and values
+ * to 8 bits and write them into the cache.
+ * k, v: rows of kv_heads * head_dim values, one row a token, k_stride and
+ * v_stride elements apart (multiples of 8, so the rows may be slices of a
+ * fused q|k|v projection's output); 16-byte aligned.  pos int32 [T] and rope
+ * (host struct): the rotation; rope NULL: keys go in as they are, pos unused.
+ * slots int32 [T]: token t goes to place slots[t] % 64 of page slots[t] / 64.
+ * A token whose slot is outside [0, 64 * pages) or whose position is outside
+ * the table is not written (padding rows: slot -1).  The slots of one call
+ * that are written must differ.  Nothing else of the cache changes. */
+int q8k_kv_append(int dtype, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+                  const int32_t* pos, const q8k_rope* rope, const int32_t* slots, const q8k_kv_cache* kv,
+                  void* stream);
+
+/* q8k_kv_read: what the cache holds for T slots, code times scale (one fp32
+ * product, rounded once to dtype).  k, v: [T][kv_heads][head_dim]; zeros for
+ * a slot outside [0, 64 * pages). */
+int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T, void* k, void* v, void* stream);
+
+/* qattend: softmax attention of the new tokens of B sequences over the cache
+ * (which holds them already: append first).
+ *   s_j = scale * <q, key_j>,  out = sum_j softmax(s)_j value_j,  lse = log sum_j e^(s_j)
+ * over the tokens j that a new token sees: with n new tokens in a sequence of
+ * length len, new token i has index p = len - n + i and sees j <= p, and with
+ * window > 0 only j > p - window.  A token that sees nothing gets out = 0 and
+ * lse = -inf.
+ * q: rows of q_heads * head_dim values, one row a new token, q_stride elements
+ * apart (a multiple of 8), 16-byte aligned; q_heads a multiple of kv_heads,
+ * query head a reading key head a / (q_heads / kv_heads).  rope (with pos int32
+ * [Tq]): q is turned by its positions on the way; NULL: q is taken as it is.
+ * A token whose position is outside the table gets NaN.  q must be finite and
+ * below 2^100 in magnitude after the scale.
+ * cu_q int32 [B + 1]: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1]-1,
+ * ascending; Tq rows in all; rows of no sequence are left as they were in out
+ * and lse.  kv_len int32 [B]: its length, the new tokens included.  page_table
+ * int32 [B][max_pages]: its pages in order; pages may be shared between
+ * sequences; a page outside [0, pages) is not read and its tokens count as
+ * unseen.  max_q, max_len: what no sequence's new tokens and length exceed
+ * (max_len <= 64 * max_pages); a longer length is cut to max_len, new tokens
+ * beyond max_q are left out.
+ * out: [Tq][q_heads][head_dim] of dtype, 16-byte aligned; lse: NULL or fp32
+ * [Tq][q_heads], natural logarithms.
+ * ws / ws_bytes: caller-owned workspace, 16-byte aligned, of at least
+ * qattend_workspace_bytes(...) bytes (0: may be NULL): the fp32 results of
+ * splits over the keys, joined in a fixed order.  Its contents are scratch:
+ * stream-ordered calls may share it, calls that overlap in time may not. */
+size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                               int64_t max_len);
+int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
+            const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table, int64_t max_pages,
+            const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
+            const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* qlogprobs: of each of T rows of V logits (stride elements apart, any
+ * alignment of whole elements; 1 <= V <= 2^20)
+ *   lse = log sum_i e^(x_i),  logprob = x[target] - lse,
+ *   entropy = lse - sum_i softmax(x)_i x_i  (natural logarithms)
+ * and the topn (0 <= topn <= min(V, Q8K_TOP_MAX)) largest logits' ids and log
+ * probabilities, the largest first, equal logits by ascending id.
+ * targets int32 [T] and logprob fp32 [T]: both or neither NULL; a target
+ * outside [0, V) selects nothing: its logprob is NaN.  entropy, lse: NULL or
+ * fp32 [T].  top_ids int32 [T][topn], top_logprob fp32 [T][topn].
+ * Logits of -inf (banned tokens) are served; a row of nothing else has lse and
+ * log probabilities -inf and entropy 0.  A row with +inf or NaN has NaN for
+ * every real result; its top ids rank NaN below every number.
+ * ws / ws_bytes: as qattend's, qlogprobs_workspace_bytes(T, V, topn) bytes. */
+size_t qlogprobs_workspace_bytes(int64_t T, int64_t V, int32_t topn);
+int qlogprobs(int dtype, const void* logits, int64_t stride, int64_t T, int64_t V, const int32_t* targets,
+              float* logprob, float* entropy, float* lse, int32_t topn, int32_t* top_ids, float* top_logprob,
+              void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------- test support --
  * The exact integer sums of the path ("Language models on the device",

@@ -20,7 +20,9 @@ __all__ = [
     "qmatvec", "qmatvec_batched", "qmatvec_f32", "qmatvec_moe", "qmatmul_prefill_workspace_bytes", "qmatmul_prefill",
     "qmatmul_prefill_f32_workspace_bytes", "qmatmul_prefill_f32",
     "qmatmul_prefill_moe_workspace_bytes", "qmatmul_prefill_moe", "qmatmul_prefill_moe_noalloc",
-    "Q8K_NOALLOC_SCRATCH_BYTES", "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
+    "Q8K_NOALLOC_SCRATCH_BYTES", "Q8K_F32", "Q8K_F16", "Q8K_BF16", "Q8K_KV_PAGE", "Q8K_TOP_MAX", "Q8K_ROPE_HALF",
+    "Q8K_ROPE_ADJACENT", "KVCache", "Rope", "q8k_kv_bytes", "q8k_kv_append", "q8k_kv_read", "qattend_workspace_bytes",
+    "qattend", "qlogprobs_workspace_bytes", "qlogprobs", "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
     "q8k_debug_wave_sums", "q8k_debug_last_launches", "q8k_status_str", "q8k_last_error", "EXPORTED",
 ]
 
@@ -32,6 +34,13 @@ Q8K_COLS_MAX = 8
 Q8K_MOE_MAX_TOKENS = 256
 Q8K_MOE_MAX_TOPK = 64
 Q8K_NOALLOC_SCRATCH_BYTES = 64 << 20
+Q8K_F32 = 0
+Q8K_F16 = 1
+Q8K_BF16 = 2
+Q8K_KV_PAGE = 64
+Q8K_TOP_MAX = 32
+Q8K_ROPE_HALF = 0
+Q8K_ROPE_ADJACENT = 1
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libq8k.so")
 
@@ -41,7 +50,8 @@ EXPORTED = (
     "qmatvec_batched", "qmatvec_f32", "qmatvec_moe", "qmatmul_prefill_workspace_bytes", "qmatmul_prefill",
     "qmatmul_prefill_f32_workspace_bytes", "qmatmul_prefill_f32",
     "qmatmul_prefill_moe_workspace_bytes", "qmatmul_prefill_moe", "qmatmul_prefill_moe_noalloc",
-    "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
+    "q8k_kv_bytes", "q8k_kv_append", "q8k_kv_read", "qattend_workspace_bytes", "qattend", "qlogprobs_workspace_bytes",
+    "qlogprobs", "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
     "q8k_debug_wave_sums", "q8k_debug_last_launches", "q8k_status_str", "q8k_last_error",
 )
 
@@ -96,6 +106,31 @@ lib.qmatmul_prefill_moe.restype = _INT
 lib.qmatmul_prefill_moe.argtypes = [_INT, _P, _I64, _I64, _I64, _P, _I64, _P, _P, ctypes.c_int32, _P, _P, _SZ, _P]
 lib.qmatmul_prefill_moe_noalloc.restype = _INT
 lib.qmatmul_prefill_moe_noalloc.argtypes = [_INT, _P, _I64, _I64, _I64, _P, _I64, _P, _P, ctypes.c_int32, _P, _P]
+
+
+class _KVStruct(ctypes.Structure):
+    _fields_ = [("data", _P), ("pages", _I64), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("table", _P), ("positions", _I64), ("dim", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+
+lib.q8k_kv_bytes.restype = _SZ
+lib.q8k_kv_bytes.argtypes = [_I64, _I64, _I64]
+lib.q8k_kv_append.restype = _INT
+lib.q8k_kv_append.argtypes = [_INT, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P]
+lib.q8k_kv_read.restype = _INT
+lib.q8k_kv_read.argtypes = [_INT, _P, _P, _I64, _P, _P, _P]
+lib.qattend_workspace_bytes.restype = _SZ
+lib.qattend_workspace_bytes.argtypes = [_P, _I64, _I64, _I64, _I64, _I64]
+lib.qattend.restype = _INT
+lib.qattend.argtypes = [_INT, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, ctypes.c_float, _I64, _P,
+                        _P, _P, _P, _P, _SZ, _P]
+lib.qlogprobs_workspace_bytes.restype = _SZ
+lib.qlogprobs_workspace_bytes.argtypes = [_I64, _I64, ctypes.c_int32]
+lib.qlogprobs.restype = _INT
+lib.qlogprobs.argtypes = [_INT, _P, _I64, _I64, _I64, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _SZ, _P]
 lib.q8k_debug_subblock_sums.restype = _INT
 lib.q8k_debug_subblock_sums.argtypes = [_INT, _P, _I64, _I64, _P, _P, _P, _P]
 lib.q8k_debug_prefill_block_sums.restype = _INT
@@ -227,6 +262,111 @@ def qmatmul_prefill_moe_noalloc(qtype: int, w, E: int, rows: int, K: int, xq, T:
                                 stream=None) -> None:
     _check(lib.qmatmul_prefill_moe_noalloc(qtype, _ptr(w), E, rows, K, _ptr(xq), T, _ptr(ids), _ptr(rw), topk,
                                            _ptr(y), _stream(stream)))
+
+
+# ---- the key/value cache, attention and log probabilities.  These check their
+# tensors' devices and index types, which the C side cannot see.
+def _on(dev, what, t, dtype=None):
+    """Device pointer of a tensor argument on GPU ``dev`` (None -> NULL, an int passes through)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what} is {t.dtype}, {dtype} is taken")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+
+
+_TYPES = {Q8K_F32: torch.float32, Q8K_F16: torch.float16, Q8K_BF16: torch.bfloat16}
+
+
+class KVCache:
+    """A paged 8-bit key/value cache (q8k_kv_cache): ``data`` is a device buffer of
+    ``q8k_kv_bytes(pages, kv_heads, head_dim)`` bytes, kept alive by this object."""
+
+    def __init__(self, data, pages: int, kv_heads: int, head_dim: int):
+        need = q8k_kv_bytes(pages, kv_heads, head_dim)
+        if not isinstance(data, int) and data is not None:
+            if not data.is_contiguous() or data.numel() * data.element_size() < need:
+                raise ValueError(f"a cache of {pages} pages, {kv_heads} heads of {head_dim} is {need} contiguous bytes")
+        self.data, self.pages, self.kv_heads, self.head_dim = data, pages, kv_heads, head_dim
+        self.struct = _KVStruct(_ptr(data), pages, kv_heads, head_dim)
+        self.ref = ctypes.addressof(self.struct)
+
+
+class Rope:
+    """A position rotation (q8k_rope): ``table`` fp32 [positions][dim], cosines then sines,
+    kept alive by this object; ``pairs`` Q8K_ROPE_HALF or Q8K_ROPE_ADJACENT."""
+
+    def __init__(self, table, positions: int, dim: int, pairs: int = Q8K_ROPE_HALF):
+        if not isinstance(table, int) and table is not None:
+            if table.dtype is not torch.float32 or not table.is_contiguous() or table.numel() < positions * dim:
+                raise ValueError(f"a rotation table is contiguous fp32 [{positions}][{dim}]")
+        self.table, self.positions, self.dim, self.pairs = table, positions, dim, pairs
+        self.struct = _RopeStruct(_ptr(table), positions, dim, pairs)
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _kv(dev, kv):
+    _on(dev, "kv", kv.data)
+    return kv.ref
+
+
+def _rope(dev, rope):
+    if rope is None:
+        return None
+    _on(dev, "rope", rope.table)
+    return rope.ref
+
+
+def q8k_kv_bytes(pages: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.q8k_kv_bytes(pages, kv_heads, head_dim))
+
+
+def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
+    dev, t = _device(), _TYPES.get(dtype)
+    _check(lib.q8k_kv_append(dtype, _on(dev, "k", k, t), k_stride, _on(dev, "v", v, t), v_stride, T,
+                             _on(dev, "pos", pos, torch.int32), _rope(dev, rope),
+                             _on(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream(stream)))
+
+
+def q8k_kv_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
+    dev, t = _device(), _TYPES.get(dtype)
+    _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _on(dev, "slots", slots, torch.int32), T, _on(dev, "k", k, t),
+                           _on(dev, "v", v, t), _stream(stream)))
+
+
+def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
+    return int(lib.qattend_workspace_bytes(kv.ref, q_heads, B, Tq, max_q, max_len))
+
+
+def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
+            max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
+            ws_bytes: int = 0, stream=None) -> None:
+    dev, t = _device(), _TYPES.get(dtype)
+    i32 = torch.int32
+    _check(lib.qattend(dtype, _on(dev, "q", q, t), q_stride, q_heads, _kv(dev, kv), B, _on(dev, "cu_q", cu_q, i32), Tq,
+                       max_q, _on(dev, "page_table", page_table, i32), max_pages, _on(dev, "kv_len", kv_len, i32),
+                       max_len, scale, window, _on(dev, "pos", pos, i32), _rope(dev, rope), _on(dev, "out", out, t),
+                       _on(dev, "lse", lse, torch.float32), _on(dev, "ws", ws), ws_bytes, _stream(stream)))
+
+
+def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:
+    return int(lib.qlogprobs_workspace_bytes(T, V, topn))
+
+
+def qlogprobs(dtype: int, logits, stride: int, T: int, V: int, targets, logprob, entropy=None, lse=None, topn: int = 0,
+              top_ids=None, top_logprob=None, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    dev, f32 = _device(), torch.float32
+    _check(lib.qlogprobs(dtype, _on(dev, "logits", logits, _TYPES.get(dtype)), stride, T, V,
+                         _on(dev, "targets", targets, torch.int32), _on(dev, "logprob", logprob, f32),
+                         _on(dev, "entropy", entropy, f32), _on(dev, "lse", lse, f32), topn,
+                         _on(dev, "top_ids", top_ids, torch.int32), _on(dev, "top_logprob", top_logprob, f32),
+                         _on(dev, "ws", ws), ws_bytes, _stream(stream)))
 
 
 def q8k_debug_subblock_sums(qtype: int, w, rows: int, K: int, xq, y, S, stream=None) -> None:

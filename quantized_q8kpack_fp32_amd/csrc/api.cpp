@@ -451,6 +451,218 @@ static int prefill_moe_common(const char* fn, int qtype, const void* w, int64_t 
                                            y, ws, (hipStream_t)stream));
 }
 
+// ---- the paged key/value cache and the operators behind the projections
+constexpr int64_t MAX_PAGES = (int64_t)1 << 24;
+constexpr int64_t MAX_HEADS = (int64_t)1 << 12;
+constexpr int64_t MAX_LEN = (int64_t)1 << 30;
+constexpr int64_t MAX_BATCH = (int64_t)1 << 20;
+constexpr int64_t MAX_VOCAB = (int64_t)1 << 20;  // 128 chunks of a row's join
+
+static int check_dtype(const char* fn, int dtype) {
+    if (dtype != Q8K_F32 && dtype != Q8K_F16 && dtype != Q8K_BF16)
+        return fail(Q8K_ERR_ARG, "%s: dtype=%d must be Q8K_F32=0, Q8K_F16=1 or Q8K_BF16=2", fn, dtype);
+    return Q8K_OK;
+}
+
+static bool kv_dim(int32_t D) { return D == 64 || D == 128 || D == 256; }
+
+static int check_kv(const char* fn, const q8k_kv_cache* kv) {
+    if (!kv) return fail(Q8K_ERR_NULL, "%s: kv is NULL", fn);
+    if (!kv_dim(kv->head_dim))
+        return fail(Q8K_ERR_SHAPE, "%s: head_dim=%d not served (64, 128 or 256)", fn, (int)kv->head_dim);
+    if (kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS)
+        return fail(Q8K_ERR_SHAPE, "%s: kv_heads=%d out of range [1, %lld]", fn, (int)kv->kv_heads,
+                    (long long)MAX_HEADS);
+    Q8K_TRY(check_count(fn, "pages", kv->pages, MAX_PAGES));
+    return check_ptr(fn, "kv->data", kv->data, 16);
+}
+
+// The rotation's description and its positions; view.table is NULL without one.
+static int check_rope(const char* fn, const q8k_rope* rope, const int32_t* pos, int32_t D, RopeView* view) {
+    *view = RopeView{nullptr, 0, 0, 0};
+    if (!rope) return Q8K_OK;
+    Q8K_TRY(check_ptr(fn, "rope->table", rope->table, 16));
+    Q8K_TRY(check_ptr(fn, "pos", pos, 4));
+    if (rope->positions < 1 || rope->positions > MAX_LEN)
+        return fail(Q8K_ERR_SHAPE, "%s: rope->positions=%lld out of range [1, %lld]", fn, (long long)rope->positions,
+                    (long long)MAX_LEN);
+    if (rope->dim < 8 || rope->dim % 8 != 0 || rope->dim > D)
+        return fail(Q8K_ERR_SHAPE, "%s: rope->dim=%d must be a positive multiple of 8, at most head_dim=%d", fn,
+                    (int)rope->dim, (int)D);
+    if (rope->pairs != Q8K_ROPE_HALF && rope->pairs != Q8K_ROPE_ADJACENT)
+        return fail(Q8K_ERR_ARG, "%s: rope->pairs=%d must be Q8K_ROPE_HALF=0 or Q8K_ROPE_ADJACENT=1", fn,
+                    (int)rope->pairs);
+    *view = RopeView{rope->table, (int)rope->positions, rope->dim, rope->pairs == Q8K_ROPE_ADJACENT};
+    return Q8K_OK;
+}
+
+static int check_stride(const char* fn, const char* what, int64_t stride, int64_t least) {
+    if (stride < least || stride % 8 != 0 || stride > ((int64_t)1 << 32))
+        return fail(Q8K_ERR_SHAPE, "%s: %s=%lld must be a multiple of 8, at least the row's %lld values", fn, what,
+                    (long long)stride, (long long)least);
+    return Q8K_OK;
+}
+
+size_t q8k_kv_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim) {
+    if (pages < 0 || pages > MAX_PAGES || kv_heads < 1 || kv_heads > MAX_HEADS ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return 0;
+    return (size_t)pages * (size_t)kv_heads * (size_t)kv_record((int)head_dim);
+}
+
+int q8k_kv_append(int dtype, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+                  const int32_t* pos, const q8k_rope* rope, const int32_t* slots, const q8k_kv_cache* kv,
+                  void* stream) {
+    begin_call();
+    const char* fn = "q8k_kv_append";
+    Q8K_TRY(check_dtype(fn, dtype));
+    Q8K_TRY(check_kv(fn, kv));
+    Q8K_TRY(check_count(fn, "T", T, MAX_TOKENS));
+    const int64_t row = (int64_t)kv->kv_heads * kv->head_dim;
+    Q8K_TRY(check_stride(fn, "k_stride", k_stride, row));
+    Q8K_TRY(check_stride(fn, "v_stride", v_stride, row));
+    Q8K_TRY(check_ptr(fn, "k", k, 16));
+    Q8K_TRY(check_ptr(fn, "v", v, 16));
+    Q8K_TRY(check_ptr(fn, "slots", slots, 4));
+    KvAppend a{k, v, k_stride, v_stride, T, pos, slots, {}, static_cast<uint8_t*>(kv->data), kv->pages,
+               kv->kv_heads, dtype};
+    Q8K_TRY(check_rope(fn, rope, pos, kv->head_dim, &a.rope));
+    Q8K_TRY(check_grid(fn, (2 * T * row + 2047) / 2048));
+    if (T == 0 || kv->pages == 0) return Q8K_OK;
+    return launched(fn, launch_kv_append(kv->head_dim, a, (hipStream_t)stream));
+}
+
+int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T, void* k, void* v, void* stream) {
+    begin_call();
+    const char* fn = "q8k_kv_read";
+    Q8K_TRY(check_dtype(fn, dtype));
+    Q8K_TRY(check_kv(fn, kv));
+    Q8K_TRY(check_count(fn, "T", T, MAX_TOKENS));
+    Q8K_TRY(check_ptr(fn, "slots", slots, 4));
+    Q8K_TRY(check_ptr(fn, "k", k, 16));
+    Q8K_TRY(check_ptr(fn, "v", v, 16));
+    Q8K_TRY(check_grid(fn, (T * kv->kv_heads * kv->head_dim + 2047) / 2048));
+    if (T == 0) return Q8K_OK;
+    const KvRead a{static_cast<const uint8_t*>(kv->data), kv->pages, kv->kv_heads, dtype, slots, T, k, v};
+    return launched(fn, launch_kv_read(kv->head_dim, a, (hipStream_t)stream));
+}
+
+static int check_attend_sizes(const char* fn, const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq,
+                              int64_t max_q, int64_t max_len) {
+    if (q_heads < 1 || q_heads > MAX_HEADS || q_heads % kv->kv_heads != 0)
+        return fail(Q8K_ERR_SHAPE, "%s: q_heads=%lld must be a positive multiple of kv_heads=%d (at most %lld)", fn,
+                    (long long)q_heads, (int)kv->kv_heads, (long long)MAX_HEADS);
+    Q8K_TRY(check_count(fn, "B", B, MAX_BATCH));
+    Q8K_TRY(check_count(fn, "Tq", Tq, MAX_TOKENS));
+    Q8K_TRY(check_count(fn, "max_q", max_q, Tq));
+    return check_count(fn, "max_len", max_len, MAX_LEN);
+}
+
+size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                               int64_t max_len) {
+    const char* fn = "qattend_workspace_bytes";
+    if (!kv || !kv_dim(kv->head_dim) || kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS ||
+        check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len) != Q8K_OK || B == 0 || max_q == 0)
+        return 0;
+    return (size_t)attend_plan(B, Tq, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, 0).ws_bytes;
+}
+
+int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
+            const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table, int64_t max_pages,
+            const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
+            const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    begin_call();
+    const char* fn = "qattend";
+    Q8K_TRY(check_dtype(fn, dtype));
+    Q8K_TRY(check_kv(fn, kv));
+    Q8K_TRY(check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len));
+    Q8K_TRY(check_count(fn, "max_pages", max_pages, MAX_PAGES));
+    if (max_len > max_pages * KV_PAGE)
+        return fail(Q8K_ERR_SHAPE, "%s: max_len=%lld exceeds the page table's %lld pages of %d tokens", fn,
+                    (long long)max_len, (long long)max_pages, KV_PAGE);
+    Q8K_TRY(check_count(fn, "window", window, MAX_LEN));
+    if (!(scale - scale == 0.0f)) return fail(Q8K_ERR_ARG, "%s: scale=%g must be finite", fn, (double)scale);
+    Q8K_TRY(check_stride(fn, "q_stride", q_stride, q_heads * kv->head_dim));
+    Q8K_TRY(check_ptr(fn, "q", q, 16));
+    Q8K_TRY(check_ptr(fn, "cu_q", cu_q, 4));
+    Q8K_TRY(check_ptr(fn, "page_table", page_table, 4));
+    Q8K_TRY(check_ptr(fn, "kv_len", kv_len, 4));
+    Q8K_TRY(check_ptr(fn, "out", out, 16));
+    if (lse) Q8K_TRY(check_ptr(fn, "lse", lse, 4));
+    Attend a{};
+    Q8K_TRY(check_rope(fn, rope, pos, kv->head_dim, &a.rope));
+    const size_t need = qattend_workspace_bytes(kv, q_heads, B, Tq, max_q, max_len);
+    if (ws_bytes < need)
+        return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+    if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
+    if (B == 0 || max_q == 0) return Q8K_OK;
+    const AttendPlan p = attend_plan(B, Tq, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, window);
+    const int64_t group = q_heads / kv->kv_heads;
+    Q8K_TRY(check_grid(fn, (max_q * group + 15) / 16 * p.splits * B * kv->kv_heads));
+    Q8K_TRY(check_grid(fn, B * max_q * q_heads));  // the join's workgroups
+    a.q = q;
+    a.q_stride = q_stride;
+    a.q_heads = (int)q_heads;
+    a.heads = kv->kv_heads;
+    a.group = (int)group;
+    a.dtype = dtype;
+    a.cache = static_cast<const uint8_t*>(kv->data);
+    a.pages = kv->pages;
+    a.B = B;
+    a.cu_q = cu_q;
+    a.Tq = Tq;
+    a.max_q = max_q;
+    a.table = page_table;
+    a.max_pages = max_pages;
+    a.kv_len = kv_len;
+    a.max_len = max_len;
+    a.scale = scale;
+    a.window = window;
+    a.pos = pos;
+    a.out = out;
+    a.lse = lse;
+    return launched(fn, launch_attend(kv->head_dim, p, a, ws, (hipStream_t)stream));
+}
+
+size_t qlogprobs_workspace_bytes(int64_t T, int64_t V, int32_t topn) {
+    if (T <= 0 || T > MAX_TOKENS || V < 1 || V > MAX_VOCAB || topn < 0 || topn > Q8K_TOP_MAX || topn > V) return 0;
+    return (size_t)logprobs_ws_bytes(T, V, topn);
+}
+
+int qlogprobs(int dtype, const void* logits, int64_t stride, int64_t T, int64_t V, const int32_t* targets,
+              float* logprob, float* entropy, float* lse, int32_t topn, int32_t* top_ids, float* top_logprob,
+              void* ws, size_t ws_bytes, void* stream) {
+    begin_call();
+    const char* fn = "qlogprobs";
+    Q8K_TRY(check_dtype(fn, dtype));
+    Q8K_TRY(check_count(fn, "T", T, MAX_TOKENS));
+    if (V < 1 || V > MAX_VOCAB)
+        return fail(Q8K_ERR_SHAPE, "%s: V=%lld out of range [1, %lld]", fn, (long long)V, (long long)MAX_VOCAB);
+    if (stride < V || stride > ((int64_t)1 << 32))
+        return fail(Q8K_ERR_SHAPE, "%s: stride=%lld must be at least V=%lld", fn, (long long)stride, (long long)V);
+    if (topn < 0 || topn > Q8K_TOP_MAX || topn > V)
+        return fail(Q8K_ERR_ARG, "%s: topn=%d must be in [0, min(V=%lld, %d)]", fn, topn, (long long)V, Q8K_TOP_MAX);
+    Q8K_TRY(check_ptr(fn, "logits", logits, dtype == Q8K_F32 ? 4 : 2));
+    if (targets || logprob) {  // both or neither
+        Q8K_TRY(check_ptr(fn, "targets", targets, 4));
+        Q8K_TRY(check_ptr(fn, "logprob", logprob, 4));
+    }
+    if (entropy) Q8K_TRY(check_ptr(fn, "entropy", entropy, 4));
+    if (lse) Q8K_TRY(check_ptr(fn, "lse", lse, 4));
+    if (topn > 0) {
+        Q8K_TRY(check_ptr(fn, "top_ids", top_ids, 4));
+        Q8K_TRY(check_ptr(fn, "top_logprob", top_logprob, 4));
+    }
+    const size_t need = qlogprobs_workspace_bytes(T, V, topn);
+    if (ws_bytes < need)
+        return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+    if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
+    Q8K_TRY(check_grid(fn, T * ((V + 1023) / 1024)));
+    if (T == 0) return Q8K_OK;
+    const LogProbs a{logits, stride, T, V, dtype, targets, logprob, entropy, lse, topn, top_ids, top_logprob};
+    return launched(fn, launch_logprobs(a, ws, (hipStream_t)stream));
+}
+
 int q8k_debug_subblock_sums(int qtype, const void* w, int64_t rows, int64_t K, const void* xq, float* y, int32_t* S,
                             void* stream) {
     begin_call();

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kv_cache.h"
+
 namespace q8k {
 
 // Launch census: every launch notes its kernel's host handle for the calling
@@ -158,6 +160,85 @@ hipError_t noalloc_scratch(void** ptr);
 hipError_t launch_prefill_moe(int fmt, const uint8_t* w, const uint16_t* prefix, int64_t E, int64_t rows, int nb,
                               Acts a, int64_t T, const int32_t* ids, const float* rw, int topk, float* y, void* ws,
                               hipStream_t s);
+
+// ---- the paged key/value cache and the operators behind the projections
+// (layout: kv_cache.h); D is 64, 128 or 256.
+struct KvAppend {
+    const void* k;  // [T] rows of heads * D values, k_stride elements apart
+    const void* v;
+    int64_t k_stride, v_stride, T;
+    const int32_t* pos;
+    const int32_t* slots;
+    RopeView rope;
+    uint8_t* cache;
+    int64_t pages;
+    int heads, dtype;
+};
+hipError_t launch_kv_append(int D, const KvAppend& a, hipStream_t s);
+struct KvRead {
+    const uint8_t* cache;
+    int64_t pages;
+    int heads, dtype;
+    const int32_t* slots;
+    int64_t T;
+    void* k;  // [T][heads][D]
+    void* v;
+};
+hipError_t launch_kv_read(int D, const KvRead& a, hipStream_t s);
+
+// Attention.  A key head's q_heads / heads query heads of a sequence's new
+// tokens are its rows: row r is token r / group, head h * group + r % group.
+struct Attend {
+    const void* q;  // [Tq] rows of q_heads * D values, q_stride elements apart
+    int64_t q_stride;
+    int q_heads, heads, group, dtype;
+    const uint8_t* cache;
+    int64_t pages;
+    int64_t B;
+    const int32_t* cu_q;  // [B + 1]
+    int64_t Tq, max_q;
+    const int32_t* table;  // [B][max_pages]
+    int64_t max_pages;
+    const int32_t* kv_len;  // [B]
+    int64_t max_len;
+    float scale;
+    int64_t window;
+    const int32_t* pos;
+    RopeView rope;
+    void* out;   // [Tq][q_heads][D]
+    float* lse;  // [Tq][q_heads] or nullptr
+    // split over the keys: splits of `chunk` pages each, a tile's first at the
+    // multiple of `chunk` that holds its first page; with splits > 1 the
+    // fp32 results per split [splits][Tq * q_heads][D] and (maximum, sum)
+    // pairs [splits][Tq * q_heads] go to the workspace and are joined
+    int splits, chunk, tile_rows;
+    float* part;
+    float2* ml;
+};
+struct AttendPlan {
+    bool tiles;  // the 128-row tile of prompts; else the 16-row kernel
+    int splits, chunk;
+    int64_t ws_bytes;
+};
+AttendPlan attend_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
+                       int64_t window);
+hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s);
+
+// Log probabilities.
+struct LogProbs {
+    const void* x;  // [T] rows of V logits, stride elements apart
+    int64_t stride, T, V;
+    int dtype;
+    const int32_t* targets;
+    float* logprob;
+    float* entropy;
+    float* lse;
+    int topn;
+    int32_t* top_ids;
+    float* top_logprob;
+};
+int64_t logprobs_ws_bytes(int64_t T, int64_t V, int topn);
+hipError_t launch_logprobs(const LogProbs& a, void* ws, hipStream_t s);
 
 // ---- test support: the shipped kernels' integer sums (template flags of the
 // same kernels, which also write y as they ship)
