@@ -15,7 +15,6 @@ namespace {
 
 constexpr int WAVES = 4;
 constexpr int ROWS = 16;
-constexpr int64_t TARGET_WGS = 2048;
 
 // Probabilities enter the second product as fp16 pieces of p * vscale / R *
 // 2^15, R a power of two at least the largest vscale a wave has met: at most
@@ -316,25 +315,34 @@ hipError_t join_d(const Attend& a, hipStream_t s) {
 
 }  // namespace
 
+// Which kernel and which splits.  The tile kernel's workgroups fill the device
+// once they are two a compute unit; the 16-row kernel's are short and hide
+// their ends behind each other.
+constexpr int64_t DECODE_WGS = 2048, TILE_WGS = 512;
+constexpr int64_t TILE_FROM_ROWS = 33;
+
 AttendPlan attend_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
                        int64_t window) {
     AttendPlan p;
-    p.tiles = false;
-    const int64_t group = q_heads / heads, tiles = (max_q * group + ROWS - 1) / ROWS;
+    const int64_t group = q_heads / heads;
+    p.tiles = max_q * group >= TILE_FROM_ROWS;
+    p.tile_rows = p.tiles ? ATTEND_TILE_ROWS : ROWS;
+    const int64_t target = p.tiles ? TILE_WGS : DECODE_WGS, least = p.tiles ? 2 : WAVES;
+    const int64_t tiles = (max_q * group + p.tile_rows - 1) / p.tile_rows;
     const int64_t pages = (max_len + KV_PAGE - 1) / KV_PAGE, units = tiles * B * heads;
     const auto chunk_of = [&](int64_t live) {
-        const int64_t c = (units * live + TARGET_WGS - 1) / TARGET_WGS;
-        return c < WAVES ? WAVES : (c + WAVES - 1) / WAVES * WAVES;
+        const int64_t c = (units * live + target - 1) / target;
+        return c < least ? least : (c + least - 1) / least * least;
     };
     // the whole sequence; a window changes the chunk, never to more splits
     int64_t chunk = chunk_of(pages), splits = (pages + chunk - 1) / chunk;
     if (splits > 1 && window > 0) {
         // pages that a tile's rows see: at most the window and the tile's own tokens, from anywhere in a page
-        const int64_t tokens = max_q < ROWS / group + 2 ? max_q : ROWS / group + 2;
+        const int64_t most = p.tile_rows / group + 2, tokens = max_q < most ? max_q : most;
         const int64_t live = (window + tokens + KV_PAGE - 2) / KV_PAGE + 1;
         if (live < pages) {
             chunk = chunk_of(live);
-            while ((live + chunk - 2) / chunk + 1 > splits) chunk += WAVES;
+            while ((live + chunk - 2) / chunk + 1 > splits) chunk += least;
             splits = (live + chunk - 2) / chunk + 1;
         }
     }
@@ -349,12 +357,15 @@ AttendPlan attend_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, in
 hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s) {
     a.splits = p.splits;
     a.chunk = p.chunk;
-    a.tile_rows = ROWS;
+    a.tile_rows = p.tile_rows;
     a.part = static_cast<float*>(ws);
     a.ml = p.splits > 1 ? reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) +
                                                     align256((size_t)p.splits * a.Tq * a.q_heads * D * 4))
                         : nullptr;
-    const hipError_t e = D == 64 ? decode_d<64>(a, s) : D == 128 ? decode_d<128>(a, s) : decode_d<256>(a, s);
+    const hipError_t e = p.tiles     ? launch_attend_tiles(D, a, s)
+                         : D == 64   ? decode_d<64>(a, s)
+                         : D == 128  ? decode_d<128>(a, s)
+                                     : decode_d<256>(a, s);
     if (e != hipSuccess || p.splits == 1) return e;
     return D == 64 ? join_d<64>(a, s) : D == 128 ? join_d<128>(a, s) : join_d<256>(a, s);
 }

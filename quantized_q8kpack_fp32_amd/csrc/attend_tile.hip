@@ -1,0 +1,325 @@
+// Attention of many rows over the paged 8-bit cache: prompts and chunks of
+// them.  The formula of attend_decode.hip; here it is the matrix instructions
+// that bound it, so the codes become fp16 once for 64 RT rows and are read by
+// all waves from LDS.
+#include "attend.h"
+
+namespace q8k {
+
+namespace {
+
+constexpr float P_UP = 32768.0f, P_DOWN = 1.0f / 32768.0f;  // attend_decode.hip
+
+// One page's operands in LDS, in the order in which the lanes of a wave read
+// them: every read and write of 16 bytes a lane is 1 KB of consecutive bytes.
+template <int D>
+struct PageOps {
+    uint4 k[4][D / 32][64];  // [16 tokens][k step][lane]
+    uint4 v[D / 16][2][64];  // [16 values][32 tokens][lane]
+    float ks[KV_PAGE], vs[KV_PAGE];
+};
+
+// One workgroup: 64 RT rows of one key head over its split's pages, 16 RT rows
+// a wave.  While a page is multiplied, the next one's codes, in registers since
+// the page before, become fp16 in the other buffer, and the one after that is
+// on its way from memory: one barrier a page.
+template <int D, int WAVES, int RT, int NQ, int NP>
+__global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
+    constexpr int KS = D / 32, DB = D / 16, ROWS = 16 * RT * WAVES;
+    constexpr int KC = D / 16 / WAVES;  // 1 KB pieces of a page's keys (and of its values) a wave brings
+    __shared__ union {
+        PageOps<D> ops[2];
+        float q[WAVES][16][D + 4];  // the queries on their way to registers
+    } sm;
+    PageOps<D>* ops = sm.ops;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int64_t units = (int64_t)a.splits * a.B * a.heads;
+    // the last rows of a prompt see the most: they start first
+    const int tile = (int)(gridDim.x / units - 1 - blockIdx.x / units);
+    const int64_t u = blockIdx.x % units;
+    const int split = (int)(u % a.splits);
+    const int h = (int)(u / a.splits % a.heads);
+    const int64_t b = u / a.splits / a.heads;
+    const Sequence seq = sequence_of(a, b);
+    const int rows = seq.nq * a.group;
+    if (tile * ROWS >= rows) return;
+    const int last_row = min(rows, tile * ROWS + ROWS) - 1;
+    const Span lo = span_of(a, seq, tile * ROWS / a.group), hi = span_of(a, seq, last_row / a.group);
+    int p0 = lo.first / KV_PAGE, p1 = hi.last >= 0 ? hi.last / KV_PAGE + 1 : 0;
+    const int first_page = (p0 / a.chunk + split) * a.chunk;
+    p0 = max(p0, first_page);
+    p1 = min(p1, first_page + a.chunk);
+    if (a.splits > 1 && p0 >= p1) return;  // the join reads only splits that some row's span meets
+
+    // queries, 16 rows at a time through LDS
+    h8_t qf[RT][NQ][KS];
+    float unit[RT];
+    Span span[RT];
+    {
+        float(*qs)[D + 4] = sm.q[wave];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int row0 = tile * ROWS + (wave * RT + rt) * 16;
+            for (int i = lane; i < 16 * (D / 8); i += 64) {
+                const int r = i / (D / 8), item = i % (D / 8);
+                if (row0 + r < rows)
+                    load_q_item<D>(a, seq, h, row0 + r, item, qs[r]);
+                else {
+                    *reinterpret_cast<float4*>(&qs[r][8 * item]) = make_float4(0, 0, 0, 0);
+                    *reinterpret_cast<float4*>(&qs[r][8 * item + 4]) = make_float4(0, 0, 0, 0);
+                }
+            }
+            __syncthreads();
+            float amax = 0.0f;
+#pragma unroll
+            for (int s = 0; s < KS / 2; ++s)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    amax = fmaxf(amax, max4(*reinterpret_cast<const float4*>(&qs[col][64 * s + 16 * g + 4 * c])));
+            amax = groups_max(amax);
+            const int qe = 12 - exponent_of(amax);
+            const float qup = pow2f(qe);
+            unit[rt] = score_unit(a, qe);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                uint32_t w[4][2];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 v = *reinterpret_cast<const float2*>(&qs[col][64 * (s / 2) + 16 * g + 8 * (s & 1) + 2 * c]);
+                    f16_pieces<NQ>(v.x * qup, v.y * qup, w[c]);
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                    qf[rt][n][s] = __builtin_bit_cast(h8_t, make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]));
+            }
+            span[rt] = span_of(a, seq, min(row0 + col, rows - 1) / a.group);
+            __syncthreads();
+        }
+    }
+
+    // A page's codes on their way: wave w brings pieces w, w + WAVES, ... of the
+    // keys (16 tokens of one plane each) and of the values (16 rows each).
+    const int32_t* pages = a.table + b * a.max_pages;
+    struct Raw {
+        uint4 k[KC], v[KC];
+        float sc;
+        bool ok;
+    } raw;
+    const auto fetch = [&](int p) {
+        const int page = p < p1 ? pages[p] : -1;
+        raw.ok = page >= 0 && page < a.pages;
+        if (!raw.ok) return;
+        const uint8_t* rec = a.cache + ((int64_t)page * a.heads + h) * kv_record(D);
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            raw.k[c] = *reinterpret_cast<const uint4*>(rec + (wave + WAVES * c) * 1024 + col * 64 + g * 16);
+            raw.v[c] = *reinterpret_cast<const uint4*>(rec + KV_PAGE * D + (wave + WAVES * c) * 1024 + col * 64 + g * 16);
+        }
+        raw.sc = reinterpret_cast<const float*>(rec + 2 * KV_PAGE * D)[threadIdx.x & 127];
+    };
+    const auto put = [&](PageOps<D>& o) {
+        if (!raw.ok) return;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            // piece i of the keys: plane i / 4, tokens 16 (i % 4) and on
+            const int i = wave + WAVES * c;
+            o.k[i & 3][2 * (i >> 2)][lane] = __builtin_bit_cast(uint4, codes_f16(raw.k[c].x, raw.k[c].y));
+            o.k[i & 3][2 * (i >> 2) + 1][lane] = __builtin_bit_cast(uint4, codes_f16(raw.k[c].z, raw.k[c].w));
+            o.v[i][0][lane] = __builtin_bit_cast(uint4, codes_f16(raw.v[c].x, raw.v[c].y));
+            o.v[i][1][lane] = __builtin_bit_cast(uint4, codes_f16(raw.v[c].z, raw.v[c].w));
+        }
+        if (threadIdx.x < 2 * KV_PAGE) o.ks[threadIdx.x] = raw.sc;  // vs follows ks
+    };
+
+    float m[RT], l[RT], R = pow2f(-100), Rinv = pow2f(100) * P_UP;
+    f4_t acc[RT][DB];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = -INFINITY, l[rt] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) acc[rt][d] = f4_t{0, 0, 0, 0};
+    }
+    fetch(p0);
+    put(ops[0]);
+    bool ok = raw.ok;
+    fetch(p0 + 1);
+    __syncthreads();
+    for (int p = p0; p < p1; ++p) {
+        const PageOps<D>& o = ops[(p - p0) & 1];
+        const bool next_ok = raw.ok;
+        put(ops[(p - p0 + 1) & 1]);
+        fetch(p + 2);
+        if (ok) {
+            f4_t s4[RT][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) s4[rt][q] = f4_t{0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const h8_t k = __builtin_bit_cast(h8_t, o.k[q][s][lane]);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+                            s4[rt][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[rt][n][s], s4[rt][q], 0, 0, 0);
+                }
+            }
+            float vs[4][4];
+            float vmax = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 k = *reinterpret_cast<const float4*>(&o.ks[16 * q + 4 * g]);
+                const float4 v = *reinterpret_cast<const float4*>(&o.vs[16 * q + 4 * g]);
+                vs[q][0] = v.x, vs[q][1] = v.y, vs[q][2] = v.z, vs[q][3] = v.w;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    s4[rt][q][0] *= k.x;
+                    s4[rt][q][1] *= k.y;
+                    s4[rt][q][2] *= k.z;
+                    s4[rt][q][3] *= k.w;
+                }
+            }
+            // pages that some row sees only in part (what lies in unseen places
+            // may be anything, NaN scales included)
+            if (p * KV_PAGE < hi.first || p * KV_PAGE + KV_PAGE - 1 > lo.last) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = p * KV_PAGE + 16 * q + 4 * g + i;
+                        bool any = false;
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const bool seen = j >= span[rt].first && j <= span[rt].last;
+                            s4[rt][q][i] = seen ? s4[rt][q][i] : -INFINITY;
+                            any |= seen;
+                        }
+                        vs[q][i] = any ? vs[q][i] : 0.0f;
+                    }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vmax = fmaxf(vmax, vs[q][i]);
+            float tmax[RT];
+            bool grew = vmax > R;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                tmax[rt] = s4[rt][0][0];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmax[rt] = fmaxf(tmax[rt], s4[rt][q][i]);
+                tmax[rt] *= unit[rt];
+                grew |= tmax[rt] > m[rt];
+            }
+            if (__any(grew)) {
+                float Rn = R;
+                if (__any(vmax > R)) Rn = fmaxf(R, pow2f(exponent_of(wave_max(vmax)) + 1));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float mn = fmaxf(m[rt], groups_max(tmax[rt]));
+                    const float base = mn == -INFINITY ? 0.0f : mn;
+                    const float down = __builtin_amdgcn_exp2f(m[rt] - base);
+                    l[rt] *= down;
+                    const float both = down * (R / Rn);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) acc[rt][d] *= both;
+                    m[rt] = mn;
+                }
+                R = Rn;
+                Rinv = P_UP / Rn;
+            }
+            uint32_t pw[RT][NP][4][2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vs[q][i] *= Rinv;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float mb = m[rt] == -INFINITY ? 0.0f : m[rt];
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[rt][q][i], unit[rt], -mb));
+                        l[rt] += e[i];
+                        e[i] *= vs[q][i];
+                    }
+                    uint32_t w0[2], w1[2];
+                    f16_pieces<NP>(e[0], e[1], w0);
+                    f16_pieces<NP>(e[2], e[3], w1);
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) pw[rt][n][q][0] = w0[n], pw[rt][n][q][1] = w1[n];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const h8_t v = __builtin_bit_cast(h8_t, o.v[d][t][lane]);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n = 0; n < NP; ++n)
+                            acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                v,
+                                __builtin_bit_cast(h8_t, make_uint4(pw[rt][n][2 * t][0], pw[rt][n][2 * t][1],
+                                                                    pw[rt][n][2 * t + 1][0], pw[rt][n][2 * t + 1][1])),
+                                acc[rt][d], 0, 0, 0);
+                }
+        }
+        ok = next_ok;
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = tile * ROWS + (wave * RT + rt) * 16 + col;
+        const float lr = groups_sum(l[rt]);
+        if (row >= rows) continue;
+        const int64_t qr = q_row_of(a, seq, h, row);
+        const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
+        float f = R * P_DOWN;
+        if (a.splits > 1) {
+            const int64_t at = (int64_t)split * a.Tq * a.q_heads + qr;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                *reinterpret_cast<float4*>(a.part + at * D + 16 * d + 4 * g) =
+                    make_float4(acc[rt][d][0] * f, acc[rt][d][1] * f, acc[rt][d][2] * f, acc[rt][d][3] * f);
+            if (g == 0) a.ml[at] = make_float2(m[rt], lr);
+        } else {
+            f = lr == 0.0f ? 0.0f : f / lr;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                store4f(a.out, qr * D + 16 * d + 4 * g, a.dtype,
+                        make_float4(acc[rt][d][0] * f, acc[rt][d][1] * f, acc[rt][d][2] * f, acc[rt][d][3] * f));
+            if (g == 0 && a.lse) a.lse[qr] = lr == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(lr)) * LN2;
+        }
+    }
+}
+
+template <int D, int NQ, int NP>
+hipError_t tile_n(const Attend& a, hipStream_t s) {
+    // heads of 256 values: eight waves of 16 rows (four of 32 do not fit the register file)
+    constexpr int WAVES = D == 256 ? 8 : 4, RT = D == 256 ? 1 : 2;
+    static_assert(16 * WAVES * RT == ATTEND_TILE_ROWS, "rows of a tile");
+    const int64_t tiles = (a.max_q * a.group + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS;
+    Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, NQ, NP>), dim3((unsigned)(tiles * a.splits * a.B * a.heads)),
+               dim3(64 * WAVES), 0, s, a);
+    return hipGetLastError();
+}
+template <int D>
+hipError_t tile_d(const Attend& a, hipStream_t s) {
+    if (a.dtype != DT_BF16) return tile_n<D, 2, 2>(a, s);
+    return a.rope.table ? tile_n<D, 2, 1>(a, s) : tile_n<D, 1, 1>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_attend_tiles(int D, const Attend& a, hipStream_t s) {
+    return D == 64 ? tile_d<64>(a, s) : D == 128 ? tile_d<128>(a, s) : tile_d<256>(a, s);
+}
+
+}  // namespace q8k

@@ -217,11 +217,13 @@ struct Attend {
 };
 struct AttendPlan {
     bool tiles;  // the 128-row tile of prompts; else the 16-row kernel
-    int splits, chunk;
+    int splits, chunk, tile_rows;
     int64_t ws_bytes;
 };
 AttendPlan attend_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
                        int64_t window);
+constexpr int ATTEND_TILE_ROWS = 128;
+hipError_t launch_attend_tiles(int D, const Attend& a, hipStream_t s);  // attend_tile.hip
 hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s);
 
 // Log probabilities.
