@@ -171,10 +171,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# torch's current stream as the handle it is; building the stream object that
+# torch.cuda.current_stream() returns takes 2.8 us, most of a small call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -268,17 +273,22 @@ def qmatmul_prefill_moe_noalloc(qtype: int, w, E: int, rows: int, K: int, xq, T:
 # tensors' devices and index types, which the C side cannot see.
 def _on(dev, what, t, dtype=None):
     """Device pointer of a tensor argument on GPU ``dev`` (None -> NULL, an int passes through)."""
-    if t is None or isinstance(t, int):
+    if t.__class__ is int or t is None:
         return t
-    if t.get_device() != dev:
-        raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} is {t.dtype}, {dtype} is taken")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
     return t.data_ptr()
 
 
 def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+    """The current device, on which the calls below run (-1 on a machine without one)."""
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+if torch.cuda.device_count() > 0:
+    _device = torch.cuda.current_device  # noqa: F811
 
 
 _TYPES = {Q8K_F32: torch.float32, Q8K_F16: torch.float16, Q8K_BF16: torch.bfloat16}

@@ -35,6 +35,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     __shared__ float qs[ROWS][D + 4];
     __shared__ float red[WAVES][ROWS][2];
     __shared__ float acc_s[WAVES][ROWS][D + 4];
+    __shared__ float scales[WAVES][2 * KV_PAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     // block -> (row tile, split, sequence, head): tiles of the same pages are a
@@ -96,51 +97,87 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
 #pragma unroll
     for (int d = 0; d < DB; ++d) acc[d] = f4_t{0, 0, 0, 0};
     const int32_t* pages = a.table + b * a.max_pages;
+    const int lane_off = col * 64 + g * 16;
+    // A page's codes and scales on their way, one page ahead of the arithmetic:
+    // the keys' registers are loaded again as soon as the scores are there, the
+    // values' as soon as the second product is.
+    // Reads go through a buffer descriptor of one record; a page that selects
+    // nothing has an empty one, whose reads return zeros and touch no memory.
+    uint4 kraw[4][KS / 2], vraw[DB];
+    float ksc, vsc;
+    bool ok, next_ok;
+    const auto record_of = [&](int p, bool& good) {
+        const int page = p < p1 ? pages[p] : -1;
+        good = page >= 0 && page < a.pages;
+        return make_rsrc(a.cache + ((int64_t)(good ? page : 0) * a.heads + h) * kv_record(D), good ? kv_record(D) : 0);
+    };
+    const auto load_keys = [&](rsrc_t rec) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int s = 0; s < KS / 2; ++s) kraw[q][s] = load16(rec, lane_off + s * 4096 + q * 1024);
+        ksc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D));
+    };
+    const auto load_values = [&](rsrc_t rec) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) vraw[d] = load16(rec, lane_off + KV_PAGE * D + d * 1024);
+        vsc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D + 4 * KV_PAGE));
+    };
+    float* sc = scales[wave];
+    {
+        const rsrc_t rec = record_of(p0 + wave, ok);
+        load_keys(rec);
+        load_values(rec);
+    }
     for (int p = p0 + wave; p < p1; p += WAVES) {
-        const int page = pages[p];
-        if (page < 0 || page >= a.pages) continue;  // selects nothing
-        const uint8_t* rec = a.cache + ((int64_t)page * a.heads + h) * kv_record(D);
-        const uint8_t* kp = rec + col * 64 + g * 16;
-        const uint8_t* vp = rec + KV_PAGE * D + col * 64 + g * 16;
-        const float* sc = reinterpret_cast<const float*>(rec + 2 * KV_PAGE * D) + 4 * g;
+        const rsrc_t rec = record_of(p + WAVES, next_ok);
+        sc[lane] = ksc;
         float t[4][4];
-        uint4 vraw[DB];
+        {
+            f4_t s4[4];
 #pragma unroll
-        for (int d = 0; d < DB; ++d) vraw[d] = *reinterpret_cast<const uint4*>(vp + d * 1024);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            f4_t s4 = {0, 0, 0, 0};
+            for (int q = 0; q < 4; ++q) s4[q] = f4_t{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < KS / 2; ++s) {
-                const uint4 c = *reinterpret_cast<const uint4*>(kp + s * 4096 + q * 1024);
-                const h8_t k0 = codes_f16(c.x, c.y), k1 = codes_f16(c.z, c.w);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    s4 = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * s], s4, 0, 0, 0);
-                    s4 = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][2 * s + 1], s4, 0, 0, 0);
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 c = kraw[q][s];
+                    const h8_t k0 = codes_f16(c.x, c.y), k1 = codes_f16(c.z, c.w);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * s], s4[q], 0, 0, 0);
+                        s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][2 * s + 1], s4[q], 0, 0, 0);
+                    }
+                    if (q & 1) __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            const float4 ks = *reinterpret_cast<const float4*>(sc + 16 * q);
-            t[q][0] = s4[0] * ks.x;
-            t[q][1] = s4[1] * ks.y;
-            t[q][2] = s4[2] * ks.z;
-            t[q][3] = s4[3] * ks.w;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 ks = *reinterpret_cast<const float4*>(&sc[16 * q + 4 * g]);
+                t[q][0] = s4[q][0] * ks.x;
+                t[q][1] = s4[q][1] * ks.y;
+                t[q][2] = s4[q][2] * ks.z;
+                t[q][3] = s4[q][3] * ks.w;
+            }
         }
+        load_keys(rec);
+        __builtin_amdgcn_sched_barrier(0);
+        sc[KV_PAGE + lane] = vsc;
         float vs[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float4 v = *reinterpret_cast<const float4*>(sc + KV_PAGE + 16 * q);
+            const float4 v = *reinterpret_cast<const float4*>(&sc[KV_PAGE + 16 * q + 4 * g]);
             vs[q][0] = v.x, vs[q][1] = v.y, vs[q][2] = v.z, vs[q][3] = v.w;
         }
         // pages that some row sees only in part (what lies in unseen places may
         // be anything, NaN scales included)
-        if (p * KV_PAGE < hi.first || p * KV_PAGE + KV_PAGE - 1 > lo.last) {
+        if (!ok || p * KV_PAGE < hi.first || p * KV_PAGE + KV_PAGE - 1 > lo.last) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = p * KV_PAGE + 16 * q + 4 * g + i;
-                    const bool seen = j >= span.first && j <= span.last;
+                    const bool seen = ok && j >= span.first && j <= span.last;
                     t[q][i] = seen ? t[q][i] : -INFINITY;
                     vs[q][i] = seen ? vs[q][i] : 0.0f;
                 }
@@ -195,7 +232,11 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
                 acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, q0, acc[d], 0, 0, 0);
                 acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, q1, acc[d], 0, 0, 0);
             }
+            if (d & 1) __builtin_amdgcn_sched_barrier(0);
         }
+        load_values(rec);
+        __builtin_amdgcn_sched_barrier(0);
+        ok = next_ok;
     }
 
     // join the four waves
