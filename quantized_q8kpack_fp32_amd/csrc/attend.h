@@ -117,27 +117,183 @@ __device__ __forceinline__ Span span_of(const Attend& a, const Sequence& s, int 
     return p;
 }
 
-// One item (eight values) of query row `row`, turned.  The scale's sign goes
-// with the query (and a scale of zero makes it zero), its magnitude comes in
-// behind the products: score_unit.  A row whose position lies outside the
-// table is NaN.
+// ---- the work items
+// A sequence's rows of one key head make tiles of a.tile_rows rows.  A tile's
+// pages are cut into chunks of c pages from the tile's first page on; an item
+// is one tile and one chunk.  c goes by the lengths on the device, not by the
+// limits the host knows (a captured step may have been captured for lengths
+// far above today's): what makes about a.target items a head, of equal size
+// whatever mix of lengths there is, and then for each sequence what cuts its
+// pages evenly.  Items are numbered sequence by
+// sequence; every workgroup finds its own by adding up the sequences before it,
+// 64 at a time.  target == 0: one item a tile, numbered without looking.
+struct Item {
+    int64_t b, first;  // sequence; its first item's number
+    int c, splits;     // pages a chunk; chunks a tile
+    int tile, split;
+};
+// A sequence's chunks: as many as come nearest to c pages each.
+__device__ __forceinline__ int splits_of(int pages, int c) { return max(1, (pages + c / 2) / c); }
+__device__ __forceinline__ int chunk_pages(int pages, int splits) { return splits == 1 ? 1 << 30 : (pages + splits - 1) / splits; }
+struct Load {
+    int tiles, pages;  // of one sequence: tiles, and pages a tile reads at most
+};
+__device__ __forceinline__ Load load_of(const Attend& a, int64_t b) {
+    const Sequence s = sequence_of(a, b);
+    Load l;
+    l.tiles = (s.nq * a.group + a.tile_rows - 1) / a.tile_rows;
+    int first = span_of(a, s, 0).first / KV_PAGE;
+    const int last = span_of(a, s, s.nq - 1).last;
+    l.pages = last < 0 ? 0 : last / KV_PAGE + 1 - first;
+    if (a.window > 0 && l.tiles > 1) {
+        // a tile's rows see the window and its own tokens, from anywhere in a page
+        const int64_t t = (a.window + a.tile_rows / a.group + 2 + KV_PAGE - 2) / KV_PAGE + 1;
+        if (t < l.pages) l.pages = (int)t;
+    }
+    return l;
+}
+__device__ __forceinline__ int64_t wave_sum_int64(int64_t v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor((long long)v, off, WAVE);
+    return v;
+}
+// The sequence of this lane among 64 from b0 on.
+__device__ __forceinline__ Load lane_load(const Attend& a, int64_t b0) {
+    const int64_t b = b0 + (threadIdx.x & 63);
+    return b < a.B ? load_of(a, b) : Load{0, 0};
+}
+
+// Pages a chunk (called by whole waves; l0: lane_load(a, 0)).
+__device__ __forceinline__ int chunk_of(const Attend& a, const Load& l0) {
+    int64_t total = wave_sum_int64((int64_t)l0.tiles * l0.pages);
+    for (int64_t b0 = 64; b0 < a.B; b0 += 64) {
+        const Load l = lane_load(a, b0);
+        total += wave_sum_int64((int64_t)l.tiles * l.pages);
+    }
+    const int64_t c = (total + a.target - 1) / a.target;
+    return (int)(c < a.least ? a.least : c);
+}
+// Item `w` of a head; false: there is none of that number.
+__device__ __forceinline__ bool item_of(const Attend& a, int64_t w, Item& it) {
+    if (a.target == 0) {
+        it = Item{w / a.tiles_max, w - w % a.tiles_max, 1 << 30, 1, (int)(w % a.tiles_max), 0};
+        return it.b < a.B;
+    }
+    const int lane = threadIdx.x & 63;
+    Load l = lane_load(a, 0);
+    const int c = chunk_of(a, l);
+    int64_t before = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
+        if (b0 > 0) l = lane_load(a, b0);
+        const int splits = splits_of(l.pages, c), n = l.tiles * splits;
+        int upto = n;  // inclusive prefix sum
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int t = __shfl_up(upto, off, WAVE);
+            if (lane >= off) upto += t;
+        }
+        const uint64_t hit = __ballot(w < before + upto);
+        if (hit) {
+            const int at = __builtin_ctzll(hit);
+            const int rest = (int)(w - before) - __builtin_amdgcn_readlane(upto - n, at);
+            it.b = b0 + at;
+            it.first = w - rest;
+            it.splits = __builtin_amdgcn_readlane(splits, at);
+            it.c = chunk_pages(__builtin_amdgcn_readlane(l.pages, at), it.splits);
+            it.tile = rest / it.splits;
+            it.split = rest % it.splits;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+// First item and chunking of sequence b.
+__device__ __forceinline__ Item items_of(const Attend& a, int64_t b) {
+    const int lane = threadIdx.x & 63;
+    Load l = lane_load(a, 0);
+    Item it{b, 0, 0, 1, 0, 0};
+    const int c = chunk_of(a, l);
+    for (int64_t b0 = 0; b0 <= b; b0 += 64) {
+        if (b0 > 0) l = lane_load(a, b0);
+        const int splits = splits_of(l.pages, c);
+        it.first += wave_sum_int64(b0 + lane < b ? l.tiles * splits : 0);
+        if (b < b0 + 64) {
+            it.splits = __builtin_amdgcn_readlane(splits, (int)(b - b0));
+            it.c = chunk_pages(__builtin_amdgcn_readlane(l.pages, (int)(b - b0)), it.splits);
+        }
+    }
+    return it;
+}
+
+// A tile's rows and pages.
+struct Tile {
+    int row0, rows;   // its first row; rows of the sequence and head
+    Span lo, hi;      // of its first and last row
+    int p0, p1;       // its pages
+};
+__device__ __forceinline__ Tile tile_of(const Attend& a, const Sequence& s, int tile) {
+    Tile t;
+    t.rows = s.nq * a.group;
+    t.row0 = tile * a.tile_rows;
+    const int last = min(t.rows, t.row0 + a.tile_rows) - 1;
+    t.lo = span_of(a, s, t.row0 / a.group);
+    t.hi = span_of(a, s, last / a.group);
+    t.p0 = t.lo.first / KV_PAGE;
+    t.p1 = t.hi.last >= 0 ? t.hi.last / KV_PAGE + 1 : 0;
+    return t;
+}
+
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+// An item's sequence and tile, their numbers as scalars: the page loop's
+// addresses and branches then cost no vector instructions.
+__device__ __forceinline__ Sequence item_sequence(const Attend& a, const Item& it) {
+    const Sequence s = sequence_of(a, it.b);
+    return Sequence{uni(s.q0), uni(s.n), uni(s.nq), uni(s.len)};
+}
+__device__ __forceinline__ Tile item_tile(const Attend& a, const Sequence& s, int tile) {
+    const Tile t = tile_of(a, s, tile);
+    return Tile{uni(t.row0), uni(t.rows), {uni(t.lo.first), uni(t.lo.last)}, {uni(t.hi.first), uni(t.hi.last)}, uni(t.p0), uni(t.p1)};
+}
+
+// ---- queries
+// One item (eight values) of a query row on its way from memory.  The scale's
+// sign goes with the query (and a scale of zero makes it zero), its magnitude
+// comes in behind the products: score_unit.  A row whose position lies outside
+// the table is NaN.
+struct QueryItem {
+    float4 x, y, c, s;
+    int oa, ob, p;
+};
+__device__ __forceinline__ int64_t q_token(const Attend& a, const Sequence& s, int row) { return s.q0 + row / a.group; }
 template <int D>
-__device__ __forceinline__ void load_q_item(const Attend& a, const Sequence& s, int h, int row, int item, float* dst) {
-    const int tok = row / a.group, t = s.q0 + tok;
-    const int64_t base = (int64_t)t * a.q_stride + (int64_t)(h * a.group + row % a.group) * D;
-    int oa, ob;
-    kv_item(a.rope, item, oa, ob);
-    float4 x = load4f(a.q, base + oa, a.dtype), y = load4f(a.q, base + ob, a.dtype);
+__device__ __forceinline__ void fetch_q(const Attend& a, const Sequence& s, int h, int row, int item, QueryItem& q) {
+    const int64_t t = q_token(a, s, row);
+    const int64_t base = t * a.q_stride + (int64_t)(h * a.group + row % a.group) * D;
+    kv_item(a.rope, item, q.oa, q.ob);
+    q.p = a.rope.table ? a.pos[t] : 0;
+    q.x = load4f(a.q, base + q.oa, a.dtype);
+    q.y = load4f(a.q, base + q.ob, a.dtype);
+}
+__device__ __forceinline__ void fetch_turn(const Attend& a, int item, QueryItem& q) {
+    if (a.rope.table && 8 * item < a.rope.dim && q.p >= 0 && q.p < a.rope.len) {
+        const float* row = a.rope.table + (int64_t)q.p * a.rope.dim + 4 * item;
+        q.c = *reinterpret_cast<const float4*>(row);
+        q.s = *reinterpret_cast<const float4*>(row + a.rope.dim / 2);
+    }
+}
+__device__ __forceinline__ void put_q(const Attend& a, int item, QueryItem& q, float* dst) {
     float f = a.scale > 0.0f ? 1.0f : a.scale < 0.0f ? -1.0f : 0.0f;
     if (a.rope.table) {
-        const int p = a.pos[t];
-        if (p >= 0 && p < a.rope.len)
-            kv_turn(a.rope, a.rope.table + (int64_t)p * a.rope.dim, item, x, y);
-        else
+        if (q.p >= 0 && q.p < a.rope.len) {
+            if (8 * item < a.rope.dim) kv_turn(a.rope, q.c, q.s, q.x, q.y);
+        } else {
             f = __builtin_nanf("");
+        }
     }
-    *reinterpret_cast<float4*>(dst + oa) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-    *reinterpret_cast<float4*>(dst + ob) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+    *reinterpret_cast<float4*>(dst + q.oa) = make_float4(q.x.x * f, q.x.y * f, q.x.z * f, q.x.w * f);
+    *reinterpret_cast<float4*>(dst + q.ob) = make_float4(q.y.x * f, q.y.y * f, q.y.z * f, q.y.w * f);
 }
 
 // What a product of codes with a query that was multiplied by 2^e counts in
@@ -145,6 +301,34 @@ __device__ __forceinline__ void load_q_item(const Attend& a, const Sequence& s, 
 __device__ __forceinline__ float score_unit(const Attend& a, int e) {
     const float s = fabsf(a.scale);
     return fmaxf((s > 0.0f ? s * LOG2E : 1.0f) * pow2f(-e), 1.17549435e-38f);
+}
+
+// The operand of a query row from LDS, in pieces times 2^(12 - e), e the
+// exponent of the row's largest magnitude; returns the row's score_unit.  Step
+// 2 s + t of lane group g holds values 64 s + 16 g + 8 t + j.
+template <int D, int NQ>
+__device__ __forceinline__ float query_operand(const Attend& a, const float* row, int g, h8_t (&qf)[NQ][D / 32]) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < D / 64; ++s)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) amax = fmaxf(amax, max4(*reinterpret_cast<const float4*>(row + 64 * s + 16 * g + 4 * c)));
+    amax = groups_max(amax);
+    const int qe = 12 - exponent_of(amax);
+    const float up = pow2f(qe);
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        uint32_t w[4][2];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float2 v = *reinterpret_cast<const float2*>(row + 64 * (s / 2) + 16 * g + 8 * (s & 1) + 2 * c);
+            f16_pieces<NQ>(v.x * up, v.y * up, w[c]);
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+            qf[n][s] = __builtin_bit_cast(h8_t, make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]));
+    }
+    return score_unit(a, qe);
 }
 
 __device__ __forceinline__ int64_t q_row_of(const Attend& a, const Sequence& s, int h, int row) {

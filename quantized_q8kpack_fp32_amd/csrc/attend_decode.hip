@@ -38,65 +38,25 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     __shared__ float scales[WAVES][2 * KV_PAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    // block -> (row tile, split, sequence, head): tiles of the same pages are a
-    // multiple of the units apart
-    const int64_t units = (int64_t)a.splits * a.B * a.heads;
-    const int tile = (int)(blockIdx.x / units);
-    const int64_t u = blockIdx.x % units;
-    const int split = (int)(u % a.splits);
-    const int h = (int)(u / a.splits % a.heads);
-    const int64_t b = u / a.splits / a.heads;
-    const Sequence seq = sequence_of(a, b);
-    const int rows = seq.nq * a.group;
-    if (tile * ROWS >= rows) return;
-    const int last_row = min(rows, tile * ROWS + ROWS) - 1;
-    const Span lo = span_of(a, seq, tile * ROWS / a.group), hi = span_of(a, seq, last_row / a.group);
-    int p0 = lo.first / KV_PAGE, p1 = hi.last >= 0 ? hi.last / KV_PAGE + 1 : 0;
-    const int first_page = (p0 / a.chunk + split) * a.chunk;  // splits start at multiples of the chunk
-    p0 = max(p0, first_page);
-    p1 = min(p1, first_page + a.chunk);
-    if (a.splits > 1 && p0 >= p1) return;  // the join reads only splits that some row's span meets
+    const int h = (int)(blockIdx.x % a.heads);
+    const int64_t item = blockIdx.x / a.heads;
+    Item it;
+    if (!item_of(a, item, it)) return;
+    const Sequence seq = item_sequence(a, it);
+    const Tile tile = item_tile(a, seq, it.tile);
+    if (tile.row0 >= tile.rows) return;
+    const int p0 = uni(tile.p0 + it.split * it.c), p1 = uni(min(tile.p1, p0 + it.c));
+    if (it.splits > 1 && p0 >= p1) return;  // the join reads only chunks that some row's span meets
 
-    for (int i = threadIdx.x; i < ROWS * (D / 8); i += 64 * WAVES) {
-        const int r = i / (D / 8), row = tile * ROWS + r;
-        if (row < rows)
-            load_q_item<D>(a, seq, h, row, i % (D / 8), qs[r]);
-        else {
-            *reinterpret_cast<float4*>(&qs[r][8 * (i % (D / 8))]) = make_float4(0, 0, 0, 0);
-            *reinterpret_cast<float4*>(&qs[r][8 * (i % (D / 8)) + 4]) = make_float4(0, 0, 0, 0);
-        }
+    // the queries and the first page set out together
+    constexpr int NI = (ROWS * (D / 8) + 64 * WAVES - 1) / (64 * WAVES);
+    QueryItem qi[NI];
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+        const int i = threadIdx.x + 64 * WAVES * n, r = tile.row0 + i / (D / 8);
+        if (i < ROWS * (D / 8) && r < tile.rows) fetch_q<D>(a, seq, h, r, i % (D / 8), qi[n]);
     }
-    __syncthreads();
-    // Q^T operands: step 2 s + t of lane group g holds values 64 s + 16 g + 8 t + j
-    float amax = 0.0f;
-#pragma unroll
-    for (int s = 0; s < KS / 2; ++s)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) amax = fmaxf(amax, max4(*reinterpret_cast<const float4*>(&qs[col][64 * s + 16 * g + 4 * c])));
-    amax = groups_max(amax);
-    const int qe = 12 - exponent_of(amax);  // the row's largest value goes to [2^12, 2^13)
-    const float qup = pow2f(qe), unit = score_unit(a, qe);
-    h8_t qf[NQ][KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        uint32_t w[4][2];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float2 v = *reinterpret_cast<const float2*>(&qs[col][64 * (s / 2) + 16 * g + 8 * (s & 1) + 2 * c]);
-            f16_pieces<NQ>(v.x * qup, v.y * qup, w[c]);
-        }
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-            qf[n][s] = __builtin_bit_cast(h8_t, make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]));
-    }
-
-    const int row = tile * ROWS + col;
-    Span span = span_of(a, seq, min(row, rows - 1) / a.group);
-    float m = -INFINITY, l = 0.0f, R = pow2f(-100), Rinv = pow2f(100) * P_UP;
-    f4_t acc[DB];
-#pragma unroll
-    for (int d = 0; d < DB; ++d) acc[d] = f4_t{0, 0, 0, 0};
-    const int32_t* pages = a.table + b * a.max_pages;
+    const int32_t* pages = a.table + it.b * a.max_pages;
     const int lane_off = col * 64 + g * 16;
     // A page's codes and scales on their way, one page ahead of the arithmetic:
     // the keys' registers are loaded again as soon as the scores are there, the
@@ -107,7 +67,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     float ksc, vsc;
     bool ok, next_ok;
     const auto record_of = [&](int p, bool& good) {
-        const int page = p < p1 ? pages[p] : -1;
+        const int page = __builtin_amdgcn_readfirstlane(p < p1 ? pages[p] : -1);
         good = page >= 0 && page < a.pages;
         return make_rsrc(a.cache + ((int64_t)(good ? page : 0) * a.heads + h) * kv_record(D), good ? kv_record(D) : 0);
     };
@@ -129,6 +89,26 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
         load_keys(rec);
         load_values(rec);
     }
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+        const int i = threadIdx.x + 64 * WAVES * n, r = i / (D / 8), q = i % (D / 8);
+        if (i >= ROWS * (D / 8)) continue;
+        if (tile.row0 + r < tile.rows) {
+            fetch_turn(a, q, qi[n]);
+            put_q(a, q, qi[n], qs[r]);
+        } else {
+            *reinterpret_cast<float4*>(&qs[r][8 * q]) = make_float4(0, 0, 0, 0);
+            *reinterpret_cast<float4*>(&qs[r][8 * q + 4]) = make_float4(0, 0, 0, 0);
+        }
+    }
+    __syncthreads();
+    h8_t qf[NQ][KS];
+    const float unit = query_operand<D, NQ>(a, qs[col], g, qf);
+    const Span span = span_of(a, seq, min(tile.row0 + col, tile.rows - 1) / a.group);
+    float m = -INFINITY, l = 0.0f, R = pow2f(-100), Rinv = pow2f(100) * P_UP;
+    f4_t acc[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) acc[d] = f4_t{0, 0, 0, 0};
     for (int p = p0 + wave; p < p1; p += WAVES) {
         const rsrc_t rec = record_of(p + WAVES, next_ok);
         sc[lane] = ksc;
@@ -171,7 +151,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
         }
         // pages that some row sees only in part (what lies in unseen places may
         // be anything, NaN scales included)
-        if (!ok || p * KV_PAGE < hi.first || p * KV_PAGE + KV_PAGE - 1 > lo.last) {
+        if (!ok || p * KV_PAGE < tile.hi.first || p * KV_PAGE + KV_PAGE - 1 > tile.lo.last) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -255,7 +235,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     __syncthreads();
     for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * WAVES) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
-        if (tile * ROWS + r >= rows) break;
+        if (tile.row0 + r >= tile.rows) break;
         float mr = red[0][r][0];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) mr = fmaxf(mr, red[w][r][0]);
@@ -268,9 +248,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             const float4 v = *reinterpret_cast<const float4*>(&acc_s[w][r][c]);
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
         }
-        const int64_t qr = q_row_of(a, seq, h, tile * ROWS + r);
-        if (a.splits > 1) {
-            const int64_t at = (int64_t)split * a.Tq * a.q_heads + qr;
+        const int64_t qr = q_row_of(a, seq, h, tile.row0 + r);
+        if (it.splits > 1) {
+            const int64_t at = (item * a.heads + h) * ROWS + r;
             *reinterpret_cast<float4*>(a.part + at * D + c) = o;
             if (c == 0) a.ml[at] = make_float2(mr, lr);
         } else {
@@ -281,66 +261,91 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     }
 }
 
-// Joins the splits of each row, in their order.  One workgroup a row, four
-// values a lane: wave w adds splits w, w + 4, ... and the waves' sums are
-// added in their order.
-template <int D>
+// Joins the chunks of each row, always in the same order.  W waves a row (four
+// where rows are few and chunks many, one where it is the other way round):
+// wave w adds chunks w, w + W, ...  Lanes first take a chunk each (its maximum
+// and sum), then D/64 values of every chunk's result.
+template <int D, int W>
 __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
-    constexpr int L = D / 4;        // lanes a split
-    constexpr int N = 256 / L;      // splits at a time
-    __shared__ float4 o_s[N][L];
-    __shared__ float2 ml_s[N];
-    const int64_t per = a.max_q * a.group;  // rows a head, at most
-    const int64_t bh = blockIdx.x / per;
-    const int row = (int)(blockIdx.x % per), h = (int)(bh % a.heads);
-    const Sequence seq = sequence_of(a, bh / a.heads);
+    constexpr int N = D / 64;
+    __shared__ float o_s[4][D];
+    __shared__ float2 ml_s[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t per = (int64_t)a.max_q * a.group;  // rows a sequence and head, at most
+    const int64_t id = W == 4 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+    const int64_t bh = id / per;
+    if (bh >= a.B * a.heads) return;
+    const int row = (int)(id % per), h = (int)(bh % a.heads);
+    const Item it = items_of(a, bh / a.heads);
+    if (it.splits == 1) return;
+    const Sequence seq = item_sequence(a, it);
     if (row >= seq.nq * a.group) return;
+    const int ti = row / a.tile_rows, r = row % a.tile_rows;
+    const Tile tile = item_tile(a, seq, ti);
     const Span span = span_of(a, seq, row / a.group);
-    const int c = 4 * (threadIdx.x % L), n = threadIdx.x / L;
-    const int64_t qr = q_row_of(a, seq, h, row), rows = a.Tq * a.q_heads;
-    // the splits that the row's span meets, counted from its tile's first
-    const int base_split = span_of(a, seq, row / a.tile_rows * a.tile_rows / a.group).first / KV_PAGE / a.chunk;
-    const int s0 = span.first / KV_PAGE / a.chunk - base_split;
-    const int s1 = span.last >= 0 ? span.last / KV_PAGE / a.chunk + 1 - base_split : s0;
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-    for (int s = s0 + n; s < s1; s += N) {
-        const int64_t at = s * rows + qr;
-        const float2 ml = a.ml[at];
-        const float4 v = *reinterpret_cast<const float4*>(a.part + at * D + c);
-        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.0f : mn;
-        const float x = __builtin_amdgcn_exp2f(m - base), y = __builtin_amdgcn_exp2f(ml.x - base);
-        l = l * x + ml.y * y;
-        o.x = o.x * x + v.x * y, o.y = o.y * x + v.y * y, o.z = o.z * x + v.z * y, o.w = o.w * x + v.w * y;
+    const int s0 = uni((span.first / KV_PAGE - tile.p0) / it.c);
+    const int s1 = uni(span.last >= 0 ? (span.last / KV_PAGE - tile.p0) / it.c + 1 : s0);
+    const int64_t first = it.first + (int64_t)ti * it.splits, step = (int64_t)a.heads * a.tile_rows;
+    float m = -INFINITY, l = 0.0f, o[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) o[n] = 0.0f;
+    const int w = W == 4 ? wave : 0;
+    for (int s = s0 + w; s < s1; s += 64 * W) {
+        const int64_t at = ((first + s) * a.heads + h) * a.tile_rows + r;
+        const int count = min(64, (s1 - s + W - 1) / W);
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < count) ml = a.ml[at + lane * W * step];
+        const float* part = a.part + at * D + N * lane;
+        const float mn = fmaxf(m, wave_max(ml.x)), base = mn == -INFINITY ? 0.0f : mn;
+        const float down = __builtin_amdgcn_exp2f(m - base), y = __builtin_amdgcn_exp2f(ml.x - base);
+        l = l * down + wave_sum_dpp(ml.y * y);
+#pragma unroll
+        for (int n = 0; n < N; ++n) o[n] *= down;
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+            const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, y), i));
+            const float* x = part + i * W * step * D;
+#pragma unroll
+            for (int n = 0; n < N; ++n) o[n] += x[n] * f;
+        }
         m = mn;
     }
-    o_s[n][threadIdx.x % L] = o;
-    if (c == 0) ml_s[n] = make_float2(m, l);
-    __syncthreads();
-    if (n != 0) return;
-    float mt = ml_s[0].x;
+    if (W == 4) {
 #pragma unroll
-    for (int i = 1; i < N; ++i) mt = fmaxf(mt, ml_s[i].x);
-    const float base = mt == -INFINITY ? 0.0f : mt;
-    l = 0.0f;
-    o = make_float4(0, 0, 0, 0);
+        for (int n = 0; n < N; ++n) o_s[wave][N * lane + n] = o[n];
+        if (lane == 0) ml_s[wave] = make_float2(m, l);
+        __syncthreads();
+        if (wave != 0) return;
+        m = fmaxf(fmaxf(ml_s[0].x, ml_s[1].x), fmaxf(ml_s[2].x, ml_s[3].x));
+        const float base = m == -INFINITY ? 0.0f : m;
+        l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float y = __builtin_amdgcn_exp2f(ml_s[i].x - base);
-        const float4 v = o_s[i][threadIdx.x];
-        l += ml_s[i].y * y;
-        o.x += v.x * y, o.y += v.y * y, o.z += v.z * y, o.w += v.w * y;
+        for (int n = 0; n < N; ++n) o[n] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float y = __builtin_amdgcn_exp2f(ml_s[i].x - base);
+            l += ml_s[i].y * y;
+#pragma unroll
+            for (int n = 0; n < N; ++n) o[n] += o_s[i][N * lane + n] * y;
+        }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    store4f(a.out, qr * D + c, a.dtype, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (c == 0 && a.lse) a.lse[qr] = l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * LN2;
+    const int64_t qr = q_row_of(a, seq, h, row);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l, base = m == -INFINITY ? 0.0f : m;
+    const int64_t to = qr * D + N * lane;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const float v = o[n] * inv;
+        if (a.dtype == DT_F32)
+            static_cast<float*>(a.out)[to + n] = v;
+        else
+            static_cast<uint16_t*>(a.out)[to + n] = (uint16_t)(a.dtype == DT_BF16 ? to_bf16(v) : to_f16(v));
+    }
+    if (lane == 0 && a.lse) a.lse[qr] = l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * LN2;
 }
 
 template <int D, int NQ, int NP>
 hipError_t decode_n(const Attend& a, hipStream_t s) {
-    const int64_t tiles = (a.max_q * a.group + ROWS - 1) / ROWS;
-    Q8K_LAUNCH((attend_decode_kernel<D, NQ, NP>), dim3((unsigned)(tiles * a.splits * a.B * a.heads)), dim3(64 * WAVES), 0, s,
-               a);
+    Q8K_LAUNCH((attend_decode_kernel<D, NQ, NP>), dim3((unsigned)(a.items * a.heads)), dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
 template <int D>
@@ -349,66 +354,63 @@ hipError_t decode_d(const Attend& a, hipStream_t s) {
     return a.rope.table ? decode_n<D, 2, 1>(a, s) : decode_n<D, 1, 1>(a, s);
 }
 template <int D>
-hipError_t join_d(const Attend& a, hipStream_t s) {
-    Q8K_LAUNCH(attend_join_kernel<D>, dim3((unsigned)(a.B * a.heads * a.max_q * a.group)), dim3(256), 0, s, a);
+hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
+    const int64_t rows = a.B * a.heads * a.max_q * a.group;
+    if (tiles)
+        Q8K_LAUNCH((attend_join_kernel<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a);
+    else
+        Q8K_LAUNCH((attend_join_kernel<D, 4>), dim3((unsigned)rows), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Which kernel and which splits.  The tile kernel's workgroups fill the device
-// once they are two a compute unit; the 16-row kernel's are short and hide
-// their ends behind each other.
-constexpr int64_t DECODE_WGS = 2048, TILE_WGS = 512;
+// Which kernel and how many work items.  Items of a size for TARGET_WGS
+// workgroups, two a compute unit: more and smaller ones measured slower (each
+// has its queries to bring and its results to join), fewer leave units idle
+// where lengths differ.  A call that has several times as many tiles is not
+// split, nor is one of more sequences than the workgroups care to look through.
+constexpr int64_t TARGET_WGS = 512;
 constexpr int64_t TILE_FROM_ROWS = 33;
+constexpr int64_t SPLIT_MAX_BATCH = 256;
 
-AttendPlan attend_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
-                       int64_t window) {
+AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {
     AttendPlan p;
     const int64_t group = q_heads / heads;
     p.tiles = max_q * group >= TILE_FROM_ROWS;
     p.tile_rows = p.tiles ? ATTEND_TILE_ROWS : ROWS;
-    const int64_t target = p.tiles ? TILE_WGS : DECODE_WGS, least = p.tiles ? 2 : WAVES;
-    const int64_t tiles = (max_q * group + p.tile_rows - 1) / p.tile_rows;
-    const int64_t pages = (max_len + KV_PAGE - 1) / KV_PAGE, units = tiles * B * heads;
-    const auto chunk_of = [&](int64_t live) {
-        const int64_t c = (units * live + target - 1) / target;
-        return c < least ? least : (c + least - 1) / least * least;
-    };
-    // the whole sequence; a window changes the chunk, never to more splits
-    int64_t chunk = chunk_of(pages), splits = (pages + chunk - 1) / chunk;
-    if (splits > 1 && window > 0) {
-        // pages that a tile's rows see: at most the window and the tile's own tokens, from anywhere in a page
-        const int64_t most = p.tile_rows / group + 2, tokens = max_q < most ? max_q : most;
-        const int64_t live = (window + tokens + KV_PAGE - 2) / KV_PAGE + 1;
-        if (live < pages) {
-            chunk = chunk_of(live);
-            while ((live + chunk - 2) / chunk + 1 > splits) chunk += least;
-            splits = (live + chunk - 2) / chunk + 1;
-        }
+    p.tiles_max = (int)((max_q * group + p.tile_rows - 1) / p.tile_rows);
+    p.least = p.tiles ? 8 : 4 * WAVES;
+    const int64_t tiles = B * p.tiles_max, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
+    p.split = pages > p.least && B <= SPLIT_MAX_BATCH && tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
+    p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;
+    p.items = tiles;
+    if (p.split) {
+        const int64_t most = tiles * (1 + pages / p.least);
+        p.items = tiles + p.target < most ? tiles + p.target : most;
     }
-    if (splits < 1) splits = 1;
-    if (splits == 1) chunk = pages > 0 ? pages : 1;
-    p.chunk = (int)chunk;
-    p.splits = (int)splits;
-    p.ws_bytes = splits > 1 ? align256((size_t)splits * Tq * q_heads * D * 4) + (size_t)splits * Tq * q_heads * 8 : 0;
+    const int64_t rows = p.items * heads * p.tile_rows;
+    p.ws_bytes = p.split ? align256(rows * D * 4) + rows * 8 : 0;
     return p;
 }
 
 hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s) {
-    a.splits = p.splits;
-    a.chunk = p.chunk;
     a.tile_rows = p.tile_rows;
+    a.tiles_max = p.tiles_max;
+    a.least = p.least;
+    a.target = p.target;
+    a.items = p.items;
     a.part = static_cast<float*>(ws);
-    a.ml = p.splits > 1 ? reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) +
-                                                    align256((size_t)p.splits * a.Tq * a.q_heads * D * 4))
-                        : nullptr;
+    if (p.split)
+        a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(p.items * a.heads * p.tile_rows * D * 4));
     const hipError_t e = p.tiles     ? launch_attend_tiles(D, a, s)
                          : D == 64   ? decode_d<64>(a, s)
                          : D == 128  ? decode_d<128>(a, s)
                                      : decode_d<256>(a, s);
-    if (e != hipSuccess || p.splits == 1) return e;
-    return D == 64 ? join_d<64>(a, s) : D == 128 ? join_d<128>(a, s) : join_d<256>(a, s);
+    if (e != hipSuccess || !p.split) return e;
+    return D == 64    ? join_d<64>(a, p.tiles, s)
+           : D == 128 ? join_d<128>(a, p.tiles, s)
+                      : join_d<256>(a, p.tiles, s);
 }
 
 }  // namespace q8k

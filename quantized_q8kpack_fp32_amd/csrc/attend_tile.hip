@@ -34,23 +34,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     PageOps<D>* ops = sm.ops;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    const int64_t units = (int64_t)a.splits * a.B * a.heads;
+    const int h = (int)(blockIdx.x % a.heads);
     // the last rows of a prompt see the most: they start first
-    const int tile = (int)(gridDim.x / units - 1 - blockIdx.x / units);
-    const int64_t u = blockIdx.x % units;
-    const int split = (int)(u % a.splits);
-    const int h = (int)(u / a.splits % a.heads);
-    const int64_t b = u / a.splits / a.heads;
-    const Sequence seq = sequence_of(a, b);
-    const int rows = seq.nq * a.group;
-    if (tile * ROWS >= rows) return;
-    const int last_row = min(rows, tile * ROWS + ROWS) - 1;
-    const Span lo = span_of(a, seq, tile * ROWS / a.group), hi = span_of(a, seq, last_row / a.group);
-    int p0 = lo.first / KV_PAGE, p1 = hi.last >= 0 ? hi.last / KV_PAGE + 1 : 0;
-    const int first_page = (p0 / a.chunk + split) * a.chunk;
-    p0 = max(p0, first_page);
-    p1 = min(p1, first_page + a.chunk);
-    if (a.splits > 1 && p0 >= p1) return;  // the join reads only splits that some row's span meets
+    const int64_t item = a.items - 1 - blockIdx.x / a.heads;
+    Item it;
+    if (!item_of(a, item, it)) return;
+    const Sequence seq = item_sequence(a, it);
+    const Tile tile = item_tile(a, seq, it.tile);
+    const int rows = tile.rows;
+    if (tile.row0 >= rows) return;
+    const int p0 = uni(tile.p0 + it.split * it.c), p1 = uni(min(tile.p1, p0 + it.c));
+    if (it.splits > 1 && p0 >= p1) return;  // the join reads only chunks that some row's span meets
 
     // queries, 16 rows at a time through LDS
     h8_t qf[RT][NQ][KS];
@@ -60,39 +54,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
         float(*qs)[D + 4] = sm.q[wave];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int row0 = tile * ROWS + (wave * RT + rt) * 16;
+            const int row0 = tile.row0 + (wave * RT + rt) * 16;
             for (int i = lane; i < 16 * (D / 8); i += 64) {
-                const int r = i / (D / 8), item = i % (D / 8);
-                if (row0 + r < rows)
-                    load_q_item<D>(a, seq, h, row0 + r, item, qs[r]);
-                else {
-                    *reinterpret_cast<float4*>(&qs[r][8 * item]) = make_float4(0, 0, 0, 0);
-                    *reinterpret_cast<float4*>(&qs[r][8 * item + 4]) = make_float4(0, 0, 0, 0);
+                const int r = i / (D / 8), q = i % (D / 8);
+                if (row0 + r < rows) {
+                    QueryItem qi;
+                    fetch_q<D>(a, seq, h, row0 + r, q, qi);
+                    fetch_turn(a, q, qi);
+                    put_q(a, q, qi, qs[r]);
+                } else {
+                    *reinterpret_cast<float4*>(&qs[r][8 * q]) = make_float4(0, 0, 0, 0);
+                    *reinterpret_cast<float4*>(&qs[r][8 * q + 4]) = make_float4(0, 0, 0, 0);
                 }
             }
             __syncthreads();
-            float amax = 0.0f;
-#pragma unroll
-            for (int s = 0; s < KS / 2; ++s)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    amax = fmaxf(amax, max4(*reinterpret_cast<const float4*>(&qs[col][64 * s + 16 * g + 4 * c])));
-            amax = groups_max(amax);
-            const int qe = 12 - exponent_of(amax);
-            const float qup = pow2f(qe);
-            unit[rt] = score_unit(a, qe);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                uint32_t w[4][2];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float2 v = *reinterpret_cast<const float2*>(&qs[col][64 * (s / 2) + 16 * g + 8 * (s & 1) + 2 * c]);
-                    f16_pieces<NQ>(v.x * qup, v.y * qup, w[c]);
-                }
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    qf[rt][n][s] = __builtin_bit_cast(h8_t, make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]));
-            }
+            unit[rt] = query_operand<D, NQ>(a, qs[col], g, qf[rt]);
             span[rt] = span_of(a, seq, min(row0 + col, rows - 1) / a.group);
             __syncthreads();
         }
@@ -100,14 +76,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
 
     // A page's codes on their way: wave w brings pieces w, w + WAVES, ... of the
     // keys (16 tokens of one plane each) and of the values (16 rows each).
-    const int32_t* pages = a.table + b * a.max_pages;
+    const int32_t* pages = a.table + it.b * a.max_pages;
     struct Raw {
         uint4 k[KC], v[KC];
         float sc;
         bool ok;
     } raw;
     const auto fetch = [&](int p) {
-        const int page = p < p1 ? pages[p] : -1;
+        const int page = __builtin_amdgcn_readfirstlane(p < p1 ? pages[p] : -1);
         raw.ok = page >= 0 && page < a.pages;
         if (!raw.ok) return;
         const uint8_t* rec = a.cache + ((int64_t)page * a.heads + h) * kv_record(D);
@@ -183,7 +159,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
             }
             // pages that some row sees only in part (what lies in unseen places
             // may be anything, NaN scales included)
-            if (p * KV_PAGE < hi.first || p * KV_PAGE + KV_PAGE - 1 > lo.last) {
+            if (p * KV_PAGE < tile.hi.first || p * KV_PAGE + KV_PAGE - 1 > tile.lo.last) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -276,14 +252,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = tile * ROWS + (wave * RT + rt) * 16 + col;
+        const int r = (wave * RT + rt) * 16 + col, row = tile.row0 + r;
         const float lr = groups_sum(l[rt]);
         if (row >= rows) continue;
         const int64_t qr = q_row_of(a, seq, h, row);
         const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
         float f = R * P_DOWN;
-        if (a.splits > 1) {
-            const int64_t at = (int64_t)split * a.Tq * a.q_heads + qr;
+        if (it.splits > 1) {
+            const int64_t at = (item * a.heads + h) * ROWS + r;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
                 *reinterpret_cast<float4*>(a.part + at * D + 16 * d + 4 * g) =
@@ -305,8 +281,7 @@ hipError_t tile_n(const Attend& a, hipStream_t s) {
     // heads of 256 values: eight waves of 16 rows (four of 32 do not fit the register file)
     constexpr int WAVES = D == 256 ? 8 : 4, RT = D == 256 ? 1 : 2;
     static_assert(16 * WAVES * RT == ATTEND_TILE_ROWS, "rows of a tile");
-    const int64_t tiles = (a.max_q * a.group + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS;
-    Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, NQ, NP>), dim3((unsigned)(tiles * a.splits * a.B * a.heads)),
+    Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, NQ, NP>), dim3((unsigned)(a.items * a.heads)),
                dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }

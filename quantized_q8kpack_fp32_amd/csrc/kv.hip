@@ -43,7 +43,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppend a) {
     const void* src = is_v ? a.v : a.k;
     const int64_t base = t * (is_v ? a.v_stride : a.k_stride) + (int64_t)h * D;
     float4 x = load4f(src, base + oa, a.dtype), y = load4f(src, base + ob, a.dtype);
-    if (turn) kv_turn(r, turn, item, x, y);
+    if (turn && 8 * item < r.dim)
+        kv_turn(r, *reinterpret_cast<const float4*>(turn + 4 * item),
+                *reinterpret_cast<const float4*>(turn + r.dim / 2 + 4 * item), x, y);
     const float amax = group_max<L>(fmaxf(max4(x), max4(y)));
     const float iscale = 127.0f / amax;
     const uint32_t cx = amax != 0.0f ? kv_codes4(x, iscale) : 0u, cy = amax != 0.0f ? kv_codes4(y, iscale) : 0u;

@@ -88,14 +88,11 @@ __device__ __forceinline__ void store4f(void* p, int64_t i, int dt, float4 v) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = w;
 }
 
-// The rotation of one item by the table's row.  Each product and each sum is
+// The rotation of one item by its cosines and sines.  Each product and each sum is
 // rounded by itself (no fused multiply-add): these values decide integer
 // codes, and so they come out the same wherever they are computed that way.
-__device__ __forceinline__ void kv_turn(const RopeView& r, const float* row, int item, float4& a, float4& b) {
+__device__ __forceinline__ void kv_turn(const RopeView& r, float4 c, float4 s, float4& a, float4& b) {
 #pragma clang fp contract(off)
-    if (8 * item >= r.dim) return;
-    const float4 c = *reinterpret_cast<const float4*>(row + 4 * item);
-    const float4 s = *reinterpret_cast<const float4*>(row + r.dim / 2 + 4 * item);
     const float4 x = a, y = b;
     if (r.adjacent) {
         a.x = x.x * c.x - x.y * s.x;

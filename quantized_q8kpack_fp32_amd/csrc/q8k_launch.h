@@ -207,21 +207,23 @@ struct Attend {
     RopeView rope;
     void* out;   // [Tq][q_heads][D]
     float* lse;  // [Tq][q_heads] or nullptr
-    // split over the keys: splits of `chunk` pages each, a tile's first at the
-    // multiple of `chunk` that holds its first page; with splits > 1 the
-    // fp32 results per split [splits][Tq * q_heads][D] and (maximum, sum)
-    // pairs [splits][Tq * q_heads] go to the workspace and are joined
-    int splits, chunk, tile_rows;
+    // Split over the keys (attend.h): tiles of tile_rows rows, at most
+    // tiles_max a sequence and head; chunks of at least `least` pages, as many
+    // as make about `target` work items a head.  fp32 results of items that are
+    // one of several of their rows go to the workspace, [item][tile_rows][D] and
+    // (maximum, sum) pairs [item][tile_rows], and are joined.
+    int tile_rows, tiles_max, least, target;
+    int64_t items;  // work items a head, at most
     float* part;
     float2* ml;
 };
 struct AttendPlan {
     bool tiles;  // the 128-row tile of prompts; else the 16-row kernel
-    int splits, chunk, tile_rows;
-    int64_t ws_bytes;
+    bool split;  // some sequence may be split
+    int tile_rows, tiles_max, least, target;
+    int64_t items, ws_bytes;
 };
-AttendPlan attend_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
-                       int64_t window);
+AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D);
 constexpr int ATTEND_TILE_ROWS = 128;
 hipError_t launch_attend_tiles(int D, const Attend& a, hipStream_t s);  // attend_tile.hip
 hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s);

@@ -307,6 +307,24 @@ def test_attend_looser_maxima(q):
     assert_within(got[[0, 1, 3]], want[[0, 1, 3]], bo[[0, 1, 3]], "out, two tokens")
 
 
+@pytest.mark.parametrize("B,D,H,Hq,window", [(70, 64, 1, 2, 0), (130, 128, 2, 2, 0), (257, 64, 1, 1, 0), (90, 64, 1, 4, 150)])
+def test_attend_many_sequences(q, B, D, H, Hq, window):
+    """Mixed lengths of more sequences than a wave has lanes, few enough and too
+    many to be split, with limits far above the lengths."""
+    g = np.random.default_rng(B)
+    lens = [int(n) for n in g.integers(0, 300, B)]
+    lens[B // 2], lens[B - 1], lens[3] = 6000, 3000, 0
+    news = [int(n) for n in g.integers(0, 3, B)]
+    news[B // 2] = 2
+    g, raw, table, cu = attend_case(D, H, lens, news, B + 1)
+    table = np.concatenate([table, np.full((B, 400), -1, np.int32)], 1)
+    qx = round_to(g.standard_normal((int(cu[-1]), Hq, D)), "f32")
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, window, None, None, "half", D, "f32")
+    got, gl = run_attend(q, raw, table, cu, lens, qx, D, "f32", window, None, None, "half", max_len=25000, max_q=5)
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
 def test_attend_far_pages(q):
     """Pages beyond 4 GiB of the cache."""
     import torch

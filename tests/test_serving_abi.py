@@ -120,16 +120,20 @@ def test_attend_refusals(q):
 
 
 def test_attend_workspace_is_bounded(q):
-    """The splits' results take at most what 2048 workgroups of 16 rows, and as
-    many again for what rounding up adds, write."""
-    for B in (1, 3, 64, 1000):
-        for n in (1, 5, 700):
-            for length in (n, 4000, 1 << 20):
-                c = kv(q, heads=8, dim=128)
+    """The parts' results take no more than one item a tile and the 512 items
+    that fill the device, whatever the lengths: a call captured for a million
+    tokens costs no more than one for ten thousand."""
+    for B in (1, 3, 64, 256, 1000):
+        for n in (1, 5, 8, 9, 700):
+            c = kv(q, heads=8, dim=128)
+            rows = 16 if 4 * n <= 32 else 128
+            tiles = B * -(-4 * n // rows)
+            last = 0
+            for length in (n, 4000, 10000, 1 << 20):
                 need = q.qattend_workspace_bytes(c, 32, B, B * n, n, length)
-                rows = B * n * 32
-                splits = need / (rows * (128 * 4 + 8))
-                assert splits == 0 or 2 <= splits <= 1 + max(2, 2 * 2048 / max(1, rows / 16)) + 256 / rows, (B, n, length, splits)
+                assert last <= need <= (tiles + 64) * 8 * rows * (128 * 4 + 8) + 256, (B, n, length)
+                last = need
+    assert q.qattend_workspace_bytes(kv(q, heads=8, dim=128), 32, 1, 1, 1, 64) == 0
     bad = kv(q, dim=72)
     assert q.qattend_workspace_bytes(bad, 4, 1, 1, 1, 100) == 0
     assert q.qattend_workspace_bytes(kv(q), 3, 1, 1, 1, 100) == 0
