@@ -61,6 +61,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     // A page's codes and scales on their way, one page ahead of the arithmetic:
     // the keys' registers are loaded again as soon as the scores are there, the
     // values' as soon as the second product is.
+    // The codes are read once, which the loads say (non-temporal: 8 x 65537
+    // tokens at 6.1 TB/s, 5.4 without).
     // Reads go through a buffer descriptor of one record; a page that selects
     // nothing has an empty one, whose reads return zeros and touch no memory.
     uint4 kraw[4][KS / 2], vraw[DB];
@@ -75,12 +77,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int s = 0; s < KS / 2; ++s) kraw[q][s] = load16(rec, lane_off + s * 4096 + q * 1024);
+            for (int s = 0; s < KS / 2; ++s) kraw[q][s] = load16_nt(rec, lane_off + s * 4096 + q * 1024);
         ksc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D));
     };
     const auto load_values = [&](rsrc_t rec) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d) vraw[d] = load16(rec, lane_off + KV_PAGE * D + d * 1024);
+        for (int d = 0; d < DB; ++d) vraw[d] = load16_nt(rec, lane_off + KV_PAGE * D + d * 1024);
         vsc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D + 4 * KV_PAGE));
     };
     float* sc = scales[wave];
