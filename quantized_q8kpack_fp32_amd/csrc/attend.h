@@ -10,9 +10,6 @@ typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float LOG2E = 1.4426950408889634f;
-
 // Eight int8 codes as eight fp16 values, exactly: a code's byte with its sign
 // bit flipped is code + 128, which under the exponent byte 0x64 reads
 // 1024 + code + 128; subtracting 1152 leaves the code.  Five instructions for

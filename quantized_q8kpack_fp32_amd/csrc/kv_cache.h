@@ -8,6 +8,9 @@ namespace q8k {
 // Activation types (the values of Q8K_F32, Q8K_F16, Q8K_BF16).
 constexpr int DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2;
 
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.4426950408889634f;
+
 // A page holds 64 tokens.  For each page and key/value head the cache holds
 // one record of 128 D + 512 bytes, contiguous and a multiple of 64 bytes:
 //   keys    int8 [D/64][64 tokens][64]  planes of 64 of the head's D values

@@ -373,7 +373,7 @@ def run_logprobs(q, x, dtype, targets, n, stride=None, offset=0):
              top_ids=torch.full((T, n), -7, dtype=torch.int32, device="cuda"))
     need = q.qlogprobs_workspace_bytes(T, V, n)
     q.qlogprobs(q_dtype(q, dtype), view, stride, T, V, to_dev(targets), r["logprob"], r["entropy"], r["lse"], n,
-                r["top_ids"] if n else None, r["top_logprob"] if n else None, poisoned(need), need)
+                r["top_ids"] if n else None, r["top_logprob"] if n else None, poisoned(need) if need else None, need)
     return {k: host(v) for k, v in r.items()}
 
 
@@ -385,7 +385,8 @@ def check_logprobs(got, want, what=""):
 
 
 @pytest.mark.parametrize("V,n", [(1, 1), (2, 2), (5, 0), (31, 31), (33, 32), (255, 3), (256, 20), (1000, 32),
-                                 (8191, 5), (8192, 1), (8193, 32), (32000, 8), (70001, 20)])
+                                 (8191, 5), (8192, 1), (8193, 32), (32000, 8),
+                                 (32769, 1), (70001, 20), (131072, 0)])
 @pytest.mark.parametrize("dtype", sh.DTYPES)
 def test_logprobs(q, V, n, dtype):
     T = 3
@@ -407,7 +408,22 @@ def test_logprobs_many_rows(q):
     check_logprobs(run_logprobs(q, x, "bf16", targets, 4), sh.logprobs(x, targets, 4))
 
 
-@pytest.mark.parametrize("V", [40, 10007])
+def test_logprobs_long_rows_whole(q):
+    """More rows than are cut into parts: one workgroup goes through a row in
+    several rounds, here with the largest last, first and in the middle."""
+    T, V, n = 260, 66000, 20
+    g = np.random.default_rng(17)
+    x = g.standard_normal((T, V)).astype(np.float32)
+    x += np.linspace(-3, 3, V, dtype=np.float32) * g.integers(-1, 2, (T, 1))
+    x[5] = -np.inf
+    x[5, 40000:40007] = 1.0
+    x[6, 33000:] = -np.inf
+    x = round_to(x, "f16")
+    t = g.integers(0, V, T).astype(np.int32)
+    check_logprobs(run_logprobs(q, x, "f16", t, n), sh.logprobs(x, t, n))
+
+
+@pytest.mark.parametrize("V", [40, 10007, 80000])
 def test_logprobs_ties(q, V):
     """Equal logits everywhere, in stretches, and as +0 and -0: the lowest ids."""
     g = np.random.default_rng(1)

@@ -161,10 +161,14 @@ def test_logprobs_refusals(q):
     refused(q, "Q8K_ERR_ALIGN", lambda: lps(q, x=A16 + 2))
     refused(q, "Q8K_ERR_ALIGN", lambda: lps(q, dtype=2, x=A16 + 1))
     refused(q, "Q8K_ERR_ALIGN", lambda: lps(q, ent=A16 + 2))
-    need = q.qlogprobs_workspace_bytes(2, 100, 4)
-    assert need > 0
-    refused(q, "Q8K_ERR_WORKSPACE", lambda: lps(q, n=4, ids=A16, tl=A16, wsb=need - 1))
-    refused(q, "Q8K_ERR_NULL", lambda: lps(q, ws=None))
+    # few long rows are cut into parts, whose results meet in the workspace
+    assert q.qlogprobs_workspace_bytes(2, 32768, 4) == 0 and q.qlogprobs_workspace_bytes(300, 200000, 4) == 0
+    need = q.qlogprobs_workspace_bytes(2, 40000, 4)
+    assert 0 < need <= 2 * 16 * (12 + 4 * 8) + 256
+    big = dict(V=40000, stride=40000, n=4, ids=A16, tl=A16)
+    refused(q, "Q8K_ERR_WORKSPACE", lambda: lps(q, wsb=need - 1, **big))
+    refused(q, "Q8K_ERR_NULL", lambda: lps(q, ws=None, **big))
+    refused(q, "Q8K_ERR_ALIGN", lambda: lps(q, ws=A16 + 8, **big))
     lps(q, T=0)
     assert q.qlogprobs_workspace_bytes(0, 100, 4) == 0 and q.qlogprobs_workspace_bytes(1, 3, 4) == 0
 
