@@ -56,14 +56,23 @@ __device__ __forceinline__ void kv_item(const RopeView& r, int item, int& oa, in
     ob = half ? r.dim / 2 + 4 * item : 8 * item + 4;
 }
 
-__device__ __forceinline__ float4 load4f(const void* p, int64_t i, int dt) {
-    if (dt == DT_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+// Four values as they lie in memory, and what they stand for: apart, so that
+// many loads set out before the first is waited for.
+__device__ __forceinline__ uint4 load4raw(const void* p, int64_t i, bool f32) {
+    if (f32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
     const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    return make_uint4(w.x, w.y, 0, 0);
+}
+__device__ __forceinline__ float4 raw4f(uint4 w, int dt) {
+    if (dt == DT_F32) return __builtin_bit_cast(float4, w);
     if (dt == DT_BF16)
         return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                            __uint_as_float(w.y & 0xffff0000u));
     return make_float4(half_bits_to_float(w.x & 0xffffu), half_bits_to_float(w.x >> 16),
                        half_bits_to_float(w.y & 0xffffu), half_bits_to_float(w.y >> 16));
+}
+__device__ __forceinline__ float4 load4f(const void* p, int64_t i, int dt) {
+    return raw4f(load4raw(p, i, dt == DT_F32), dt);
 }
 
 // One rounding to the type, to nearest even.
@@ -135,21 +144,22 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
-// Codes of four values: q8_K's rule with the block's scale (q8k_quant.h),
-// round-half-even(x * (127/amax)) clamped to [-127, 127].
+// Codes of four values: q8_K's rule with the row's scale (q8k_quant.h),
+// round-half-even(x * (127/amax)) clamped to [-127, 127].  Adding 1.5 * 2^23
+// rounds a product to a whole number, half to even, and leaves it in the low
+// bits of the sum.  A finite 127/amax needs no clamp; where it overflows (amax
+// zero or nearly), nonzero values saturate and zeros stay zero.
 __device__ __forceinline__ uint32_t kv_codes4(float4 v, float iscale) {
 #pragma clang fp contract(off)
     const float x[4] = {v.x, v.y, v.z, v.w};
-    uint32_t w = 0;
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float r = __builtin_rintf(x[e] * iscale);
-        if (r != r) r = 0.0f;  // 0 * inf when 127/amax overflows
-        r = r > 127.0f ? 127.0f : r;
-        r = r < -127.0f ? -127.0f : r;
-        w |= (uint32_t)((int)r & 255) << (8 * e);
-    }
-    return w;
+    for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(uint32_t, x[e] * iscale + 12582912.0f);
+    if (!(iscale < INFINITY))
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = x[e] > 0.0f ? 127u : x[e] < 0.0f ? 129u : 0u;
+    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u), b = __builtin_amdgcn_perm(w[3], w[2], 0x0c0c0400u);
+    return a | b << 16;
 }
 
 }  // namespace q8k

@@ -55,6 +55,10 @@ APPEND = [
     (256, "f16", "half", 128, 4, 200),
     (64, "f32", "half", 0, 2, 129),
     (128, "f16", "half", 8, 1, 700),
+    # tokens by the tile
+    (64, "bf16", "adjacent", 64, 16, 521),
+    (256, "f32", "half", 128, 32, 257),
+    (128, "f16", "half", 128, 8, 1030),
 ]
 
 
@@ -76,6 +80,10 @@ def append_case(D, dtype, heads, T, seed, scattered=True):
 @pytest.mark.parametrize("scattered", [True, False])
 def test_append(q, D, dtype, pairs, rot, heads, T, scattered):
     g, row, pages, slots = append_case(D, dtype, heads, T, 11 + T, scattered)
+    if not scattered and T > 200:  # and runs with breaks, of every length and start
+        slots[100:] += 5
+        slots[150:] += 64
+        slots[170:180] = slots[170:180][::-1].copy()
     table = sh.rope_table(g, 300, rot) if rot else None
     pos = g.integers(0, 300, T).astype(np.int32)
     if T > 16 and rot:
@@ -91,7 +99,7 @@ def test_append(q, D, dtype, pairs, rot, heads, T, scattered):
 
 def test_append_one_by_one_and_at_once(q):
     """Appends touch no token but their own: any cutting into calls gives the same bytes."""
-    D, heads, T = 128, 4, 150
+    D, heads, T = 128, 16, 520
     g, row, pages, slots = append_case(D, "f32", heads, T, 5, scattered=False)
     table = sh.rope_table(g, T, D)
     pos = np.arange(T, dtype=np.int32)
@@ -107,11 +115,11 @@ def test_append_one_by_one_and_at_once(q):
 
     want = poisoned_cache(pages, heads, D)
     sh.append(want, row[:, heads: 2 * heads], row[:, 2 * heads:], table, pos, "half", slots, D)
-    for cuts in ([0, T], list(range(T + 1)), [0, 1, 70, 71, T]):
+    for cuts in ([0, T], list(range(T + 1)), [0, 1, 3, T]):
         assert_exact(run(cuts), want, f"cuts {cuts[:4]}")
 
 
-@pytest.mark.parametrize("D,heads,T", [(64, 1, 1), (128, 8, 70), (256, 3, 333), (64, 4, 1000)])
+@pytest.mark.parametrize("D,heads,T", [(64, 1, 1), (128, 8, 70), (256, 3, 333), (64, 4, 1000), (64, 16, 600), (256, 32, 259), (128, 9, 1000)])
 @pytest.mark.parametrize("dtype", sh.DTYPES)
 def test_read(q, D, heads, T, dtype):
     g = np.random.default_rng(T)
