@@ -65,20 +65,22 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppend a) {
         reinterpret_cast<float*>(rec + 2 * KV_PAGE * D)[(is_v ? KV_PAGE : 0) + token] = amax / 127.0f;
 }
 
-// Many tokens: one workgroup takes 64 tokens of one head.  Keys go as above.
+// Many tokens: one workgroup takes 32 tokens of one head.  Keys go as above.
 // The values' codes first meet in LDS.  Four tokens that follow each other from
 // a multiple of four on have places that follow each other, and a wave then
-// stores the four codes of 16 such groups to four rows of places at a time, 64
+// stores the four codes of eight such groups to four rows of places at a time, 32
 // consecutive bytes of each; the tokens that are left (a run's ends, or slots
-// in no order) go byte by byte.  (8191 tokens of 8 heads of 128, bf16: FIGURE)
-constexpr int TILE = 64;
+// in no order) go byte by byte.  8191 tokens of 8 heads of 128, bf16, take 18 us
+// for the simple form's 49; tiles of 64 tokens take as long there, and longer
+// where tokens are fewer.
+constexpr int TILE = 32, FOURS = TILE / 4;
 // Tokens of a tile (lane t: token t's slot, -1: none) that begin a group of
 // four, and those in none.
 struct Groups {
     uint64_t fours, singles;
 };
 __device__ __forceinline__ Groups groups_of(const int* slots, int lane) {
-    const int s = slots[lane];
+    const int s = lane < TILE ? slots[lane] : -1;
     bool four = s >= 0 && (s & 3) == 0 && lane + 3 < TILE;
     if (four) four = slots[lane + 1] == s + 1 && slots[lane + 2] == s + 2 && slots[lane + 3] == s + 3;
     Groups g;
@@ -89,7 +91,7 @@ __device__ __forceinline__ Groups groups_of(const int* slots, int lane) {
 // The token of the n-th group (n-th bit of the mask), -1 behind the last: lane
 // t's entry is written by it.
 __device__ __forceinline__ void list_groups(uint64_t fours, int lane, int* list) {
-    if (lane < TILE / 4 && lane >= __popcll(fours)) list[lane] = -1;
+    if (lane < FOURS && lane >= __popcll(fours)) list[lane] = -1;
     if (fours >> lane & 1) list[__popcll(fours & ((1ull << lane) - 1))] = lane;
 }
 // Rows of four bytes as columns: w[e] byte i becomes word i byte e.
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(256) void kv_append_tile_kernel(KvAppend a) {
     constexpr int N = TILE / ROWS;
     __shared__ uint32_t codes[TILE][D / 4 + 1];
     __shared__ float scales[TILE];
-    __shared__ int slots[TILE], fours[TILE / 4];
+    __shared__ int slots[TILE], fours[FOURS];
     const int h = (int)(blockIdx.x % a.heads);
     const int64_t t0 = (int64_t)(blockIdx.x / a.heads) * TILE;
     const int n = (int)(a.T - t0 < TILE ? a.T - t0 : TILE);
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(256) void kv_append_tile_kernel(KvAppend a) {
         }
     }
     __syncthreads();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slot = slots[lane];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, slot = lane < TILE ? slots[lane] : -1;
     const Groups g = groups_of(slots, lane);
     if (wave == 0) {
         list_groups(g.fours, lane, fours);
@@ -184,12 +186,12 @@ __global__ __launch_bounds__(256) void kv_append_tile_kernel(KvAppend a) {
                                      2 * KV_PAGE * D)[KV_PAGE + slot % KV_PAGE] = scales[lane];
     }
     __syncthreads();
-    const int first = fours[lane & 15];
+    const int first = fours[lane % FOURS];
     if (first >= 0) {
         const int s = slots[first];
         uint8_t* v = a.cache + ((int64_t)(s / KV_PAGE) * a.heads + h) * kv_record(D) + KV_PAGE * D + kv_place(s % KV_PAGE);
 #pragma unroll
-        for (int c = 4 * wave + (lane >> 4); c < D / 4; c += 16) {
+        for (int c = 64 / FOURS * wave + lane / FOURS; c < D / 4; c += 256 / FOURS) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = codes[first + e][c];
@@ -248,17 +250,17 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvRead a) {
     store4f(a.v, o + 4, a.dtype, v1);
 }
 
-// Many tokens, as kv_append_tile_kernel's: 64 tokens of one head.
+// Many tokens, as kv_append_tile_kernel's: 32 tokens of one head.
 template <int D>
 __global__ __launch_bounds__(256) void kv_read_tile_kernel(KvRead a) {
     constexpr int L = D / 8, ROWS = 256 / L;
     __shared__ uint32_t codes[TILE][D / 4 + 1];
-    __shared__ int slots[TILE], fours[TILE / 4];
+    __shared__ int slots[TILE], fours[FOURS];
     const int h = (int)(blockIdx.x % a.heads);
     const int64_t t0 = (int64_t)(blockIdx.x / a.heads) * TILE;
     const int n = (int)(a.T - t0 < TILE ? a.T - t0 : TILE);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (wave == 0) {
+    if (wave == 0 && lane < TILE) {
         const int s = lane < n ? a.slots[t0 + lane] : -1;
         slots[lane] = s >= a.pages * KV_PAGE ? -1 : s;
     }
@@ -266,13 +268,13 @@ __global__ __launch_bounds__(256) void kv_read_tile_kernel(KvRead a) {
     const Groups g = groups_of(slots, lane);
     if (wave == 0) list_groups(g.fours, lane, fours);
     __syncthreads();
-    const int first = fours[lane & 15];
+    const int first = fours[lane % FOURS];
     if (first >= 0) {
         const int s = slots[first];
         const uint8_t* v = a.cache + ((int64_t)(s / KV_PAGE) * a.heads + h) * kv_record(D) + KV_PAGE * D +
                            kv_place(s % KV_PAGE);
 #pragma unroll
-        for (int c = 4 * wave + (lane >> 4); c < D / 4; c += 16) {
+        for (int c = 64 / FOURS * wave + lane / FOURS; c < D / 4; c += 256 / FOURS) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t*>(v + (4 * c + e) * KV_PAGE);
@@ -318,9 +320,9 @@ __global__ __launch_bounds__(256) void kv_read_tile_kernel(KvRead a) {
     }
 }
 
-// Tokens times heads from which on the tiles take less time (1024 x 8: 16.6 us
-// with the read back, 18.3 the simple form; 512 x 8: 15.1 and 12.1).
-constexpr int64_t TILE_FROM_ROWS = 8192;
+// Tokens times heads from which on the tiles take less time (512 x 8: 10.8 us
+// with the read back, 12.1 the simple form; 256 x 8: 10.7 and 9.8).
+constexpr int64_t TILE_FROM_ROWS = 4096;
 
 template <int D>
 hipError_t append_d(const KvAppend& a, hipStream_t s) {
