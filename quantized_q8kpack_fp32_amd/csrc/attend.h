@@ -123,7 +123,7 @@ __device__ __forceinline__ Span span_of(const Attend& a, const Sequence& s, int 
 // whatever mix of lengths there is, and then for each sequence what cuts its
 // pages evenly.  Items are numbered sequence by
 // sequence; every workgroup finds its own by adding up the sequences before it,
-// 64 at a time.  target == 0: one item a tile, numbered without looking.
+// 64 at a time.  target == 0: one item a tile (there are enough of them).
 struct Item {
     int64_t b, first;  // sequence; its first item's number
     int c, splits;     // pages a chunk; chunks a tile
@@ -172,11 +172,22 @@ __device__ __forceinline__ int chunk_of(const Attend& a, const Load& l0) {
 }
 // Item `w` of a head; false: there is none of that number.
 __device__ __forceinline__ bool item_of(const Attend& a, int64_t w, Item& it) {
-    if (a.target == 0) {
-        it = Item{w / a.tiles_max, w - w % a.tiles_max, 1 << 30, 1, (int)(w % a.tiles_max), 0};
-        return it.b < a.B;
-    }
     const int lane = threadIdx.x & 63;
+    if (a.target == 0) {
+        // whole tiles: of the longest sequence first, and of its last tokens, which see the most
+        it = Item{w / a.tiles_max, 0, 1 << 30, 1, a.tiles_max - 1 - (int)(w % a.tiles_max), 0};
+        if (it.b >= a.B) return false;
+        if (a.B > 1 && a.B <= 64) {
+            const int mine = lane_load(a, 0).pages;
+            int rank = 0;
+            for (int j = 0; j < (int)a.B; ++j) {
+                const int other = __builtin_amdgcn_readlane(mine, j);
+                rank += other > mine || (other == mine && j < lane) ? 1 : 0;
+            }
+            it.b = __builtin_ctzll(__ballot(lane < (int)a.B && rank == (int)it.b));
+        }
+        return true;
+    }
     Load l = lane_load(a, 0);
     const int c = chunk_of(a, l);
     int64_t before = 0;

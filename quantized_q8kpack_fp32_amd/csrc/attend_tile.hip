@@ -17,6 +17,8 @@ struct PageOps {
     uint4 k[4][D / 32][64];  // [16 tokens][k step][lane]
     uint4 v[D / 16][2][64];  // [16 values][32 tokens][lane]
     float ks[KV_PAGE], vs[KV_PAGE];
+    float vmax;  // the largest of the vs that some row of the tile sees
+    float pad[3];
 };
 
 // One workgroup: 64 RT rows of one key head over its split's pages, 16 RT rows
@@ -35,8 +37,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int h = (int)(blockIdx.x % a.heads);
-    // the last rows of a prompt see the most: they start first
-    const int64_t item = a.items - 1 - blockIdx.x / a.heads;
+    const int64_t item = blockIdx.x / a.heads;
     Item it;
     if (!item_of(a, item, it)) return;
     const Sequence seq = item_sequence(a, it);
@@ -75,37 +76,51 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     }
 
     // A page's codes on their way: wave w brings pieces w, w + WAVES, ... of the
-    // keys (16 tokens of one plane each) and of the values (16 rows each).
+    // keys (16 tokens of one plane each) and of the values (16 rows each), wave
+    // 0 the keys' scales and wave 1 the values'.  Reads go through a buffer
+    // descriptor of one record, an empty one where the page selects nothing.
+    // Page numbers come 64 at a time, one a lane.
     const int32_t* pages = a.table + it.b * a.max_pages;
-    struct Raw {
-        uint4 k[KC], v[KC];
-        float sc;
-        bool ok;
-    } raw;
+    int ids = p0 + lane < p1 ? pages[p0 + lane] : -1;
+    const int lane_off = col * 64 + g * 16;
+    uint4 kraw[KC], vraw[KC];
+    float sc_raw;
+    int at_p = p0;  // the page that the registers hold
+    bool raw_ok;
     const auto fetch = [&](int p) {
-        const int page = __builtin_amdgcn_readfirstlane(p < p1 ? pages[p] : -1);
-        raw.ok = page >= 0 && page < a.pages;
-        if (!raw.ok) return;
-        const uint8_t* rec = a.cache + ((int64_t)page * a.heads + h) * kv_record(D);
+        const int n = p - p0;
+        if (n > 0 && (n & 63) == 0) ids = p + lane < p1 ? pages[p + lane] : -1;
+        const int page = __builtin_amdgcn_readlane(ids, n & 63);
+        at_p = p;
+        raw_ok = p < p1 && page >= 0 && page < a.pages;
+        const rsrc_t rec = make_rsrc(a.cache + ((int64_t)(raw_ok ? page : 0) * a.heads + h) * kv_record(D),
+                                     raw_ok ? kv_record(D) : 0);
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            raw.k[c] = *reinterpret_cast<const uint4*>(rec + (wave + WAVES * c) * 1024 + col * 64 + g * 16);
-            raw.v[c] = *reinterpret_cast<const uint4*>(rec + KV_PAGE * D + (wave + WAVES * c) * 1024 + col * 64 + g * 16);
+            kraw[c] = load16(rec, lane_off + (wave + WAVES * c) * 1024);
+            vraw[c] = load16(rec, lane_off + KV_PAGE * D + (wave + WAVES * c) * 1024);
         }
-        raw.sc = reinterpret_cast<const float*>(rec + 2 * KV_PAGE * D)[threadIdx.x & 127];
+        sc_raw = __builtin_bit_cast(float, load4(rec, 2 * KV_PAGE * D + 4 * (threadIdx.x & 127)));
     };
     const auto put = [&](PageOps<D>& o) {
-        if (!raw.ok) return;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
             // piece i of the keys: plane i / 4, tokens 16 (i % 4) and on
             const int i = wave + WAVES * c;
-            o.k[i & 3][2 * (i >> 2)][lane] = __builtin_bit_cast(uint4, codes_f16(raw.k[c].x, raw.k[c].y));
-            o.k[i & 3][2 * (i >> 2) + 1][lane] = __builtin_bit_cast(uint4, codes_f16(raw.k[c].z, raw.k[c].w));
-            o.v[i][0][lane] = __builtin_bit_cast(uint4, codes_f16(raw.v[c].x, raw.v[c].y));
-            o.v[i][1][lane] = __builtin_bit_cast(uint4, codes_f16(raw.v[c].z, raw.v[c].w));
+            o.k[i & 3][2 * (i >> 2)][lane] = __builtin_bit_cast(uint4, codes_f16(kraw[c].x, kraw[c].y));
+            o.k[i & 3][2 * (i >> 2) + 1][lane] = __builtin_bit_cast(uint4, codes_f16(kraw[c].z, kraw[c].w));
+            o.v[i][0][lane] = __builtin_bit_cast(uint4, codes_f16(vraw[c].x, vraw[c].y));
+            o.v[i][1][lane] = __builtin_bit_cast(uint4, codes_f16(vraw[c].z, vraw[c].w));
         }
-        if (threadIdx.x < 2 * KV_PAGE) o.ks[threadIdx.x] = raw.sc;  // vs follows ks
+        if (wave == 0) o.ks[lane] = sc_raw;
+        if (wave == 1) {
+            // what lies in places that no row sees may be anything, NaN scales included
+            const int j = at_p * KV_PAGE + lane;
+            const float v = j >= tile.lo.first && j <= tile.hi.last ? sc_raw : 0.0f;
+            o.vs[lane] = v;
+            const float most = wave_max(v);
+            if (lane == 0) o.vmax = most;
+        }
     };
 
     float m[RT], l[RT], R = pow2f(-100), Rinv = pow2f(100) * P_UP;
@@ -118,37 +133,40 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     }
     fetch(p0);
     put(ops[0]);
-    bool ok = raw.ok;
+    bool ok = raw_ok;
     fetch(p0 + 1);
     __syncthreads();
     for (int p = p0; p < p1; ++p) {
         const PageOps<D>& o = ops[(p - p0) & 1];
-        const bool next_ok = raw.ok;
+        const bool next_ok = raw_ok;
         put(ops[(p - p0 + 1) & 1]);
         fetch(p + 2);
         if (ok) {
+            // scores, the next 16 tokens' keys on their way while these are multiplied
             f4_t s4[RT][4];
+            h8_t kf[2][KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) kf[0][s] = __builtin_bit_cast(h8_t, o.k[0][s][lane]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+                if (q < 3)
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) kf[(q + 1) & 1][s] = __builtin_bit_cast(h8_t, o.k[q + 1][s][lane]);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) s4[rt][q] = f4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const h8_t k = __builtin_bit_cast(h8_t, o.k[q][s][lane]);
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
+                    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n)
-                            s4[rt][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qf[rt][n][s], s4[rt][q], 0, 0, 0);
-                }
+                        for (int rt = 0; rt < RT; ++rt)
+                            s4[rt][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q & 1][s], qf[rt][n][s], s4[rt][q], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            float vs[4][4];
-            float vmax = 0.0f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 k = *reinterpret_cast<const float4*>(&o.ks[16 * q + 4 * g]);
-                const float4 v = *reinterpret_cast<const float4*>(&o.vs[16 * q + 4 * g]);
-                vs[q][0] = v.x, vs[q][1] = v.y, vs[q][2] = v.z, vs[q][3] = v.w;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     s4[rt][q][0] *= k.x;
@@ -157,28 +175,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
                     s4[rt][q][3] *= k.w;
                 }
             }
-            // pages that some row sees only in part (what lies in unseen places
-            // may be anything, NaN scales included)
+            // pages that some row sees only in part
             if (p * KV_PAGE < tile.hi.first || p * KV_PAGE + KV_PAGE - 1 > tile.lo.last) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = p * KV_PAGE + 16 * q + 4 * g + i;
-                        bool any = false;
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            const bool seen = j >= span[rt].first && j <= span[rt].last;
-                            s4[rt][q][i] = seen ? s4[rt][q][i] : -INFINITY;
-                            any |= seen;
-                        }
-                        vs[q][i] = any ? vs[q][i] : 0.0f;
+                        for (int rt = 0; rt < RT; ++rt)
+                            s4[rt][q][i] = j >= span[rt].first && j <= span[rt].last ? s4[rt][q][i] : -INFINITY;
                     }
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vmax = fmaxf(vmax, vs[q][i]);
+            const float vmax = o.vmax;
             float tmax[RT];
             bool grew = vmax > R;
 #pragma unroll
@@ -192,8 +201,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
                 grew |= tmax[rt] > m[rt];
             }
             if (__any(grew)) {
-                float Rn = R;
-                if (__any(vmax > R)) Rn = fmaxf(R, pow2f(exponent_of(wave_max(vmax)) + 1));
+                const float Rn = vmax > R ? pow2f(exponent_of(vmax) + 1) : R;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     const float mn = fmaxf(m[rt], groups_max(tmax[rt]));
@@ -208,43 +216,61 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
                 R = Rn;
                 Rinv = P_UP / Rn;
             }
-            uint32_t pw[RT][NP][4][2];
+            // the first values on their way while the probabilities are made
+            constexpr int AHEAD = 2;
+            h8_t vf[AHEAD + 1][2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int d = 0; d < AHEAD; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) vs[q][i] *= Rinv;
+                for (int t = 0; t < 2; ++t) vf[d][t] = __builtin_bit_cast(h8_t, o.v[d][t][lane]);
+            h8_t pf[RT][NP][2];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const float mb = m[rt] == -INFINITY ? 0.0f : m[rt];
-                    float e[4];
+            for (int t = 0; t < 2; ++t) {
+                uint32_t w[RT][2][2][2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[rt][q][i], unit[rt], -mb));
-                        l[rt] += e[i];
-                        e[i] *= vs[q][i];
+                for (int b = 0; b < 2; ++b) {
+                    const int q = 2 * t + b;
+                    const float4 vq = *reinterpret_cast<const float4*>(&o.vs[16 * q + 4 * g]);
+                    const float v[4] = {vq.x * Rinv, vq.y * Rinv, vq.z * Rinv, vq.w * Rinv};
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float mb = m[rt] == -INFINITY ? 0.0f : m[rt];
+                        float e[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[rt][q][i], unit[rt], -mb));
+                            l[rt] += e[i];
+                            e[i] *= v[i];
+                        }
+                        f16_pieces<NP>(e[0], e[1], w[rt][b][0]);
+                        f16_pieces<NP>(e[2], e[3], w[rt][b][1]);
                     }
-                    uint32_t w0[2], w1[2];
-                    f16_pieces<NP>(e[0], e[1], w0);
-                    f16_pieces<NP>(e[2], e[3], w1);
-#pragma unroll
-                    for (int n = 0; n < NP; ++n) pw[rt][n][q][0] = w0[n], pw[rt][n][q][1] = w1[n];
                 }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+                        pf[rt][n][t] = __builtin_bit_cast(
+                            h8_t, make_uint4(w[rt][0][0][n], w[rt][0][1][n], w[rt][1][0][n], w[rt][1][1][n]));
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int d = 0; d < DB; ++d) {
+                if (d + AHEAD < DB)
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const h8_t v = __builtin_bit_cast(h8_t, o.v[d][t][lane]);
+                    for (int t = 0; t < 2; ++t)
+                        vf[(d + AHEAD) % (AHEAD + 1)][t] = __builtin_bit_cast(h8_t, o.v[d + AHEAD][t][lane]);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int n = 0; n < NP; ++n)
-                            acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                                v,
-                                __builtin_bit_cast(h8_t, make_uint4(pw[rt][n][2 * t][0], pw[rt][n][2 * t][1],
-                                                                    pw[rt][n][2 * t + 1][0], pw[rt][n][2 * t + 1][1])),
-                                acc[rt][d], 0, 0, 0);
-                }
+                    for (int n = 0; n < NP; ++n)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d % (AHEAD + 1)][t], pf[rt][n][t],
+                                                                                acc[rt][d], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         ok = next_ok;
         __syncthreads();
