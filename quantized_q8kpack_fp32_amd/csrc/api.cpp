@@ -564,7 +564,7 @@ size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t 
     if (!kv || !kv_dim(kv->head_dim) || kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS ||
         check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len) != Q8K_OK || B == 0 || max_q == 0)
         return 0;
-    return (size_t)attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim).ws_bytes;
+    return (size_t)attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, 0).ws_bytes;
 }
 
 int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
@@ -596,7 +596,7 @@ int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q
         return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
     if (B == 0 || max_q == 0) return Q8K_OK;
-    const AttendPlan p = attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim);
+    const AttendPlan p = attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, window);
     const int64_t group = q_heads / kv->kv_heads;
     Q8K_TRY(check_grid(fn, p.items * kv->kv_heads));
     a.q = q;

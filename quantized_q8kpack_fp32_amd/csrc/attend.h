@@ -271,7 +271,8 @@ __device__ __forceinline__ Tile item_tile(const Attend& a, const Sequence& s, in
 // comes in behind the products: score_unit.  A row whose position lies outside
 // the table is NaN.
 struct QueryItem {
-    float4 x, y, c, s;
+    uint4 x, y;  // as they lie in memory
+    float4 c, s;
     int oa, ob, p;
 };
 __device__ __forceinline__ int64_t q_token(const Attend& a, const Sequence& s, int row) { return s.q0 + row / a.group; }
@@ -281,8 +282,8 @@ __device__ __forceinline__ void fetch_q(const Attend& a, const Sequence& s, int 
     const int64_t base = t * a.q_stride + (int64_t)(h * a.group + row % a.group) * D;
     kv_item(a.rope, item, q.oa, q.ob);
     q.p = a.rope.table ? a.pos[t] : 0;
-    q.x = load4f(a.q, base + q.oa, a.dtype);
-    q.y = load4f(a.q, base + q.ob, a.dtype);
+    q.x = load4raw(a.q, base + q.oa, a.dtype == DT_F32);
+    q.y = load4raw(a.q, base + q.ob, a.dtype == DT_F32);
 }
 __device__ __forceinline__ void fetch_turn(const Attend& a, int item, QueryItem& q) {
     if (a.rope.table && 8 * item < a.rope.dim && q.p >= 0 && q.p < a.rope.len) {
@@ -291,17 +292,18 @@ __device__ __forceinline__ void fetch_turn(const Attend& a, int item, QueryItem&
         q.s = *reinterpret_cast<const float4*>(row + a.rope.dim / 2);
     }
 }
-__device__ __forceinline__ void put_q(const Attend& a, int item, QueryItem& q, float* dst) {
+__device__ __forceinline__ void put_q(const Attend& a, int item, const QueryItem& q, float* dst) {
+    float4 x = raw4f(q.x, a.dtype), y = raw4f(q.y, a.dtype);
     float f = a.scale > 0.0f ? 1.0f : a.scale < 0.0f ? -1.0f : 0.0f;
     if (a.rope.table) {
         if (q.p >= 0 && q.p < a.rope.len) {
-            if (8 * item < a.rope.dim) kv_turn(a.rope, q.c, q.s, q.x, q.y);
+            if (8 * item < a.rope.dim) kv_turn(a.rope, q.c, q.s, x, y);
         } else {
             f = __builtin_nanf("");
         }
     }
-    *reinterpret_cast<float4*>(dst + q.oa) = make_float4(q.x.x * f, q.x.y * f, q.x.z * f, q.x.w * f);
-    *reinterpret_cast<float4*>(dst + q.ob) = make_float4(q.y.x * f, q.y.y * f, q.y.z * f, q.y.w * f);
+    *reinterpret_cast<float4*>(dst + q.oa) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    *reinterpret_cast<float4*>(dst + q.ob) = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
 }
 
 // What a product of codes with a query that was multiplied by 2^e counts in

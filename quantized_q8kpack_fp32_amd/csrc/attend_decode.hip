@@ -376,7 +376,7 @@ constexpr int64_t TARGET_WGS = 512;
 constexpr int64_t TILE_FROM_ROWS = 33;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
 
-AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {
+AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
     AttendPlan p;
     const int64_t group = q_heads / heads;
     p.tiles = max_q * group >= TILE_FROM_ROWS;
@@ -384,7 +384,10 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
     p.tiles_max = (int)((max_q * group + p.tile_rows - 1) / p.tile_rows);
     p.least = p.tiles ? 8 : 4 * WAVES;
     const int64_t tiles = B * p.tiles_max, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
-    p.split = pages > p.least && B <= SPLIT_MAX_BATCH && tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
+    // what a tile reads at most; a window only ever makes a plan without a workspace of one with
+    const int64_t seen = (window + p.tile_rows / group + KV_PAGE) / KV_PAGE + 1;
+    const int64_t live = window > 0 && seen < pages ? seen : pages;
+    p.split = live > p.least + p.least / 2 && B <= SPLIT_MAX_BATCH && tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
     p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;
     p.items = tiles;
     if (p.split) {

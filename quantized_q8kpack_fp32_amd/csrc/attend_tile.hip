@@ -47,33 +47,39 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     const int p0 = uni(tile.p0 + it.split * it.c), p1 = uni(min(tile.p1, p0 + it.c));
     if (it.splits > 1 && p0 >= p1) return;  // the join reads only chunks that some row's span meets
 
-    // queries, 16 rows at a time through LDS
+    // The wave's queries: all on their way at once, then 16 rows at a time
+    // through its part of LDS into the registers that the products take.
     h8_t qf[RT][NQ][KS];
     float unit[RT];
     Span span[RT];
     {
+        constexpr int NI = D / 32;  // items of 16 rows a lane
         float(*qs)[D + 4] = sm.q[wave];
+        QueryItem qi[RT][NI];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                const int i = lane + 64 * n, row = tile.row0 + (wave * RT + rt) * 16 + i / (D / 8);
+                fetch_q<D>(a, seq, h, min(row, rows - 1), i % (D / 8), qi[rt][n]);
+            }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int n = 0; n < NI; ++n) fetch_turn(a, (lane + 64 * n) % (D / 8), qi[rt][n]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             const int row0 = tile.row0 + (wave * RT + rt) * 16;
-            for (int i = lane; i < 16 * (D / 8); i += 64) {
-                const int r = i / (D / 8), q = i % (D / 8);
-                if (row0 + r < rows) {
-                    QueryItem qi;
-                    fetch_q<D>(a, seq, h, row0 + r, q, qi);
-                    fetch_turn(a, q, qi);
-                    put_q(a, q, qi, qs[r]);
-                } else {
-                    *reinterpret_cast<float4*>(&qs[r][8 * q]) = make_float4(0, 0, 0, 0);
-                    *reinterpret_cast<float4*>(&qs[r][8 * q + 4]) = make_float4(0, 0, 0, 0);
-                }
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                const int i = lane + 64 * n;
+                put_q(a, i % (D / 8), qi[rt][n], qs[i / (D / 8)]);
             }
-            __syncthreads();
             unit[rt] = query_operand<D, NQ>(a, qs[col], g, qf[rt]);
             span[rt] = span_of(a, seq, min(row0 + col, rows - 1) / a.group);
-            __syncthreads();
         }
     }
+    __syncthreads();
 
     // A page's codes on their way: wave w brings pieces w, w + WAVES, ... of the
     // keys (16 tokens of one plane each) and of the values (16 rows each), wave
