@@ -555,6 +555,9 @@ static int check_attend_sizes(const char* fn, const q8k_kv_cache* kv, int64_t q_
     Q8K_TRY(check_count(fn, "B", B, MAX_BATCH));
     Q8K_TRY(check_count(fn, "Tq", Tq, MAX_TOKENS));
     Q8K_TRY(check_count(fn, "max_q", max_q, Tq));
+    if (max_q * (q_heads / kv->kv_heads) > ((int64_t)1 << 30))
+        return fail(Q8K_ERR_SHAPE, "%s: max_q=%lld new tokens of %lld query heads a key head are over 2^30 rows", fn,
+                    (long long)max_q, (long long)(q_heads / kv->kv_heads));
     return check_count(fn, "max_len", max_len, MAX_LEN);
 }
 

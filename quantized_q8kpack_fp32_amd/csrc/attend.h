@@ -75,6 +75,13 @@ __device__ __forceinline__ float groups_sum(float v) {
     return __builtin_bit_cast(float, t0) + __builtin_bit_cast(float, t1);
 }
 
+// Maximum over the wave, in every lane, without LDS.
+__device__ __forceinline__ float wave_max_dpp(float v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v = fmaxf(v, dpp_f(v, k));
+    return groups_max(v);
+}
+
 // A power of two as a float, |e| <= 126.
 __device__ __forceinline__ float pow2f(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
 
@@ -234,26 +241,26 @@ __device__ __forceinline__ Item items_of(const Attend& a, int64_t b) {
     return it;
 }
 
-// A tile's rows and pages.
-struct Tile {
-    int row0, rows;   // its first row; rows of the sequence and head
-    Span lo, hi;      // of its first and last row
-    int p0, p1;       // its pages
-};
-__device__ __forceinline__ Tile tile_of(const Attend& a, const Sequence& s, int tile) {
-    Tile t;
-    t.rows = s.nq * a.group;
-    t.row0 = tile * a.tile_rows;
-    const int last = min(t.rows, t.row0 + a.tile_rows) - 1;
-    t.lo = span_of(a, s, t.row0 / a.group);
-    t.hi = span_of(a, s, last / a.group);
-    t.p0 = t.lo.first / KV_PAGE;
-    t.p1 = t.hi.last >= 0 ? t.hi.last / KV_PAGE + 1 : 0;
-    return t;
-}
-
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A tile's rows and pages.
+struct Tile {
+    int row0, rows;    // its first row; rows of the sequence and head
+    int tok0, head0;   // the first row's token and query head (of the key head's)
+    Span lo, hi;       // of its first and last row
+    int p0, p1;        // its pages
+};
+// Row r of a tile: its token and query head.  The division by the group is of a
+// number below 2^13 (at most 4095 + 127): half added, the product with the
+// rounded reciprocal is off by less than the half is from the next whole number.
+struct TileRow {
+    int tok, head;
+};
+__device__ __forceinline__ TileRow row_of_tile(const Attend& a, const Tile& t, int r) {
+    const int x = t.head0 + r, q = (int)(((float)x + 0.5f) * a.inv_group);
+    return TileRow{t.tok0 + q, x - q * a.group};
+}
 // An item's sequence and tile, their numbers as scalars: the page loop's
 // addresses and branches then cost no vector instructions.
 __device__ __forceinline__ Sequence item_sequence(const Attend& a, const Item& it) {
@@ -261,8 +268,18 @@ __device__ __forceinline__ Sequence item_sequence(const Attend& a, const Item& i
     return Sequence{uni(s.q0), uni(s.n), uni(s.nq), uni(s.len)};
 }
 __device__ __forceinline__ Tile item_tile(const Attend& a, const Sequence& s, int tile) {
-    const Tile t = tile_of(a, s, tile);
-    return Tile{uni(t.row0), uni(t.rows), {uni(t.lo.first), uni(t.lo.last)}, {uni(t.hi.first), uni(t.hi.last)}, uni(t.p0), uni(t.p1)};
+    Tile t;
+    t.rows = uni(s.nq * a.group);
+    t.row0 = uni(tile * a.tile_rows);
+    t.tok0 = uni(t.row0 / a.group);
+    t.head0 = uni(t.row0 - t.tok0 * a.group);
+    const int last = min(t.rows, t.row0 + a.tile_rows) - 1;
+    const Span lo = span_of(a, s, t.tok0), hi = span_of(a, s, row_of_tile(a, t, max(last - t.row0, 0)).tok);
+    t.lo = Span{uni(lo.first), uni(lo.last)};
+    t.hi = Span{uni(hi.first), uni(hi.last)};
+    t.p0 = t.lo.first / KV_PAGE;
+    t.p1 = t.hi.last >= 0 ? t.hi.last / KV_PAGE + 1 : 0;
+    return t;
 }
 
 // ---- queries
@@ -275,11 +292,10 @@ struct QueryItem {
     float4 c, s;
     int oa, ob, p;
 };
-__device__ __forceinline__ int64_t q_token(const Attend& a, const Sequence& s, int row) { return s.q0 + row / a.group; }
 template <int D>
-__device__ __forceinline__ void fetch_q(const Attend& a, const Sequence& s, int h, int row, int item, QueryItem& q) {
-    const int64_t t = q_token(a, s, row);
-    const int64_t base = t * a.q_stride + (int64_t)(h * a.group + row % a.group) * D;
+__device__ __forceinline__ void fetch_q(const Attend& a, const Sequence& s, int h, TileRow r, int item, QueryItem& q) {
+    const int64_t t = s.q0 + r.tok;
+    const int64_t base = t * a.q_stride + (int64_t)(h * a.group + r.head) * D;
     kv_item(a.rope, item, q.oa, q.ob);
     q.p = a.rope.table ? a.pos[t] : 0;
     q.x = load4raw(a.q, base + q.oa, a.dtype == DT_F32);
@@ -341,8 +357,9 @@ __device__ __forceinline__ float query_operand(const Attend& a, const float* row
     return score_unit(a, qe);
 }
 
-__device__ __forceinline__ int64_t q_row_of(const Attend& a, const Sequence& s, int h, int row) {
-    return (int64_t)(s.q0 + row / a.group) * a.q_heads + h * a.group + row % a.group;
+// A row's place in the results.
+__device__ __forceinline__ int64_t q_row_of(const Attend& a, const Sequence& s, int h, TileRow r) {
+    return (int64_t)(s.q0 + r.tok) * a.q_heads + h * a.group + r.head;
 }
 
 }  // namespace q8k

@@ -53,8 +53,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     QueryItem qi[NI];
 #pragma unroll
     for (int n = 0; n < NI; ++n) {
-        const int i = threadIdx.x + 64 * WAVES * n, r = tile.row0 + i / (D / 8);
-        if (i < ROWS * (D / 8) && r < tile.rows) fetch_q<D>(a, seq, h, r, i % (D / 8), qi[n]);
+        const int i = threadIdx.x + 64 * WAVES * n, r = i / (D / 8);
+        if (i < ROWS * (D / 8) && tile.row0 + r < tile.rows)
+            fetch_q<D>(a, seq, h, row_of_tile(a, tile, r), i % (D / 8), qi[n]);
     }
     const int32_t* pages = a.table + it.b * a.max_pages;
     const int lane_off = col * 64 + g * 16;
@@ -106,7 +107,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     __syncthreads();
     h8_t qf[NQ][KS];
     const float unit = query_operand<D, NQ>(a, qs[col], g, qf);
-    const Span span = span_of(a, seq, min(tile.row0 + col, tile.rows - 1) / a.group);
+    const Span span = span_of(a, seq, row_of_tile(a, tile, min(col, tile.rows - 1 - tile.row0)).tok);
     float m = -INFINITY, l = 0.0f, R = pow2f(-100), Rinv = pow2f(100) * P_UP;
     f4_t acc[DB];
 #pragma unroll
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             const float mn = fmaxf(m, groups_max(tmax));
             float Rn = R;
             if (__any(vmax > R)) {
-                const float v = wave_max(vmax);
+                const float v = wave_max_dpp(vmax);
                 Rn = fmaxf(R, pow2f(exponent_of(v) + 1));
             }
             const float base = mn == -INFINITY ? 0.0f : mn;
@@ -250,7 +251,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             const float4 v = *reinterpret_cast<const float4*>(&acc_s[w][r][c]);
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
         }
-        const int64_t qr = q_row_of(a, seq, h, tile.row0 + r);
+        const int64_t qr = q_row_of(a, seq, h, row_of_tile(a, tile, r));
         if (it.splits > 1) {
             const int64_t at = (item * a.heads + h) * ROWS + r;
             *reinterpret_cast<float4*>(a.part + at * D + c) = o;
@@ -284,7 +285,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
     if (row >= seq.nq * a.group) return;
     const int ti = row / a.tile_rows, r = row % a.tile_rows;
     const Tile tile = item_tile(a, seq, ti);
-    const Span span = span_of(a, seq, row / a.group);
+    const TileRow tr = row_of_tile(a, tile, r);
+    const Span span = span_of(a, seq, tr.tok);
     const int s0 = uni((span.first / KV_PAGE - tile.p0) / it.c);
     const int s1 = uni(span.last >= 0 ? (span.last / KV_PAGE - tile.p0) / it.c + 1 : s0);
     const int64_t first = it.first + (int64_t)ti * it.splits, step = (int64_t)a.heads * a.tile_rows;
@@ -298,7 +300,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
         float2 ml = make_float2(-INFINITY, 0.0f);
         if (lane < count) ml = a.ml[at + lane * W * step];
         const float* part = a.part + at * D + N * lane;
-        const float mn = fmaxf(m, wave_max(ml.x)), base = mn == -INFINITY ? 0.0f : mn;
+        const float mn = fmaxf(m, wave_max_dpp(ml.x)), base = mn == -INFINITY ? 0.0f : mn;
         const float down = __builtin_amdgcn_exp2f(m - base), y = __builtin_amdgcn_exp2f(ml.x - base);
         l = l * down + wave_sum_dpp(ml.y * y);
 #pragma unroll
@@ -331,7 +333,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
             for (int n = 0; n < N; ++n) o[n] += o_s[i][N * lane + n] * y;
         }
     }
-    const int64_t qr = q_row_of(a, seq, h, row);
+    const int64_t qr = q_row_of(a, seq, h, tr);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l, base = m == -INFINITY ? 0.0f : m;
     const int64_t to = qr * D + N * lane;
 #pragma unroll
@@ -405,6 +407,7 @@ hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStre
     a.least = p.least;
     a.target = p.target;
     a.items = p.items;
+    a.inv_group = 1.0f / (float)a.group;
     a.part = static_cast<float*>(ws);
     if (p.split)
         a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(p.items * a.heads * p.tile_rows * D * 4));

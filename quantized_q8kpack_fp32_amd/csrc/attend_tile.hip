@@ -60,8 +60,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
-                const int i = lane + 64 * n, row = tile.row0 + (wave * RT + rt) * 16 + i / (D / 8);
-                fetch_q<D>(a, seq, h, min(row, rows - 1), i % (D / 8), qi[rt][n]);
+                const int i = lane + 64 * n, r = (wave * RT + rt) * 16 + i / (D / 8);
+                fetch_q<D>(a, seq, h, row_of_tile(a, tile, min(r, rows - 1 - tile.row0)), i % (D / 8), qi[rt][n]);
             }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -69,14 +69,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
             for (int n = 0; n < NI; ++n) fetch_turn(a, (lane + 64 * n) % (D / 8), qi[rt][n]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int row0 = tile.row0 + (wave * RT + rt) * 16;
 #pragma unroll
             for (int n = 0; n < NI; ++n) {
                 const int i = lane + 64 * n;
                 put_q(a, i % (D / 8), qi[rt][n], qs[i / (D / 8)]);
             }
             unit[rt] = query_operand<D, NQ>(a, qs[col], g, qf[rt]);
-            span[rt] = span_of(a, seq, min(row0 + col, rows - 1) / a.group);
+            span[rt] = span_of(a, seq, row_of_tile(a, tile, min((wave * RT + rt) * 16 + col, rows - 1 - tile.row0)).tok);
         }
     }
     __syncthreads();
@@ -124,7 +123,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
             const int j = at_p * KV_PAGE + lane;
             const float v = j >= tile.lo.first && j <= tile.hi.last ? sc_raw : 0.0f;
             o.vs[lane] = v;
-            const float most = wave_max(v);
+            const float most = wave_max_dpp(v);
             if (lane == 0) o.vmax = most;
         }
     };
@@ -284,10 +283,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int r = (wave * RT + rt) * 16 + col, row = tile.row0 + r;
+        const int r = (wave * RT + rt) * 16 + col;
         const float lr = groups_sum(l[rt]);
-        if (row >= rows) continue;
-        const int64_t qr = q_row_of(a, seq, h, row);
+        if (tile.row0 + r >= rows) continue;
+        const int64_t qr = q_row_of(a, seq, h, row_of_tile(a, tile, r));
         const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
         float f = R * P_DOWN;
         if (it.splits > 1) {

@@ -192,6 +192,7 @@ struct Attend {
     const void* q;  // [Tq] rows of q_heads * D values, q_stride elements apart
     int64_t q_stride;
     int q_heads, heads, group, dtype;
+    float inv_group;  // 1 / group
     const uint8_t* cache;
     int64_t pages;
     int64_t B;

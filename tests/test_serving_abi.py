@@ -97,6 +97,8 @@ def test_attend_refusals(q):
     refused(q, "Q8K_ERR_SHAPE", lambda: att(q, Tq=-1))
     refused(q, "Q8K_ERR_SHAPE", lambda: att(q, max_q=3))  # more than Tq
     refused(q, "Q8K_ERR_SHAPE", lambda: att(q, max_len=-1))
+    msg = refused(q, "Q8K_ERR_SHAPE", lambda: att(q, cache=kv(q, heads=1), heads=4096, qs=1 << 18, Tq=1 << 20, max_q=1 << 20))
+    assert "2^30" in msg
     assert "257" in refused(q, "Q8K_ERR_SHAPE", lambda: att(q, max_len=257))  # 4 pages hold 256
     refused(q, "Q8K_ERR_SHAPE", lambda: att(q, window=-1))
     refused(q, "Q8K_ERR_ARG", lambda: att(q, scale=float("inf")))
