@@ -376,13 +376,19 @@ hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
 // split, nor is one of more sequences than the workgroups care to look through.
 constexpr int64_t TARGET_WGS = 512;
 constexpr int64_t TILE_FROM_ROWS = 33;
+// Large tiles that leave compute units without one are halved.
+constexpr int64_t SMALL_TILES_BELOW = 256;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
 
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
     AttendPlan p;
     const int64_t group = q_heads / heads;
     p.tiles = max_q * group >= TILE_FROM_ROWS;
-    p.tile_rows = p.tiles ? ATTEND_TILE_ROWS : ROWS;
+    p.tile_rows = ROWS;
+    if (p.tiles) {
+        const int64_t large = (max_q * group + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS * B * heads;
+        p.tile_rows = large < SMALL_TILES_BELOW ? ATTEND_TILE_FEW : ATTEND_TILE_ROWS;
+    }
     p.tiles_max = (int)((max_q * group + p.tile_rows - 1) / p.tile_rows);
     p.least = p.tiles ? 8 : 4 * WAVES;
     const int64_t tiles = B * p.tiles_max, pages = (max_len + KV_PAGE - 1) / KV_PAGE;

@@ -307,19 +307,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     }
 }
 
-template <int D, int NQ, int NP>
-hipError_t tile_n(const Attend& a, hipStream_t s) {
-    // heads of 256 values: eight waves of 16 rows (four of 32 do not fit the register file)
-    constexpr int WAVES = D == 256 ? 8 : 4, RT = D == 256 ? 1 : 2;
-    static_assert(16 * WAVES * RT == ATTEND_TILE_ROWS, "rows of a tile");
-    Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, NQ, NP>), dim3((unsigned)(a.items * a.heads)),
-               dim3(64 * WAVES), 0, s, a);
+template <int D, int WAVES, int RT>
+hipError_t tile_w(const Attend& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.items * a.heads)), block(64 * WAVES);
+    if (a.dtype != DT_BF16)
+        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, 2, 2>), grid, block, 0, s, a);
+    else if (a.rope.table)
+        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, 2, 1>), grid, block, 0, s, a);
+    else
+        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, 1, 1>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 template <int D>
 hipError_t tile_d(const Attend& a, hipStream_t s) {
-    if (a.dtype != DT_BF16) return tile_n<D, 2, 2>(a, s);
-    return a.rope.table ? tile_n<D, 2, 1>(a, s) : tile_n<D, 1, 1>(a, s);
+    if (a.tile_rows == ATTEND_TILE_FEW) return tile_w<D, 4, 1>(a, s);
+    // heads of 256 values: eight waves of 16 rows (four of 32 do not fit the register file)
+    return tile_w<D, D == 256 ? 8 : 4, D == 256 ? 1 : 2>(a, s);
 }
 
 }  // namespace

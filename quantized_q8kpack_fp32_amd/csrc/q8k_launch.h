@@ -219,14 +219,14 @@ struct Attend {
     float2* ml;
 };
 struct AttendPlan {
-    bool tiles;  // the 128-row tile of prompts; else the 16-row kernel
+    bool tiles;  // the 128- or 64-row tile of prompts; else the 16-row kernel
     bool split;  // some sequence may be split
     int tile_rows, tiles_max, least, target;
     int64_t items, ws_bytes;
 };
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
                        int64_t window);
-constexpr int ATTEND_TILE_ROWS = 128;
+constexpr int ATTEND_TILE_ROWS = 128, ATTEND_TILE_FEW = 64;
 hipError_t launch_attend_tiles(int D, const Attend& a, hipStream_t s);  // attend_tile.hip
 hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s);
 

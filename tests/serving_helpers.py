@@ -181,32 +181,34 @@ def attend(q, cu_q, cache, table_of_pages, kv_len, scale, window, rope, pos, pai
         k = kc.astype(np.float64) * ks[..., None]
         v = vc.astype(np.float64) * vs[..., None]
         x = rotate(q[q0: q0 + n].astype(np.float64), rope, pos[q0: q0 + n] if pos is not None else None, pairs)
-        for i in range(n):
-            p = L - n + i
-            seen = good & (j <= p)
-            if window:
-                seen &= j > p - window
-            for a in range(Hq):
-                h = a // G
-                kk, vv = k[seen, h], v[seen, h]
-                r = q0 + i
-                if not seen.any():
-                    out[r, a], lse[r, a], bo[r, a], bl[r, a] = 0, -np.inf, 0, 0
-                    continue
-                s = kk @ x[i, a] * scale
-                S = (np.abs(kk) @ np.abs(x[i, a])).max() * abs(scale)
-                m = s.max()
-                w = np.exp(s - m)
-                z = w.sum()
-                out[r, a] = (w / z) @ vv
-                lse[r, a] = m + np.log(z)
-                ds = S * (2.0 ** -21 + (2 * D + 10) * 2.0 ** -24) + 2.0 ** -22
-                A = (w / z) @ np.abs(vv)
-                # the pieces' smallest step: 2^-40 of the largest share
-                floor = 2.0 ** -40 * seen.sum() * np.abs(vv).max()
-                bo[r, a] = A * (2 * ds + piece + (seen.sum() + 64) * 2.0 ** -24) + floor
-                bo[r, a] += np.abs(out[r, a]) * HALF_STEP[dtype] + (2.0 ** -25 if dtype == "f16" else 0)
-                bl[r, a] = ds + (seen.sum() + 16) * 2.0 ** -24 + abs(lse[r, a]) * 2.0 ** -22 + abs(m) * 2.0 ** -22
+        p = np.arange(L - n, L)[:, None]
+        seen = good & (j <= p)
+        if window:
+            seen &= j > p - window
+        some = seen.any(1)
+        count = seen.sum(1)[:, None]
+        for a in range(Hq):
+            h, rows = a // G, slice(q0, q0 + n)
+            # unseen places may hold anything: out of every sum and maximum
+            kk, vv = np.where(good[:, None], k[:, h], 0), np.where(good[:, None], v[:, h], 0)
+            s = np.where(seen, x[:, a] @ kk.T * scale, -np.inf)
+            S = np.where(seen, np.abs(x[:, a]) @ np.abs(kk).T, 0).max(1, initial=0)[:, None] * abs(scale)
+            m = np.where(some, s.max(1, initial=-np.inf), 0)[:, None]
+            w = np.exp(s - m)
+            z = w.sum(1, keepdims=True)
+            w = w / np.where(z == 0, 1, z)
+            out[rows, a] = w @ vv
+            with np.errstate(divide="ignore"):
+                lse[rows, a] = (m + np.log(z))[:, 0]
+            ds = S * (2.0 ** -21 + (2 * D + 10) * 2.0 ** -24) + 2.0 ** -22
+            A = w @ np.abs(vv)
+            # the pieces' smallest step: 2^-40 of the largest share
+            vmax = np.where(seen, np.abs(vv).max(1), 0).max(1, initial=0)[:, None]
+            bo[rows, a] = A * (2 * ds + piece + (count + 64) * 2.0 ** -24) + 2.0 ** -40 * count * vmax
+            bo[rows, a] += np.abs(out[rows, a]) * HALF_STEP[dtype] + (2.0 ** -25 if dtype == "f16" else 0)
+            fin = np.where(some, lse[rows, a], 0)[:, None]
+            bl[rows, a] = (ds + (count + 16) * 2.0 ** -24 + np.abs(fin) * 2.0 ** -22 + np.abs(m) * 2.0 ** -22)[:, 0]
+            bo[rows, a][~some] = 0
     return out, lse, bo, bl
 
 

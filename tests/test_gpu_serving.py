@@ -222,6 +222,21 @@ ATTEND = [
     (64, "f32", 4, 2, [1100, 900], [40, 33], 0, 0, "half"),
     (256, "bf16", 2, 1, [300], [300], 0, 0, "half"),
     (128, "f16", 6, 2, [400, 410, 1], [90, 100, 1], 130, 64, "half"),
+    (64, "bf16", 6, 2, [190], [60], 0, 64, "half"),
+    (64, "bf16", 6, 2, [190], [60], 33, 0, "half"),
+    (256, "bf16", 3, 1, [100, 50], [31, 50], 0, 128, "half"),
+    (128, "bf16", 3, 1, [100, 50], [31, 50], 0, 0, "half"),
+    # many heads: enough of the larger tiles
+    (64, "f32", 128, 128, [129, 140], [129, 70], 0, 64, "half"),
+    (64, "bf16", 128, 128, [150, 3], [140, 3], 0, 32, "adjacent"),
+    (64, "bf16", 128, 128, [150], [150], 0, 0, "half"),
+    (128, "f32", 128, 128, [200, 140], [129, 70], 50, 128, "half"),
+    (128, "bf16", 128, 128, [150, 3], [140, 3], 0, 32, "adjacent"),
+    (128, "bf16", 128, 128, [150], [150], 0, 0, "half"),
+    (256, "f16", 128, 128, [129, 140], [129, 70], 0, 256, "half"),
+    (256, "bf16", 128, 128, [150, 3], [140, 3], 70, 32, "adjacent"),
+    (256, "bf16", 128, 128, [150], [150], 0, 0, "half"),
+    (128, "f32", 256, 32, [90, 64, 5], [64, 64, 5], 0, 128, "half"),
 ]
 
 
