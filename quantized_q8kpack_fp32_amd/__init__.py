@@ -288,7 +288,14 @@ def _device() -> int:
 
 
 if torch.cuda.device_count() > 0:
-    _device = torch.cuda.current_device  # noqa: F811
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_of(dev, stream) -> int | None:
+    """_stream(stream), the current device being known."""
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 _TYPES = {Q8K_F32: torch.float32, Q8K_F16: torch.float16, Q8K_BF16: torch.bfloat16}
@@ -341,13 +348,13 @@ def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, r
     dev, t = _device(), _TYPES.get(dtype)
     _check(lib.q8k_kv_append(dtype, _on(dev, "k", k, t), k_stride, _on(dev, "v", v, t), v_stride, T,
                              _on(dev, "pos", pos, torch.int32), _rope(dev, rope),
-                             _on(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream(stream)))
+                             _on(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream_of(dev, stream)))
 
 
 def q8k_kv_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
     _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _on(dev, "slots", slots, torch.int32), T, _on(dev, "k", k, t),
-                           _on(dev, "v", v, t), _stream(stream)))
+                           _on(dev, "v", v, t), _stream_of(dev, stream)))
 
 
 def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
@@ -362,7 +369,7 @@ def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: in
     _check(lib.qattend(dtype, _on(dev, "q", q, t), q_stride, q_heads, _kv(dev, kv), B, _on(dev, "cu_q", cu_q, i32), Tq,
                        max_q, _on(dev, "page_table", page_table, i32), max_pages, _on(dev, "kv_len", kv_len, i32),
                        max_len, scale, window, _on(dev, "pos", pos, i32), _rope(dev, rope), _on(dev, "out", out, t),
-                       _on(dev, "lse", lse, torch.float32), _on(dev, "ws", ws), ws_bytes, _stream(stream)))
+                       _on(dev, "lse", lse, torch.float32), _on(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
 
 
 def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:
@@ -376,7 +383,7 @@ def qlogprobs(dtype: int, logits, stride: int, T: int, V: int, targets, logprob,
                          _on(dev, "targets", targets, torch.int32), _on(dev, "logprob", logprob, f32),
                          _on(dev, "entropy", entropy, f32), _on(dev, "lse", lse, f32), topn,
                          _on(dev, "top_ids", top_ids, torch.int32), _on(dev, "top_logprob", top_logprob, f32),
-                         _on(dev, "ws", ws), ws_bytes, _stream(stream)))
+                         _on(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
 
 
 def q8k_debug_subblock_sums(qtype: int, w, rows: int, K: int, xq, y, S, stream=None) -> None:
