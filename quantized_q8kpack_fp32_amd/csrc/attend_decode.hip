@@ -13,7 +13,6 @@ namespace q8k {
 
 namespace {
 
-constexpr int WAVES = 4;
 constexpr int ROWS = 16;
 
 // Probabilities enter the second product as fp16 pieces of p * vscale / R *
@@ -22,13 +21,15 @@ constexpr int ROWS = 16;
 // token is 2^-40 of the largest one's share.
 constexpr float P_UP = 32768.0f, P_DOWN = 1.0f / 32768.0f;
 
+// A product's steps go round four accumulators, so that no instruction waits
+// for the one before it (1024 tokens: 13.1 us, 14.0 one chain after the other).
 // One workgroup: 16 rows of one key head over `chunk` pages, wave w taking
-// pages w, w + 4, ...  S^T = K Q^T leaves a lane the scores of one row
+// pages w, w + WAVES, ...  S^T = K Q^T leaves a lane the scores of one row
 // (lane % 16) and 16 of a page's 64 tokens, in the layout that P^T has to have
 // as the second product's operand (kv_cache.h): nothing moves between lanes
 // but the running maximum, and that only where it grew.
 // NQ and NP: fp16 pieces of the queries and of the probabilities (f16_pieces).
-template <int D, int NQ, int NP>
+template <int D, int WAVES, int NQ, int NP>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_kernel(Attend a) {
     constexpr int KS = D / 32;  // k steps of the first product
     constexpr int DB = D / 16;  // row blocks of the second
@@ -122,17 +123,20 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             for (int q = 0; q < 4; ++q) s4[q] = f4_t{0, 0, 0, 0};
 #pragma unroll
             for (int s = 0; s < KS / 2; ++s) {
+                h8_t kf[4][2];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint4 c = kraw[q][s];
-                    const h8_t k0 = codes_f16(c.x, c.y), k1 = codes_f16(c.z, c.w);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[n][2 * s], s4[q], 0, 0, 0);
-                        s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[n][2 * s + 1], s4[q], 0, 0, 0);
-                    }
-                    if (q & 1) __builtin_amdgcn_sched_barrier(0);
+                    kf[q][0] = codes_f16(c.x, c.y);
+                    kf[q][1] = codes_f16(c.z, c.w);
                 }
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q][t], qf[n][2 * s + t], s4[q], 0, 0, 0);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -206,23 +210,30 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             for (int n = 0; n < NP; ++n) pw[n][q][0] = w0[n], pw[n][q][1] = w1[n];
         }
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-            const h8_t v0 = codes_f16(vraw[d].x, vraw[d].y), v1 = codes_f16(vraw[d].z, vraw[d].w);
+        for (int d0 = 0; d0 < DB; d0 += 4) {
+            h8_t vf[4][2];
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const h8_t q0 = __builtin_bit_cast(h8_t, make_uint4(pw[n][0][0], pw[n][0][1], pw[n][1][0], pw[n][1][1]));
-                const h8_t q1 = __builtin_bit_cast(h8_t, make_uint4(pw[n][2][0], pw[n][2][1], pw[n][3][0], pw[n][3][1]));
-                acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, q0, acc[d], 0, 0, 0);
-                acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, q1, acc[d], 0, 0, 0);
+            for (int d = 0; d < 4; ++d) {
+                vf[d][0] = codes_f16(vraw[d0 + d].x, vraw[d0 + d].y);
+                vf[d][1] = codes_f16(vraw[d0 + d].z, vraw[d0 + d].w);
             }
-            if (d & 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    const h8_t pf = __builtin_bit_cast(h8_t, make_uint4(pw[n][2 * t][0], pw[n][2 * t][1],
+                                                                        pw[n][2 * t + 1][0], pw[n][2 * t + 1][1]));
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        acc[d0 + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d][t], pf, acc[d0 + d], 0, 0, 0);
+                }
         }
         load_values(rec);
         __builtin_amdgcn_sched_barrier(0);
         ok = next_ok;
     }
 
-    // join the four waves
+    // join the waves
     l = groups_sum(l);
     if (g == 0) red[wave][col][0] = m, red[wave][col][1] = l;
     __syncthreads();
@@ -231,10 +242,11 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     for (int w = 1; w < WAVES; ++w) mt = fmaxf(mt, red[w][col][0]);
     const float base = mt == -INFINITY ? 0.0f : mt;
     const float f = __builtin_amdgcn_exp2f(m - base) * R * P_DOWN;
+    if (tile.row0 + col < tile.rows)
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
-        *reinterpret_cast<float4*>(&acc_s[wave][col][16 * d + 4 * g]) =
-            make_float4(acc[d][0] * f, acc[d][1] * f, acc[d][2] * f, acc[d][3] * f);
+        for (int d = 0; d < DB; ++d)
+            *reinterpret_cast<float4*>(&acc_s[wave][col][16 * d + 4 * g]) =
+                make_float4(acc[d][0] * f, acc[d][1] * f, acc[d][2] * f, acc[d][3] * f);
     __syncthreads();
     for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * WAVES) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
@@ -347,15 +359,22 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
     if (lane == 0 && a.lse) a.lse[qr] = l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-template <int D, int NQ, int NP>
+template <int D, int WAVES, int NQ, int NP>
 hipError_t decode_n(const Attend& a, hipStream_t s) {
-    Q8K_LAUNCH((attend_decode_kernel<D, NQ, NP>), dim3((unsigned)(a.items * a.heads)), dim3(64 * WAVES), 0, s, a);
+    Q8K_LAUNCH((attend_decode_kernel<D, WAVES, NQ, NP>), dim3((unsigned)(a.items * a.heads)), dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
+template <int D, int WAVES>
+hipError_t decode_w(const Attend& a, hipStream_t s) {
+    if (a.dtype != DT_BF16) return decode_n<D, WAVES, 2, 2>(a, s);
+    return a.rope.table ? decode_n<D, WAVES, 2, 1>(a, s) : decode_n<D, WAVES, 1, 1>(a, s);
+}
 template <int D>
-hipError_t decode_d(const Attend& a, hipStream_t s) {
-    if (a.dtype != DT_BF16) return decode_n<D, 2, 2>(a, s);
-    return a.rope.table ? decode_n<D, 2, 1>(a, s) : decode_n<D, 1, 1>(a, s);
+hipError_t decode_d(const Attend& a, int waves, hipStream_t s) {
+    // 256 values: eight waves' accumulators would not fit
+    if constexpr (D < 256)
+        if (waves == 8) return decode_w<D, 8>(a, s);
+    return decode_w<D, 4>(a, s);
 }
 template <int D>
 hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
@@ -378,6 +397,13 @@ constexpr int64_t TARGET_WGS = 512;
 constexpr int64_t TILE_FROM_ROWS = 33;
 // Large tiles that leave compute units without one are halved.
 constexpr int64_t SMALL_TILES_BELOW = 256;
+// Short sequences keep to one workgroup a tile: of eight waves up to
+// UNSPLIT_PAGES pages (2048 tokens of 64 sequences, 8 heads of 128: 42.6 us, in
+// four-wave chunks with a join 47.0; 3000 tokens of one: 23.8 against 19.3), but of
+// four where they have hardly a page each (513 tokens: 10.9 us, eight waves 11.5).
+// 12 sequences of 1000 tokens: 12.3 us, of four waves 13.7.  256 values (four
+// waves only) are cut from half more than a chunk on (2048 tokens: 27.8 us, 32.3 whole).
+constexpr int64_t UNSPLIT_PAGES = 32, EIGHT_WAVES_FROM_PAGES = 13;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
 
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
@@ -390,12 +416,15 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
         p.tile_rows = large < SMALL_TILES_BELOW ? ATTEND_TILE_FEW : ATTEND_TILE_ROWS;
     }
     p.tiles_max = (int)((max_q * group + p.tile_rows - 1) / p.tile_rows);
-    p.least = p.tiles ? 8 : 4 * WAVES;
+    p.least = p.tiles ? 8 : 16;
     const int64_t tiles = B * p.tiles_max, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
     // what a tile reads at most; a window only ever makes a plan without a workspace of one with
     const int64_t seen = (window + p.tile_rows / group + KV_PAGE) / KV_PAGE + 1;
     const int64_t live = window > 0 && seen < pages ? seen : pages;
-    p.split = live > p.least + p.least / 2 && B <= SPLIT_MAX_BATCH && tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
+    const bool eight = !p.tiles && D < 256;
+    p.split = live > (eight ? UNSPLIT_PAGES : p.least + p.least / 2) && B <= SPLIT_MAX_BATCH &&
+              tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
+    p.waves = eight && live >= EIGHT_WAVES_FROM_PAGES && live <= UNSPLIT_PAGES ? 8 : 4;
     p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;
     p.items = tiles;
     if (p.split) {
@@ -418,9 +447,9 @@ hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStre
     if (p.split)
         a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(p.items * a.heads * p.tile_rows * D * 4));
     const hipError_t e = p.tiles     ? launch_attend_tiles(D, a, s)
-                         : D == 64   ? decode_d<64>(a, s)
-                         : D == 128  ? decode_d<128>(a, s)
-                                     : decode_d<256>(a, s);
+                         : D == 64   ? decode_d<64>(a, p.waves, s)
+                         : D == 128  ? decode_d<128>(a, p.waves, s)
+                                     : decode_d<256>(a, p.waves, s);
     if (e != hipSuccess || !p.split) return e;
     return D == 64    ? join_d<64>(a, p.tiles, s)
            : D == 128 ? join_d<128>(a, p.tiles, s)

@@ -253,6 +253,25 @@ def test_attend(q, D, dtype, Hq, H, lens, news, window, rot, pairs):
     assert_within(gl, lse, bl, "lse")
 
 
+@pytest.mark.parametrize("D,dtype,rot", [(64, "f32", 64), (64, "bf16", 16), (64, "bf16", 0), (128, "f16", 128),
+                                         (128, "bf16", 128), (128, "bf16", 0), (256, "f32", 0)])
+@pytest.mark.parametrize("most", [13 * 64, 1025, 32 * 64, 32 * 64 + 1])
+def test_attend_middle_lengths(q, D, dtype, rot, most):
+    """Sequences of one workgroup a key head, of four waves or eight, and the
+    first length that is cut, among shorter ones."""
+    H, Hq = 2, 10
+    lens, news = [most, 0, 70, most - 300], [1, 0, 3, 2]
+    g, raw, table, cu = attend_case(D, H, lens, news, most + D)
+    qx = round_to(g.standard_normal((6, Hq, D)), dtype)
+    rt = sh.rope_table(g, 100, rot) if rot else None
+    pos = g.integers(0, 100, 6).astype(np.int32) if rot else None
+    for window in (0, 64 * 14):
+        want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, window, rt, pos, "half", D, dtype)
+        got, gl = run_attend(q, raw, table, cu, lens, qx, D, dtype, window, rt, pos, "half")
+        assert_within(got, want, bo, f"out {window}")
+        assert_within(gl, lse, bl, f"lse {window}")
+
+
 def test_attend_large_scores(q):
     """Scores in the hundreds, falling and rising along the sequence: the running
     maximum is what keeps the exponentials finite."""
