@@ -403,7 +403,11 @@ constexpr int64_t SMALL_TILES_BELOW = 256;
 // four where they have hardly a page each (513 tokens: 10.9 us, eight waves 11.5).
 // 12 sequences of 1000 tokens: 12.3 us, of four waves 13.7.  256 values (four
 // waves only) are cut from half more than a chunk on (2048 tokens: 27.8 us, 32.3 whole).
-constexpr int64_t UNSPLIT_PAGES = 32, EIGHT_WAVES_FROM_PAGES = 13;
+// Large tiles stay whole as long where there are WHOLE_TILES of them (300
+// tokens over 2000, 152 tiles: 49.2 us, in chunks 52.8; 1000 over 1000: 55.5 and
+// 76.3), and are cut from half more than a chunk on where there are fewer
+// (64 over 1500, 32 tiles: 30.0, whole 36.5).
+constexpr int64_t UNSPLIT_PAGES = 32, EIGHT_WAVES_FROM_PAGES = 13, WHOLE_TILES = 128;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
 
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
@@ -422,7 +426,7 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
     const int64_t seen = (window + p.tile_rows / group + KV_PAGE) / KV_PAGE + 1;
     const int64_t live = window > 0 && seen < pages ? seen : pages;
     const bool eight = !p.tiles && D < 256;
-    p.split = live > (eight ? UNSPLIT_PAGES : p.least + p.least / 2) && B <= SPLIT_MAX_BATCH &&
+    p.split = live > (eight || (p.tiles && tiles * heads >= WHOLE_TILES) ? UNSPLIT_PAGES : p.least + p.least / 2) && B <= SPLIT_MAX_BATCH &&
               tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
     p.waves = eight && live >= EIGHT_WAVES_FROM_PAGES && live <= UNSPLIT_PAGES ? 8 : 4;
     p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;

@@ -24,17 +24,27 @@ struct PageOps {
 // One workgroup: 64 RT rows of one key head over its split's pages, 16 RT rows
 // a wave.  While a page is multiplied, the next one's codes, in registers since
 // the page before, become fp16 in the other buffer, and the one after that is
-// on its way from memory: one barrier a page.
-template <int D, int WAVES, int RT, int NQ, int NP>
-__global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
+// on its way from memory: one barrier a page.  HALVES == 2: as many waves again
+// take every other page, with buffers of their own, and the two results are
+// joined through LDS: for calls of few short tiles, where a tile's own time
+// counts (512 tokens of one prompt, 32 heads of 128 over 8: 21.6 us, 24.3 with
+// one half; tiles that are split into chunks lose by it: 500 tokens over 16001
+// 283 us, 275).
+template <int D, int WAVES, int HALVES, int RT, int NQ, int NP>
+__global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Attend a) {
     constexpr int KS = D / 32, DB = D / 16, ROWS = 16 * RT * WAVES;
     constexpr int KC = D / 16 / WAVES;  // 1 KB pieces of a page's keys (and of its values) a wave brings
     __shared__ union {
-        PageOps<D> ops[2];
-        float q[WAVES][16][D + 4];  // the queries on their way to registers
+        PageOps<D> ops[HALVES][2];
+        float q[HALVES * WAVES][16][D + 4];  // the queries on their way to registers
+        struct {
+            float4 acc[RT][D / 16][64];
+            float2 ml[RT][64];
+        } join[WAVES];
     } sm;
-    PageOps<D>* ops = sm.ops;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = wave_of_all / WAVES, wave = wave_of_all % WAVES;
+    PageOps<D>* ops = sm.ops[half];
     const int col = lane & 15, g = lane >> 4;
     const int h = (int)(blockIdx.x % a.heads);
     const int64_t item = blockIdx.x / a.heads;
@@ -54,7 +64,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     Span span[RT];
     {
         constexpr int NI = D / 32;  // items of 16 rows a lane
-        float(*qs)[D + 4] = sm.q[wave];
+        float(*qs)[D + 4] = sm.q[wave_of_all];
         QueryItem qi[RT][NI];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -90,11 +100,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     const int lane_off = col * 64 + g * 16;
     uint4 kraw[KC], vraw[KC];
     float sc_raw;
-    int at_p = p0;  // the page that the registers hold
+    int at_p;  // the page that the registers hold
     bool raw_ok;
     const auto fetch = [&](int p) {
         const int n = p - p0;
-        if (n > 0 && (n & 63) == 0) ids = p + lane < p1 ? pages[p + lane] : -1;
+        // (tiles of two halves have at most 33 pages: attend_plan)
+        if (HALVES == 1 && n > 0 && (n & 63) == 0) ids = p + lane < p1 ? pages[p + lane] : -1;
         const int page = __builtin_amdgcn_readlane(ids, n & 63);
         at_p = p;
         raw_ok = p < p1 && page >= 0 && page < a.pages;
@@ -136,16 +147,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
 #pragma unroll
         for (int d = 0; d < DB; ++d) acc[rt][d] = f4_t{0, 0, 0, 0};
     }
-    fetch(p0);
+    fetch(p0 + half);
     put(ops[0]);
     bool ok = raw_ok;
-    fetch(p0 + 1);
+    fetch(p0 + half + HALVES);
     __syncthreads();
-    for (int p = p0; p < p1; ++p) {
-        const PageOps<D>& o = ops[(p - p0) & 1];
+    for (int p = p0 + half, turn = 0; p - half < p1; p += HALVES, turn ^= 1) {
+        const PageOps<D>& o = ops[turn];
         const bool next_ok = raw_ok;
-        put(ops[(p - p0 + 1) & 1]);
-        fetch(p + 2);
+        put(ops[turn ^ 1]);
+        fetch(p + 2 * HALVES);
         if (ok) {
             // scores, the next 16 tokens' keys on their way while these are multiplied
             f4_t s4[RT][4];
@@ -281,6 +292,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
         __syncthreads();
     }
 
+    if (HALVES == 2) {
+        auto& join = sm.join[wave];
+        if (half == 1) {
+            const float f = R * P_DOWN;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    join.acc[rt][d][lane] = make_float4(acc[rt][d][0] * f, acc[rt][d][1] * f, acc[rt][d][2] * f,
+                                                        acc[rt][d][3] * f);
+                join.ml[rt][lane] = make_float2(m[rt], l[rt]);
+            }
+        }
+        __syncthreads();
+        if (half == 1) return;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const float2 ml = join.ml[rt][lane];
+            const float mn = fmaxf(m[rt], ml.x), base = mn == -INFINITY ? 0.0f : mn;
+            const float f0 = __builtin_amdgcn_exp2f(m[rt] - base), f1 = __builtin_amdgcn_exp2f(ml.x - base);
+            l[rt] = l[rt] * f0 + ml.y * f1;
+            m[rt] = mn;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const float4 v = join.acc[rt][d][lane];
+                acc[rt][d] = acc[rt][d] * (f0 * R * P_DOWN) + f4_t{v.x, v.y, v.z, v.w} * f1;
+            }
+        }
+    }
+    const float unscale = HALVES == 2 ? 1.0f : R * P_DOWN;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int r = (wave * RT + rt) * 16 + col;
@@ -288,7 +329,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
         if (tile.row0 + r >= rows) continue;
         const int64_t qr = q_row_of(a, seq, h, row_of_tile(a, tile, r));
         const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
-        float f = R * P_DOWN;
+        float f = unscale;
         if (it.splits > 1) {
             const int64_t at = (item * a.heads + h) * ROWS + r;
 #pragma unroll
@@ -307,22 +348,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_tile_kernel(Attend a) {
     }
 }
 
-template <int D, int WAVES, int RT>
+template <int D, int WAVES, int HALVES, int RT>
 hipError_t tile_w(const Attend& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.items * a.heads)), block(64 * WAVES);
+    const dim3 grid((unsigned)(a.items * a.heads)), block(64 * WAVES * HALVES);
     if (a.dtype != DT_BF16)
-        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, 2, 2>), grid, block, 0, s, a);
+        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, HALVES, RT, 2, 2>), grid, block, 0, s, a);
     else if (a.rope.table)
-        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, 2, 1>), grid, block, 0, s, a);
+        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, HALVES, RT, 2, 1>), grid, block, 0, s, a);
     else
-        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, RT, 1, 1>), grid, block, 0, s, a);
+        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, HALVES, RT, 1, 1>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 template <int D>
 hipError_t tile_d(const Attend& a, hipStream_t s) {
-    if (a.tile_rows == ATTEND_TILE_FEW) return tile_w<D, 4, 1>(a, s);
+    if (a.tile_rows == ATTEND_TILE_FEW) {
+        // two pages at a time in tiles that are not split; 256 values' operands fill LDS
+        if constexpr (D < 256)
+            if (a.target == 0) return tile_w<D, 4, 2, 1>(a, s);
+        return tile_w<D, 4, 1, 1>(a, s);
+    }
     // heads of 256 values: eight waves of 16 rows (four of 32 do not fit the register file)
-    return tile_w<D, D == 256 ? 8 : 4, D == 256 ? 1 : 2>(a, s);
+    return tile_w<D, D == 256 ? 8 : 4, 1, D == 256 ? 1 : 2>(a, s);
 }
 
 }  // namespace

@@ -226,6 +226,20 @@ ATTEND = [
     (64, "bf16", 6, 2, [190], [60], 33, 0, "half"),
     (256, "bf16", 3, 1, [100, 50], [31, 50], 0, 128, "half"),
     (128, "bf16", 3, 1, [100, 50], [31, 50], 0, 0, "half"),
+    # few tiles of a long sequence
+    (64, "bf16", 8, 2, [1000, 800], [33, 12], 0, 64, "half"),
+    (64, "bf16", 8, 2, [1000, 800], [33, 12], 0, 0, "half"),
+    (64, "f16", 8, 2, [1000, 800], [33, 12], 700, 32, "half"),
+    (128, "f32", 8, 2, [1000, 800, 0], [33, 12, 0], 0, 128, "adjacent"),
+    (128, "bf16", 8, 2, [1000, 800], [33, 12], 900, 64, "half"),
+    (128, "bf16", 8, 2, [1000, 800], [33, 12], 0, 0, "half"),
+    (256, "f32", 4, 1, [1000], [33], 0, 256, "half"),
+    (256, "bf16", 4, 1, [1000], [33], 0, 64, "half"),
+    # whole ones of an odd and an even number of pages
+    (128, "f32", 16, 16, [450, 449, 65, 1], [40, 65, 65, 1], 0, 128, "half"),
+    (64, "bf16", 16, 16, [450, 449, 385], [40, 65, 65], 200, 0, "half"),
+    (128, "f32", 32, 16, [4200], [40], 4100, 128, "half"),
+    (128, "bf16", 64, 64, [2048, 300], [100, 90], 0, 128, "half"),
     # many heads: enough of the larger tiles
     (64, "f32", 128, 128, [129, 140], [129, 70], 0, 64, "half"),
     (64, "bf16", 128, 128, [150, 3], [140, 3], 0, 32, "adjacent"),
