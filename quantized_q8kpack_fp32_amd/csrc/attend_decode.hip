@@ -28,19 +28,24 @@ constexpr float P_UP = 32768.0f, P_DOWN = 1.0f / 32768.0f;
 // (lane % 16) and 16 of a page's 64 tokens, in the layout that P^T has to have
 // as the second product's operand (kv_cache.h): nothing moves between lanes
 // but the running maximum, and that only where it grew.
+// Of SLICES workgroups each makes its part of the row's values, the scores all of them.
 // NQ and NP: fp16 pieces of the queries and of the probabilities (f16_pieces).
-template <int D, int WAVES, int NQ, int NP>
+template <int D, int WAVES, int SLICES, int NQ, int NP>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_kernel(Attend a) {
     constexpr int KS = D / 32;  // k steps of the first product
-    constexpr int DB = D / 16;  // row blocks of the second
+    constexpr int DV = D / SLICES;  // values of the result
+    constexpr int DB = DV / 16;     // row blocks of the second product
+    constexpr int VB = DB < 4 ? DB : 4;  // of them, by turns
     __shared__ float qs[ROWS][D + 4];
     __shared__ float red[WAVES][ROWS][2];
-    __shared__ float acc_s[WAVES][ROWS][D + 4];
+    __shared__ float acc_s[WAVES][ROWS][DV + 4];
     __shared__ float scales[WAVES][2 * KV_PAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int h = (int)(blockIdx.x % a.heads);
-    const int64_t item = blockIdx.x / a.heads;
+    const int64_t item_slice = blockIdx.x / a.heads;
+    const int64_t item = SLICES == 1 ? item_slice : item_slice % a.items;
+    const int slice = SLICES == 1 ? 0 : (int)(item_slice / a.items);
     Item it;
     if (!item_of(a, item, it)) return;
     const Sequence seq = item_sequence(a, it);
@@ -84,7 +89,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     };
     const auto load_values = [&](rsrc_t rec) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d) vraw[d] = load16_nt(rec, lane_off + KV_PAGE * D + d * 1024);
+        for (int d = 0; d < DB; ++d) vraw[d] = load16_nt(rec, lane_off + KV_PAGE * D + (slice * DB + d) * 1024);
         vsc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D + 4 * KV_PAGE));
     };
     float* sc = scales[wave];
@@ -210,10 +215,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             for (int n = 0; n < NP; ++n) pw[n][q][0] = w0[n], pw[n][q][1] = w1[n];
         }
 #pragma unroll
-        for (int d0 = 0; d0 < DB; d0 += 4) {
-            h8_t vf[4][2];
+        for (int d0 = 0; d0 < DB; d0 += VB) {
+            h8_t vf[VB][2];
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
+            for (int d = 0; d < VB; ++d) {
                 vf[d][0] = codes_f16(vraw[d0 + d].x, vraw[d0 + d].y);
                 vf[d][1] = codes_f16(vraw[d0 + d].z, vraw[d0 + d].w);
             }
@@ -224,7 +229,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
                     const h8_t pf = __builtin_bit_cast(h8_t, make_uint4(pw[n][2 * t][0], pw[n][2 * t][1],
                                                                         pw[n][2 * t + 1][0], pw[n][2 * t + 1][1]));
 #pragma unroll
-                    for (int d = 0; d < 4; ++d)
+                    for (int d = 0; d < VB; ++d)
                         acc[d0 + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d][t], pf, acc[d0 + d], 0, 0, 0);
                 }
         }
@@ -248,8 +253,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             *reinterpret_cast<float4*>(&acc_s[wave][col][16 * d + 4 * g]) =
                 make_float4(acc[d][0] * f, acc[d][1] * f, acc[d][2] * f, acc[d][3] * f);
     __syncthreads();
-    for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * WAVES) {
-        const int r = i / (D / 4), c = 4 * (i % (D / 4));
+    for (int i = threadIdx.x; i < ROWS * (DV / 4); i += 64 * WAVES) {
+        const int r = i / (DV / 4), c = 4 * (i % (DV / 4));
         if (tile.row0 + r >= tile.rows) break;
         float mr = red[0][r][0];
 #pragma unroll
@@ -266,12 +271,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
         const int64_t qr = q_row_of(a, seq, h, row_of_tile(a, tile, r));
         if (it.splits > 1) {
             const int64_t at = (item * a.heads + h) * ROWS + r;
-            *reinterpret_cast<float4*>(a.part + at * D + c) = o;
-            if (c == 0) a.ml[at] = make_float2(mr, lr);
+            *reinterpret_cast<float4*>(a.part + at * D + slice * DV + c) = o;
+            if (c == 0 && slice == 0) a.ml[at] = make_float2(mr, lr);
         } else {
             const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
-            store4f(a.out, qr * D + c, a.dtype, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-            if (c == 0 && a.lse) a.lse[qr] = lr == 0.0f ? -INFINITY : (br + __builtin_amdgcn_logf(lr)) * LN2;
+            store4f(a.out, qr * D + slice * DV + c, a.dtype, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+            if (c == 0 && slice == 0 && a.lse) a.lse[qr] = lr == 0.0f ? -INFINITY : (br + __builtin_amdgcn_logf(lr)) * LN2;
         }
     }
 }
@@ -359,22 +364,26 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
     if (lane == 0 && a.lse) a.lse[qr] = l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-template <int D, int WAVES, int NQ, int NP>
+template <int D, int WAVES, int SLICES, int NQ, int NP>
 hipError_t decode_n(const Attend& a, hipStream_t s) {
-    Q8K_LAUNCH((attend_decode_kernel<D, WAVES, NQ, NP>), dim3((unsigned)(a.items * a.heads)), dim3(64 * WAVES), 0, s, a);
+    Q8K_LAUNCH((attend_decode_kernel<D, WAVES, SLICES, NQ, NP>), dim3((unsigned)(a.items * a.heads * SLICES)),
+               dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
-template <int D, int WAVES>
+template <int D, int WAVES, int SLICES>
 hipError_t decode_w(const Attend& a, hipStream_t s) {
-    if (a.dtype != DT_BF16) return decode_n<D, WAVES, 2, 2>(a, s);
-    return a.rope.table ? decode_n<D, WAVES, 2, 1>(a, s) : decode_n<D, WAVES, 1, 1>(a, s);
+    if (a.dtype != DT_BF16) return decode_n<D, WAVES, SLICES, 2, 2>(a, s);
+    return a.rope.table ? decode_n<D, WAVES, SLICES, 2, 1>(a, s) : decode_n<D, WAVES, SLICES, 1, 1>(a, s);
 }
 template <int D>
-hipError_t decode_d(const Attend& a, int waves, hipStream_t s) {
-    // 256 values: eight waves' accumulators would not fit
+hipError_t decode_d(const Attend& a, const AttendPlan& p, hipStream_t s) {
+    // eight waves' accumulators of 256 values would not fit; 64 values by four
+    // are one row block each
     if constexpr (D < 256)
-        if (waves == 8) return decode_w<D, 8>(a, s);
-    return decode_w<D, 4>(a, s);
+        if (p.waves == 8) return decode_w<D, 8, 1>(a, s);
+    if constexpr (D > 64)
+        if (p.slices == 4) return decode_w<D, 4, 4>(a, s);
+    return p.slices == 2 ? decode_w<D, 4, 2>(a, s) : decode_w<D, 4, 1>(a, s);
 }
 template <int D>
 hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
@@ -388,27 +397,42 @@ hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel and how many work items.  Items of a size for TARGET_WGS
-// workgroups, two a compute unit: more and smaller ones measured slower (each
-// has its queries to bring and its results to join), fewer leave units idle
-// where lengths differ.  A call that has several times as many tiles is not
-// split, nor is one of more sequences than the workgroups care to look through.
+// Which kernel and how many work items.  Times are of one key/value cache with
+// 8 key heads of 128 and 32 query heads unless it says otherwise.
+//
+// Chunks are of a size for TARGET_WGS workgroups, two a compute unit: more and
+// smaller ones measured slower (each has its queries to bring and its results
+// to join), fewer leave units idle where lengths differ.  A call that has
+// several times as many tiles is not split, nor is one of more sequences than
+// the workgroups care to look through.
 constexpr int64_t TARGET_WGS = 512;
-constexpr int64_t TILE_FROM_ROWS = 33;
-// Large tiles that leave compute units without one are halved.
-constexpr int64_t SMALL_TILES_BELOW = 256;
-// Short sequences keep to one workgroup a tile: of eight waves up to
-// UNSPLIT_PAGES pages (2048 tokens of 64 sequences, 8 heads of 128: 42.6 us, in
-// four-wave chunks with a join 47.0; 3000 tokens of one: 23.8 against 19.3), but of
-// four where they have hardly a page each (513 tokens: 10.9 us, eight waves 11.5).
-// 12 sequences of 1000 tokens: 12.3 us, of four waves 13.7.  256 values (four
-// waves only) are cut from half more than a chunk on (2048 tokens: 27.8 us, 32.3 whole).
-// Large tiles stay whole as long where there are WHOLE_TILES of them (300
-// tokens over 2000, 152 tiles: 49.2 us, in chunks 52.8; 1000 over 1000: 55.5 and
-// 76.3), and are cut from half more than a chunk on where there are fewer
-// (64 over 1500, 32 tiles: 30.0, whole 36.5).
-constexpr int64_t UNSPLIT_PAGES = 32, EIGHT_WAVES_FROM_PAGES = 13, WHOLE_TILES = 128;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
+// A chunk has at least this many pages (4096 tokens of one sequence: 15.6 us;
+// with 16 pages 17.2, with 4 15.3, but 16000 tokens then 22.6 and not 20.8).
+constexpr int LEAST_PAGES = 8;
+// The join costs a launch: up to UNSPLIT_PAGES pages (UNSPLIT_PAGES_256 of the
+// larger records) a tile is one workgroup's (16 x 1500 tokens: 16.3 us, in
+// chunks 19.4; 1 x 2000 15.3 and 14.6, 1 x 3000 19.7 and 15.2; 256 values,
+// 1 x 1000: 14.5 and 16.9, 1 x 2000: 21.1 and 17.6).  Large tiles stay whole as long
+// where there are WHOLE_TILES of them (300 tokens over 2000, 152 tiles: 49.2
+// us, in chunks 52.8; 1000 over 1000: 55.5 and 76.3), and are cut from half
+// more than a chunk on where there are fewer (64 over 1500, 32 tiles: 30.0,
+// whole 36.5).
+constexpr int64_t UNSPLIT_PAGES = 32, UNSPLIT_PAGES_256 = 24, WHOLE_TILES = 128;
+// A compute unit alone draws no more than some 50 GB/s of codes it has not met, so
+// few workgroups share a tile's values between them, each with all of the keys:
+// four up to 64 workgroups, two up to 128 (513 tokens: 9.4 us, by two 9.9, alone
+// 10.8; 256 values: 13.3, 15.1, 18.4; 16 x 2000 tokens by two 19.2, alone 22.2;
+// 32 x 2000 by two 29.5, alone 24.6).
+constexpr int64_t FOUR_SLICES_TO = 64, TWO_SLICES_TO = 128;
+// Where one workgroup a compute unit is all there is, it has eight waves if there are
+// pages for them (12 sequences of 1000 tokens, five tokens each: 12.3 us, of
+// four waves 13.6); where there are more, four (64 x 2000: 36 us, of eight 43).
+constexpr int64_t EIGHT_WAVES_TO = 256, EIGHT_WAVES_FROM_PAGES = 13;
+// Rows from which on the tiles of 64 and 128 rows take over, and the number of
+// the larger from which on they fill the compute units and are not halved.
+constexpr int64_t TILE_FROM_ROWS = 33;
+constexpr int64_t SMALL_TILES_BELOW = 256;
 
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
     AttendPlan p;
@@ -420,21 +444,24 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
         p.tile_rows = large < SMALL_TILES_BELOW ? ATTEND_TILE_FEW : ATTEND_TILE_ROWS;
     }
     p.tiles_max = (int)((max_q * group + p.tile_rows - 1) / p.tile_rows);
-    p.least = p.tiles ? 8 : 16;
+    p.least = LEAST_PAGES;
     const int64_t tiles = B * p.tiles_max, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
     // what a tile reads at most; a window only ever makes a plan without a workspace of one with
     const int64_t seen = (window + p.tile_rows / group + KV_PAGE) / KV_PAGE + 1;
     const int64_t live = window > 0 && seen < pages ? seen : pages;
-    const bool eight = !p.tiles && D < 256;
-    p.split = live > (eight || (p.tiles && tiles * heads >= WHOLE_TILES) ? UNSPLIT_PAGES : p.least + p.least / 2) && B <= SPLIT_MAX_BATCH &&
-              tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
-    p.waves = eight && live >= EIGHT_WAVES_FROM_PAGES && live <= UNSPLIT_PAGES ? 8 : 4;
+    const int64_t whole = p.tiles ? (tiles * heads >= WHOLE_TILES ? UNSPLIT_PAGES : LEAST_PAGES + LEAST_PAGES / 2)
+                          : D < 256 ? UNSPLIT_PAGES
+                                    : UNSPLIT_PAGES_256;
+    p.split = live > whole && B <= SPLIT_MAX_BATCH && tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
     p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;
     p.items = tiles;
     if (p.split) {
         const int64_t most = tiles * (1 + pages / p.least);
         p.items = tiles + p.target < most ? tiles + p.target : most;
     }
+    const int64_t wgs = p.items * heads;
+    p.slices = wgs <= FOUR_SLICES_TO && D > 64 ? 4 : wgs <= TWO_SLICES_TO ? 2 : 1;
+    p.waves = D < 256 && p.slices == 1 && wgs <= EIGHT_WAVES_TO && !p.split && live >= EIGHT_WAVES_FROM_PAGES ? 8 : 4;
     const int64_t rows = p.items * heads * p.tile_rows;
     p.ws_bytes = p.split ? align256(rows * D * 4) + rows * 8 : 0;
     return p;
@@ -451,9 +478,9 @@ hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStre
     if (p.split)
         a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(p.items * a.heads * p.tile_rows * D * 4));
     const hipError_t e = p.tiles     ? launch_attend_tiles(D, a, s)
-                         : D == 64   ? decode_d<64>(a, p.waves, s)
-                         : D == 128  ? decode_d<128>(a, p.waves, s)
-                                     : decode_d<256>(a, p.waves, s);
+                         : D == 64   ? decode_d<64>(a, p, s)
+                         : D == 128  ? decode_d<128>(a, p, s)
+                                     : decode_d<256>(a, p, s);
     if (e != hipSuccess || !p.split) return e;
     return D == 64    ? join_d<64>(a, p.tiles, s)
            : D == 128 ? join_d<128>(a, p.tiles, s)

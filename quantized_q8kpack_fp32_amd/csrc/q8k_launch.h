@@ -221,7 +221,8 @@ struct Attend {
 struct AttendPlan {
     bool tiles;  // the 128- or 64-row tile of prompts; else the 16-row kernel
     bool split;  // some sequence may be split
-    int tile_rows, tiles_max, least, target, waves;  // waves: of the 16-row kernel
+    int tile_rows, tiles_max, least, target;
+    int waves, slices;  // of the 16-row kernel
     int64_t items, ws_bytes;
 };
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,

@@ -286,6 +286,28 @@ def test_attend_middle_lengths(q, D, dtype, rot, most):
         assert_within(gl, lse, bl, f"lse {window}")
 
 
+@pytest.mark.parametrize("D,dtype,rot", [(64, "f32", 64), (64, "bf16", 16), (64, "bf16", 0), (128, "f16", 128),
+                                         (128, "bf16", 128), (128, "bf16", 0), (256, "f32", 64), (256, "bf16", 256),
+                                         (256, "bf16", 0)])
+@pytest.mark.parametrize("lens,H,max_len", [([70, 200], 2, 200), ([70, 200], 40, 200), ([70, 200], 66, 900),
+                                            ([70, 200], 150, 200), ([1200, 700], 2, 2200), ([1200, 700], 8, 2200),
+                                            ([1200, 700, 90, 1], 8, 2200)])
+def test_attend_more_and_fewer_heads(q, D, dtype, rot, lens, H, max_len):
+    """From a few workgroups, which share a tile's values, to several a compute
+    unit; whole and in chunks."""
+    news = ([1, 2] + [1] * len(lens))[: len(lens)]
+    g, raw, table, cu = attend_case(D, H, lens, news, H + D)
+    table = np.concatenate([table, np.full((len(lens), 35), -1, np.int32)], 1)
+    Tq = int(cu[-1])
+    qx = round_to(g.standard_normal((Tq, 3 * H, D)), dtype)
+    rt = sh.rope_table(g, 100, rot) if rot else None
+    pos = g.integers(0, 100, Tq).astype(np.int32) if rot else None
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, 0, rt, pos, "half", D, dtype)
+    got, gl = run_attend(q, raw, table, cu, lens, qx, D, dtype, 0, rt, pos, "half", max_len=max_len)
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
 def test_attend_large_scores(q):
     """Scores in the hundreds, falling and rising along the sequence: the running
     maximum is what keeps the exponentials finite."""
