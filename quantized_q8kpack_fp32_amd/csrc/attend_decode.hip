@@ -413,12 +413,9 @@ constexpr int LEAST_PAGES = 8;
 // The join costs a launch: up to UNSPLIT_PAGES pages (UNSPLIT_PAGES_256 of the
 // larger records) a tile is one workgroup's (16 x 1500 tokens: 16.3 us, in
 // chunks 19.4; 1 x 2000 15.3 and 14.6, 1 x 3000 19.7 and 15.2; 256 values,
-// 1 x 1000: 14.5 and 16.9, 1 x 2000: 21.1 and 17.6).  Large tiles stay whole as long
-// where there are WHOLE_TILES of them (300 tokens over 2000, 152 tiles: 49.2
-// us, in chunks 52.8; 1000 over 1000: 55.5 and 76.3), and are cut from half
-// more than a chunk on where there are fewer (64 over 1500, 32 tiles: 30.0,
-// whole 36.5).
-constexpr int64_t UNSPLIT_PAGES = 32, UNSPLIT_PAGES_256 = 24, WHOLE_TILES = 128;
+// 1 x 1000: 14.5 and 16.9, 1 x 2000: 21.1 and 17.6; tiles of 64 rows, 1000 new
+// tokens over 2000: 97 and 107).
+constexpr int64_t UNSPLIT_PAGES = 32, UNSPLIT_PAGES_256 = 24;
 // A compute unit alone draws no more than some 50 GB/s of codes it has not met, so
 // few workgroups share a tile's values between them, each with all of the keys:
 // four up to 64 workgroups, two up to 128 (513 tokens: 9.4 us, by two 9.9, alone
@@ -429,30 +426,41 @@ constexpr int64_t FOUR_SLICES_TO = 64, TWO_SLICES_TO = 128;
 // pages for them (12 sequences of 1000 tokens, five tokens each: 12.3 us, of
 // four waves 13.6); where there are more, four (64 x 2000: 36 us, of eight 43).
 constexpr int64_t EIGHT_WAVES_TO = 256, EIGHT_WAVES_FROM_PAGES = 13;
-// Rows from which on the tiles of 64 and 128 rows take over, and the number of
-// the larger from which on they fill the compute units and are not halved.
-constexpr int64_t TILE_FROM_ROWS = 33;
+// Rows of one key head by the sixteen, each 16 with the whole cache before
+// them, or by the 64 or 128 that share a page's conversion but leave compute
+// units without work where there are few of them.  Over what is not cut, up to
+// SIXTEENS tiles of 16 are the faster (64 new tokens over 1000, 128 tiles: 12.8
+// us, by 64 rows 29.2; 200 over 1000: 21.4 and 34.7; 256 over 256, 512 tiles: 11.8 and
+// 14.5; 384 over 384, 768: 21.3 and 18.0); over more, what pays is three of them
+// (16 sequences of 8191 tokens, nine new ones each: 68.5 us and 76.9, 16 new ones: 94
+// and 78), or a few of any over up to SIXTEENS_LONG_PAGES pages (32 over 4000,
+// 64 tiles: 24.3 and 31.7, over 16000 43.0 and 47.7, over 65000 127 and 106;
+// 100 over 4000, 200 tiles: 51 and 42).
+constexpr int64_t SIXTEENS = 512, SIXTEENS_LONG = 64, SIXTEENS_LONG_PAGES = 256;
+// 128 rows a tile where they fill the compute units, else 64.
 constexpr int64_t SMALL_TILES_BELOW = 256;
 
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
     AttendPlan p;
-    const int64_t group = q_heads / heads;
-    p.tiles = max_q * group >= TILE_FROM_ROWS;
+    const int64_t group = q_heads / heads, rows = max_q * group, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
+    // what a tile reads at most; a window only ever makes a plan without a workspace of one with
+    const auto live_of = [&](int64_t tile_rows) {
+        const int64_t seen = (window + tile_rows / group + KV_PAGE) / KV_PAGE + 1;
+        return window > 0 && seen < pages ? seen : pages;
+    };
+    const int64_t sixteens = (rows + ROWS - 1) / ROWS * B * heads, few = live_of(ROWS);
+    p.tiles = rows > 3 * ROWS && (few <= UNSPLIT_PAGES ? sixteens > SIXTEENS
+                                                       : sixteens > SIXTEENS_LONG || few > SIXTEENS_LONG_PAGES);
     p.tile_rows = ROWS;
     if (p.tiles) {
-        const int64_t large = (max_q * group + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS * B * heads;
+        const int64_t large = (rows + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS * B * heads;
         p.tile_rows = large < SMALL_TILES_BELOW ? ATTEND_TILE_FEW : ATTEND_TILE_ROWS;
     }
-    p.tiles_max = (int)((max_q * group + p.tile_rows - 1) / p.tile_rows);
+    p.tiles_max = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     p.least = LEAST_PAGES;
-    const int64_t tiles = B * p.tiles_max, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
-    // what a tile reads at most; a window only ever makes a plan without a workspace of one with
-    const int64_t seen = (window + p.tile_rows / group + KV_PAGE) / KV_PAGE + 1;
-    const int64_t live = window > 0 && seen < pages ? seen : pages;
-    const int64_t whole = p.tiles ? (tiles * heads >= WHOLE_TILES ? UNSPLIT_PAGES : LEAST_PAGES + LEAST_PAGES / 2)
-                          : D < 256 ? UNSPLIT_PAGES
-                                    : UNSPLIT_PAGES_256;
-    p.split = live > whole && B <= SPLIT_MAX_BATCH && tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
+    const int64_t tiles = B * p.tiles_max, live = live_of(p.tile_rows);
+    p.split = live > (D == 256 && !p.tiles ? UNSPLIT_PAGES_256 : UNSPLIT_PAGES) && B <= SPLIT_MAX_BATCH &&
+              tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
     p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;
     p.items = tiles;
     if (p.split) {
@@ -462,8 +470,8 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
     const int64_t wgs = p.items * heads;
     p.slices = wgs <= FOUR_SLICES_TO && D > 64 ? 4 : wgs <= TWO_SLICES_TO ? 2 : 1;
     p.waves = D < 256 && p.slices == 1 && wgs <= EIGHT_WAVES_TO && !p.split && live >= EIGHT_WAVES_FROM_PAGES ? 8 : 4;
-    const int64_t rows = p.items * heads * p.tile_rows;
-    p.ws_bytes = p.split ? align256(rows * D * 4) + rows * 8 : 0;
+    const int64_t parts = p.items * heads * p.tile_rows;
+    p.ws_bytes = p.split ? align256(parts * D * 4) + parts * 8 : 0;
     return p;
 }
 

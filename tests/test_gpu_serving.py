@@ -308,6 +308,41 @@ def test_attend_more_and_fewer_heads(q, D, dtype, rot, lens, H, max_len):
     assert_within(gl, lse, bl, "lse")
 
 
+@pytest.mark.parametrize("D,dtype,rot", [(64, "f32", 64), (64, "bf16", 16), (64, "bf16", 0), (128, "f16", 128),
+                                         (128, "bf16", 128), (128, "bf16", 0), (256, "f32", 64), (256, "bf16", 256),
+                                         (256, "bf16", 0)])
+@pytest.mark.parametrize("lens,news,H,max_len", [
+    ([200, 140], [150, 70], 32, 200),  # tiles of 64 rows, whole
+    ([65, 450, 1], [65, 135, 1], 32, 700),
+    ([900, 300], [65, 33], 16, 2200),  # in chunks
+    ([129, 140], [129, 70], 64, 140),  # of 128 rows
+])
+@pytest.mark.parametrize("window", [0, 100])
+def test_attend_prompt_tiles(q, D, dtype, rot, lens, news, H, max_len, window):
+    g, raw, table, cu = attend_case(D, H, lens, news, H + D)
+    table = np.concatenate([table, np.full((len(lens), 35), -1, np.int32)], 1)
+    Tq = int(cu[-1])
+    qx = round_to(g.standard_normal((Tq, H, D)), dtype)
+    rt = sh.rope_table(g, 100, rot) if rot else None
+    pos = g.integers(0, 100, Tq).astype(np.int32) if rot else None
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, window, rt, pos, "half", D, dtype)
+    got, gl = run_attend(q, raw, table, cu, lens, qx, D, dtype, window, rt, pos, "half", max_len=max_len)
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
+def test_attend_large_tiles_in_chunks(q):
+    D, H = 64, 128
+    lens, news = [800, 100], [100, 70]
+    g, raw, table, cu = attend_case(D, H, lens, news, 1)
+    table = np.concatenate([table, np.full((2, 35), -1, np.int32)], 1)
+    qx = round_to(g.standard_normal((170, H, D)), "f32")
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, 0, None, None, "half", D, "f32")
+    got, gl = run_attend(q, raw, table, cu, lens, qx, D, "f32", 0, None, None, "half", max_len=2200)
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
 def test_attend_large_scores(q):
     """Scores in the hundreds, falling and rising along the sequence: the running
     maximum is what keeps the exponentials finite."""
