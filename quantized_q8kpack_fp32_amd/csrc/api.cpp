@@ -456,7 +456,7 @@ constexpr int64_t MAX_PAGES = (int64_t)1 << 24;
 constexpr int64_t MAX_HEADS = (int64_t)1 << 12;
 constexpr int64_t MAX_LEN = (int64_t)1 << 30;
 constexpr int64_t MAX_BATCH = (int64_t)1 << 20;
-constexpr int64_t MAX_VOCAB = (int64_t)1 << 20;  // 128 chunks of a row's join
+constexpr int64_t MAX_VOCAB = (int64_t)1 << 20;  // a row's byte offsets stay in 32 bits
 
 static int check_dtype(const char* fn, int dtype) {
     if (dtype != Q8K_F32 && dtype != Q8K_F16 && dtype != Q8K_BF16)
