@@ -270,7 +270,7 @@ def qmatmul_prefill_moe_noalloc(qtype: int, w, E: int, rows: int, K: int, xq, T:
 
 
 # ---- the key/value cache, attention and log probabilities.  These check their
-# tensors' devices and index types, which the C side cannot see.
+# tensors' devices, types and strides, which the C side cannot see.
 def _on(dev, what, t, dtype=None):
     """Device pointer of a tensor argument on GPU ``dev`` (None -> NULL, an int passes through)."""
     if t.__class__ is int or t is None:
@@ -280,6 +280,13 @@ def _on(dev, what, t, dtype=None):
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
     return t.data_ptr()
+
+
+def _flat(dev, what, t, dtype=None):
+    """_on of a tensor whose strides the call is not told."""
+    if t.__class__ is not int and t is not None and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _on(dev, what, t, dtype)
 
 
 def _device() -> int:
@@ -347,14 +354,14 @@ def q8k_kv_bytes(pages: int, kv_heads: int, head_dim: int) -> int:
 def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
     _check(lib.q8k_kv_append(dtype, _on(dev, "k", k, t), k_stride, _on(dev, "v", v, t), v_stride, T,
-                             _on(dev, "pos", pos, torch.int32), _rope(dev, rope),
-                             _on(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream_of(dev, stream)))
+                             _flat(dev, "pos", pos, torch.int32), _rope(dev, rope),
+                             _flat(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream_of(dev, stream)))
 
 
 def q8k_kv_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
-    _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _on(dev, "slots", slots, torch.int32), T, _on(dev, "k", k, t),
-                           _on(dev, "v", v, t), _stream_of(dev, stream)))
+    _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _flat(dev, "slots", slots, torch.int32), T, _flat(dev, "k", k, t),
+                           _flat(dev, "v", v, t), _stream_of(dev, stream)))
 
 
 def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
@@ -366,10 +373,10 @@ def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: in
             ws_bytes: int = 0, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
     i32 = torch.int32
-    _check(lib.qattend(dtype, _on(dev, "q", q, t), q_stride, q_heads, _kv(dev, kv), B, _on(dev, "cu_q", cu_q, i32), Tq,
-                       max_q, _on(dev, "page_table", page_table, i32), max_pages, _on(dev, "kv_len", kv_len, i32),
-                       max_len, scale, window, _on(dev, "pos", pos, i32), _rope(dev, rope), _on(dev, "out", out, t),
-                       _on(dev, "lse", lse, torch.float32), _on(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
+    _check(lib.qattend(dtype, _on(dev, "q", q, t), q_stride, q_heads, _kv(dev, kv), B, _flat(dev, "cu_q", cu_q, i32), Tq,
+                       max_q, _flat(dev, "page_table", page_table, i32), max_pages, _flat(dev, "kv_len", kv_len, i32),
+                       max_len, scale, window, _flat(dev, "pos", pos, i32), _rope(dev, rope), _flat(dev, "out", out, t),
+                       _flat(dev, "lse", lse, torch.float32), _flat(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
 
 
 def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:
@@ -380,10 +387,10 @@ def qlogprobs(dtype: int, logits, stride: int, T: int, V: int, targets, logprob,
               top_ids=None, top_logprob=None, ws=None, ws_bytes: int = 0, stream=None) -> None:
     dev, f32 = _device(), torch.float32
     _check(lib.qlogprobs(dtype, _on(dev, "logits", logits, _TYPES.get(dtype)), stride, T, V,
-                         _on(dev, "targets", targets, torch.int32), _on(dev, "logprob", logprob, f32),
-                         _on(dev, "entropy", entropy, f32), _on(dev, "lse", lse, f32), topn,
-                         _on(dev, "top_ids", top_ids, torch.int32), _on(dev, "top_logprob", top_logprob, f32),
-                         _on(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
+                         _flat(dev, "targets", targets, torch.int32), _flat(dev, "logprob", logprob, f32),
+                         _flat(dev, "entropy", entropy, f32), _flat(dev, "lse", lse, f32), topn,
+                         _flat(dev, "top_ids", top_ids, torch.int32), _flat(dev, "top_logprob", top_logprob, f32),
+                         _flat(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
 
 
 def q8k_debug_subblock_sums(qtype: int, w, rows: int, K: int, xq, y, S, stream=None) -> None:

@@ -420,6 +420,37 @@ def test_attend_looser_maxima(q):
     assert_within(got[[0, 1, 3]], want[[0, 1, 3]], bo[[0, 1, 3]], "out, two tokens")
 
 
+@pytest.mark.parametrize("D,Hq,n,max_len", [(64, 2, 2, 300), (128, 64, 70, 300), (64, 2, 2, 9000), (128, 64, 70, 2500)])
+def test_attend_numbers_out_of_range(q, D, Hq, n, max_len):
+    """Bounds and lengths that lie outside what the call's sizes allow are cut to
+    it: rows before the first and behind the last, a negative length, one beyond
+    the page table."""
+    H = Hq // 2
+    g, raw, table, cu = attend_case(D, H, [1, 5, 300], [1, 0, n], 17)
+    table = np.concatenate([table, np.full((3, 150), -1, np.int32)], 1)
+    Tq = int(cu[-1])
+    qx = round_to(g.standard_normal((Tq, Hq, D)), "f32")
+    cut = [0, 5, max_len]
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, cut, D ** -0.5, 0, None, None, "half", D, "f32")
+    odd = np.array([-4, 1, 1, 2 ** 31 - 1], np.int32)
+    got, gl = run_attend(q, raw, table, odd, [-(2 ** 31), 5, 2 ** 31 - 1], qx, D, "f32", 0, None, None, "half",
+                         max_len=max_len, max_q=n, extra_rows=0)
+    assert np.isneginf(gl[0]).all()
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
+def test_tensors_elsewhere_are_refused(q):
+    import torch
+
+    kv = cache_of(q, poisoned_cache(2, 1, 64), 64)
+    x = torch.zeros(1, 1, 64, device="cuda")
+    with pytest.raises(ValueError):
+        q.q8k_kv_read(q.Q8K_F32, kv, torch.zeros(1, dtype=torch.int32), 1, x, x.clone())
+    with pytest.raises(ValueError):
+        q.q8k_kv_read(q.Q8K_F32, kv, torch.zeros(1, dtype=torch.int32, device="cuda"), 1, x, x.cpu())
+
+
 @pytest.mark.parametrize("B,D,H,Hq,window", [(70, 64, 1, 2, 0), (130, 128, 2, 2, 0), (257, 64, 1, 1, 0), (90, 64, 1, 4, 150)])
 def test_attend_many_sequences(q, B, D, H, Hq, window):
     """Mixed lengths of more sequences than a wave has lanes, few enough and too

@@ -186,3 +186,11 @@ def test_binding_checks_tensors(q):
         q.Rope(torch.zeros(4, 64), 5, 64)
     with pytest.raises(TypeError):
         app(q, slots=torch.zeros(1, dtype=torch.int64))
+    with pytest.raises(ValueError, match="slots must be contiguous"):
+        app(q, slots=torch.zeros(4, 2, dtype=torch.int32)[:, 0])
+    with pytest.raises(ValueError, match="page_table must be contiguous"):
+        att(q, table=torch.zeros(2, 8, dtype=torch.int32)[:, :4])
+    with pytest.raises(TypeError):
+        att(q, lse=torch.zeros(2, 4, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="top_ids must be contiguous"):
+        lps(q, n=2, ids=torch.zeros(2, 4, dtype=torch.int32)[:, :2], tl=A16)
