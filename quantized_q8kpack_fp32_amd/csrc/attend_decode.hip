@@ -433,33 +433,38 @@ constexpr int64_t FOUR_SLICES_TO = 64, TWO_SLICES_TO = 128;
 constexpr int64_t EIGHT_WAVES_TO = 256, EIGHT_WAVES_FROM_PAGES = 13;
 // Rows of one key head by the sixteen, each 16 with the whole cache before
 // them, or by the 64 or 128 that share a page's conversion but leave compute
-// units without work where there are few of them.  Over what is not cut, up to
-// SIXTEENS tiles of 16 are the faster (64 new tokens over 1000, 128 tiles: 12.8
-// us, by 64 rows 29.2; 200 over 1000: 21.4 and 34.7; 256 over 256, 512 tiles: 11.8 and
-// 14.5; 384 over 384, 768: 21.3 and 18.0); over more, what pays is three of them
-// (16 sequences of 8191 tokens, nine new ones each: 68.5 us and 76.9, 16 new ones: 94
-// and 78), or a few of any over up to SIXTEENS_LONG_PAGES pages (32 over 4000,
-// 64 tiles: 24.3 and 31.7, over 16000 43.0 and 47.7, over 65000 127 and 106;
-// 100 over 4000, 200 tiles: 51 and 42).
-constexpr int64_t SIXTEENS = 512, SIXTEENS_LONG = 64, SIXTEENS_LONG_PAGES = 256;
-// 128 rows a tile where they fill the compute units, else 64.
-constexpr int64_t SMALL_TILES_BELOW = 256;
+// units without work where there are few of them, and half a tile where the rows
+// are.  Up to SHORT_PAGES pages the sixteens are the faster for up to 48 rows and
+// up to SIXTEENS tiles (64 new tokens over 1000, 128 tiles: 12.8 us, by 64 rows
+// 29.2; 256 over 256, 512 tiles: 11.8 and 14.5; 384 over 384, 768: 21.3 and
+// 18.0; 64 sequences of 500 tokens, 12 new ones each: 40 and 41, 16: 55 and 42);
+// over more for up to 96 rows (16 sequences of 8191 tokens, nine new ones each: 67 us
+// and 115, 16: 94 and 115, 24: 123 and 122; 64 of 2000, 20 each: 98 and 111) and up to
+// SIXTEENS_PAGES pages of all tiles together (32 over 4000, 64 tiles: 24 and
+// 39, over 16000 43 and 49, over 65000 133 and 108; 64 over 8000, 128 tiles: 44 and
+// 46, over 16000 67 and 66).
+constexpr int64_t SHORT_PAGES = 16, SIXTEENS = 512, SIXTEENS_PAGES = 16384;
+// 128 rows a tile where they fill the compute units or are cut into enough chunks
+// to, else 64 (32 heads over 4, 250 new tokens, over 2500: 44 us, by 128 rows 51;
+// over 4000 56 and 55, over 16001 149 and 132; 1000 over 16001: 503 and 435, of
+// 256 values 1244 and 729).
+constexpr int64_t SMALL_TILES_BELOW = 256, SMALL_TILES_PAGES = 48;
 
-AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
+static AttendPlan plan_for(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
     AttendPlan p;
     const int64_t group = q_heads / heads, rows = max_q * group, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
-    // what a tile reads at most; a window only ever makes a plan without a workspace of one with
+    // what a tile reads at most
     const auto live_of = [&](int64_t tile_rows) {
         const int64_t seen = (window + tile_rows / group + KV_PAGE) / KV_PAGE + 1;
         return window > 0 && seen < pages ? seen : pages;
     };
     const int64_t sixteens = (rows + ROWS - 1) / ROWS * B * heads, few = live_of(ROWS);
-    p.tiles = rows > 3 * ROWS && (few <= UNSPLIT_PAGES ? sixteens > SIXTEENS
-                                                       : sixteens > SIXTEENS_LONG || few > SIXTEENS_LONG_PAGES);
+    p.tiles = few <= SHORT_PAGES ? rows > 3 * ROWS && sixteens > SIXTEENS
+                                 : rows > 6 * ROWS && sixteens * few > SIXTEENS_PAGES;
     p.tile_rows = ROWS;
     if (p.tiles) {
         const int64_t large = (rows + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS * B * heads;
-        p.tile_rows = large < SMALL_TILES_BELOW ? ATTEND_TILE_FEW : ATTEND_TILE_ROWS;
+        p.tile_rows = large < SMALL_TILES_BELOW && few <= SMALL_TILES_PAGES ? ATTEND_TILE_FEW : ATTEND_TILE_ROWS;
     }
     p.tiles_max = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     p.least = LEAST_PAGES;
@@ -481,6 +486,15 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
         p.ws_bytes = align256(parts * D * 4) + parts * 8;
     }
     return p;
+}
+
+// Callers size the workspace without a window: a plan that a window changes to
+// one of a larger workspace is not taken (either serves any window).
+AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
+    const AttendPlan all = plan_for(B, max_q, max_len, q_heads, heads, D, 0);
+    if (window == 0) return all;
+    const AttendPlan p = plan_for(B, max_q, max_len, q_heads, heads, D, window);
+    return p.ws_bytes > all.ws_bytes ? all : p;
 }
 
 hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s) {

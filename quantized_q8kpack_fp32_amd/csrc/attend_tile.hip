@@ -3,11 +3,13 @@
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
 // Three chunks of 1000 tokens over up to 16001 (32 heads of 128 over 4, bf16,
-// turned): 778 us, 593 TFLOP/s of the formula's, where a large matrix product
-// reaches 1140.  Matrix instructions are busy for 36% of the cycles and vector
-// ones for 43%, and little of the two overlaps: a query of two fp16 pieces makes
-// the first product twice as long as the formula's, and a score costs some
-// twelve vector instructions.  The rest is the last, unfilled round of tiles.
+// turned): 770 us, 600 TFLOP/s of the formula's, where a large matrix product
+// reaches 1140.  A query of two fp16 pieces makes the first product twice as long
+// as the formula's, so that the matrix work alone would take 607 us at that rate;
+// matrix instructions are busy for 36% of the cycles and vector ones (some twelve a
+// score) for 43%, and little of the two overlaps, neither from wave to wave nor
+// where the instructions are put between each other.  756 tiles on 512 places
+// leave the last round unfilled: equal lengths reach 720.
 #include "attend.h"
 
 namespace q8k {
@@ -238,16 +240,15 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
                 R = Rn;
                 Rinv = P_UP / Rn;
             }
-            // the first values on their way while the probabilities are made
+            // The second product by halves of the page's tokens (all probabilities
+            // first: 1.4% longer), its values two row blocks ahead.
             constexpr int AHEAD = 2;
-            h8_t vf[AHEAD + 1][2];
+            h8_t vf[AHEAD + 1];
 #pragma unroll
-            for (int d = 0; d < AHEAD; ++d)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) vf[d][t] = __builtin_bit_cast(h8_t, o.v[d][t][lane]);
-            h8_t pf[RT][NP][2];
+            for (int d = 0; d < AHEAD; ++d) vf[d] = __builtin_bit_cast(h8_t, o.v[d][0][lane]);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+                h8_t pf[RT][NP];
                 uint32_t w[RT][2][2][2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -272,26 +273,22 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
-                        pf[rt][n][t] = __builtin_bit_cast(
+                        pf[rt][n] = __builtin_bit_cast(
                             h8_t, make_uint4(w[rt][0][0][n], w[rt][0][1][n], w[rt][1][0][n], w[rt][1][1][n]));
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                if (d + AHEAD < DB)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        vf[(d + AHEAD) % (AHEAD + 1)][t] = __builtin_bit_cast(h8_t, o.v[d + AHEAD][t][lane]);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int d = 0; d < DB; ++d) {
+                    const int i = t * DB + d, k = i + AHEAD;
+                    if (k < 2 * DB) vf[k % (AHEAD + 1)] = __builtin_bit_cast(h8_t, o.v[k % DB][k / DB][lane]);
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
-                            acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d % (AHEAD + 1)][t], pf[rt][n][t],
+                            acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i % (AHEAD + 1)], pf[rt][n],
                                                                                 acc[rt][d], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         ok = next_ok;

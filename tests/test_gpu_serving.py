@@ -316,6 +316,8 @@ def test_attend_more_and_fewer_heads(q, D, dtype, rot, lens, H, max_len):
     ([65, 450, 1], [65, 135, 1], 32, 700),
     ([900, 300], [65, 33], 16, 2200),  # in chunks
     ([129, 140], [129, 70], 64, 140),  # of 128 rows
+    ([900, 300], [128, 100], 32, 2200),
+    ([900, 300], [128, 100], 32, 3200),
 ])
 @pytest.mark.parametrize("window", [0, 100])
 def test_attend_prompt_tiles(q, D, dtype, rot, lens, news, H, max_len, window):
@@ -327,6 +329,20 @@ def test_attend_prompt_tiles(q, D, dtype, rot, lens, news, H, max_len, window):
     pos = g.integers(0, 100, Tq).astype(np.int32) if rot else None
     want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, window, rt, pos, "half", D, dtype)
     got, gl = run_attend(q, raw, table, cu, lens, qx, D, dtype, window, rt, pos, "half", max_len=max_len)
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
+@pytest.mark.parametrize("D,H,G,n,L,window", [(256, 8, 2, 590, 1994, 1514), (256, 4, 8, 77, 1975, 1523), (128, 2, 4, 100, 9000, 700),
+                                              (64, 8, 8, 40, 5000, 2000)])
+def test_attend_window_and_the_workspace_without(q, D, H, G, n, L, window):
+    """A window that would have another kernel take the call, in chunks, does not
+    where the workspace, sized without it, has no room for them."""
+    lens, news = [L, 40], [n, 3]
+    g, raw, table, cu = attend_case(D, H, lens, news, L)
+    qx = round_to(g.standard_normal((n + 3, H * G, D)), "f32")
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, window, None, None, "half", D, "f32")
+    got, gl = run_attend(q, raw, table, cu, lens, qx, D, "f32", window, None, None, "half")
     assert_within(got, want, bo, "out")
     assert_within(gl, lse, bl, "lse")
 
