@@ -3,13 +3,13 @@
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
 // Three chunks of 1000 tokens over up to 16001 (32 heads of 128 over 4, bf16,
-// turned): 770 us, 600 TFLOP/s of the formula's, where a large matrix product
+// turned): 803 us, 574 TFLOP/s of the formula's, where a large matrix product
 // reaches 1140.  A query of two fp16 pieces makes the first product twice as long
 // as the formula's, so that the matrix work alone would take 607 us at that rate;
 // matrix instructions are busy for 36% of the cycles and vector ones (some twelve a
 // score) for 43%, and little of the two overlaps, neither from wave to wave nor
 // where the instructions are put between each other.  756 tiles on 512 places
-// leave the last round unfilled: equal lengths reach 720.
+// leave the last round unfilled: four of 1024 over 8192 reach 674.
 #include "attend.h"
 
 namespace q8k {
