@@ -92,6 +92,9 @@ __device__ __forceinline__ int exponent_of(float v) {
     return e < -100 ? -100 : e > 120 ? 120 : e;
 }
 
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // A sequence's new tokens and length, with what the device-side values say
 // cut to what the call's sizes allow, so that no access leaves its buffer.
 struct Sequence {
@@ -135,19 +138,21 @@ struct Item {
     int64_t b, first;  // sequence; its first item's number
     int c, splits;     // pages a chunk; chunks a tile
     int tile, split;
+    Sequence seq;
 };
 // A sequence's chunks: as many as come nearest to c pages each.
 __device__ __forceinline__ int splits_of(int pages, int c) { return max(1, (pages + c / 2) / c); }
 __device__ __forceinline__ int chunk_pages(int pages, int splits) { return splits == 1 ? 1 << 30 : (pages + splits - 1) / splits; }
 struct Load {
-    int tiles, pages;  // of one sequence: tiles, and pages a tile reads at most
+    Sequence seq;
+    int tiles, pages;  // tiles, and pages a tile reads at most
 };
 __device__ __forceinline__ Load load_of(const Attend& a, int64_t b) {
-    const Sequence s = sequence_of(a, b);
     Load l;
-    l.tiles = (s.nq * a.group + a.tile_rows - 1) / a.tile_rows;
-    int first = span_of(a, s, 0).first / KV_PAGE;
-    const int last = span_of(a, s, s.nq - 1).last;
+    l.seq = sequence_of(a, b);
+    l.tiles = (l.seq.nq * a.group + a.tile_rows - 1) / a.tile_rows;
+    const int first = span_of(a, l.seq, 0).first / KV_PAGE;
+    const int last = span_of(a, l.seq, l.seq.nq - 1).last;
     l.pages = last < 0 ? 0 : last / KV_PAGE + 1 - first;
     if (a.window > 0 && l.tiles > 1) {
         // a tile's rows see the window and its own tokens, from anywhere in a page
@@ -156,23 +161,35 @@ __device__ __forceinline__ Load load_of(const Attend& a, int64_t b) {
     }
     return l;
 }
-__device__ __forceinline__ int64_t wave_sum_int64(int64_t v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor((long long)v, off, WAVE);
+// Sum of the lanes up to this one, without LDS: rows of 16 lanes, then the
+// last lane of each row to the rows behind it.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
     return v;
 }
+__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
 // The sequence of this lane among 64 from b0 on.
 __device__ __forceinline__ Load lane_load(const Attend& a, int64_t b0) {
     const int64_t b = b0 + (threadIdx.x & 63);
-    return b < a.B ? load_of(a, b) : Load{0, 0};
+    return b < a.B ? load_of(a, b) : Load{Sequence{0, 0, 0, 0}, 0, 0};
+}
+__device__ __forceinline__ Sequence sequence_of_lane(const Sequence& s, int lane) {
+    return Sequence{__builtin_amdgcn_readlane(s.q0, lane), __builtin_amdgcn_readlane(s.n, lane),
+                    __builtin_amdgcn_readlane(s.nq, lane), __builtin_amdgcn_readlane(s.len, lane)};
 }
 
 // Pages a chunk (called by whole waves; l0: lane_load(a, 0)).
 __device__ __forceinline__ int chunk_of(const Attend& a, const Load& l0) {
-    int64_t total = wave_sum_int64((int64_t)l0.tiles * l0.pages);
-    for (int64_t b0 = 64; b0 < a.B; b0 += 64) {
-        const Load l = lane_load(a, b0);
-        total += wave_sum_int64((int64_t)l.tiles * l.pages);
+    int64_t total = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
+        const Load l = b0 == 0 ? l0 : lane_load(a, b0);
+        const int64_t n = (int64_t)l.tiles * l.pages;  // summed in two parts of 32 bits
+        total += ((int64_t)wave_total((int)(n >> 20)) << 20) + wave_total((int)(n & 0xfffff));
     }
     const int64_t c = (total + a.target - 1) / a.target;
     return (int)(c < a.least ? a.least : c);
@@ -181,17 +198,23 @@ __device__ __forceinline__ int chunk_of(const Attend& a, const Load& l0) {
 __device__ __forceinline__ bool item_of(const Attend& a, int64_t w, Item& it) {
     const int lane = threadIdx.x & 63;
     if (a.target == 0) {
-        // whole tiles: of the longest sequence first, and of its last tokens, which see the most
-        it = Item{w / a.tiles_max, 0, 1 << 30, 1, a.tiles_max - 1 - (int)(w % a.tiles_max), 0};
-        if (it.b >= a.B) return false;
-        if (a.B > 1 && a.B <= 64) {
-            const int mine = lane_load(a, 0).pages;
+        // whole tiles: of the longest sequence first (where the plan says so), and of
+        // its last tokens, which see the most
+        const int64_t b = w / a.tiles_max;
+        it = Item{b, 0, 1 << 30, 1, a.tiles_max - 1 - (int)(w % a.tiles_max), 0, {}};
+        if (b >= a.B) return false;
+        if (a.order) {
+            const Load l = lane_load(a, 0);
             int rank = 0;
             for (int j = 0; j < (int)a.B; ++j) {
-                const int other = __builtin_amdgcn_readlane(mine, j);
-                rank += other > mine || (other == mine && j < lane) ? 1 : 0;
+                const int other = __builtin_amdgcn_readlane(l.pages, j);
+                rank += other > l.pages || (other == l.pages && j < lane) ? 1 : 0;
             }
-            it.b = __builtin_ctzll(__ballot(lane < (int)a.B && rank == (int)it.b));
+            const int at = __builtin_ctzll(__ballot(lane < (int)a.B && rank == (int)b));
+            it.b = at;
+            it.seq = sequence_of_lane(l.seq, at);
+        } else {
+            it.seq = sequence_of_lane(sequence_of(a, b), 0);
         }
         return true;
     }
@@ -200,13 +223,7 @@ __device__ __forceinline__ bool item_of(const Attend& a, int64_t w, Item& it) {
     int64_t before = 0;
     for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
         if (b0 > 0) l = lane_load(a, b0);
-        const int splits = splits_of(l.pages, c), n = l.tiles * splits;
-        int upto = n;  // inclusive prefix sum
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int t = __shfl_up(upto, off, WAVE);
-            if (lane >= off) upto += t;
-        }
+        const int splits = splits_of(l.pages, c), n = l.tiles * splits, upto = wave_scan(n);
         const uint64_t hit = __ballot(w < before + upto);
         if (hit) {
             const int at = __builtin_ctzll(hit);
@@ -217,6 +234,7 @@ __device__ __forceinline__ bool item_of(const Attend& a, int64_t w, Item& it) {
             it.c = chunk_pages(__builtin_amdgcn_readlane(l.pages, at), it.splits);
             it.tile = rest / it.splits;
             it.split = rest % it.splits;
+            it.seq = sequence_of_lane(l.seq, at);
             return true;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
@@ -225,24 +243,24 @@ __device__ __forceinline__ bool item_of(const Attend& a, int64_t w, Item& it) {
 }
 // First item and chunking of sequence b.
 __device__ __forceinline__ Item items_of(const Attend& a, int64_t b) {
-    const int lane = threadIdx.x & 63;
     Load l = lane_load(a, 0);
-    Item it{b, 0, 0, 1, 0, 0};
+    Item it{b, 0, 0, 1, 0, 0, {}};
     const int c = chunk_of(a, l);
     for (int64_t b0 = 0; b0 <= b; b0 += 64) {
         if (b0 > 0) l = lane_load(a, b0);
-        const int splits = splits_of(l.pages, c);
-        it.first += wave_sum_int64(b0 + lane < b ? l.tiles * splits : 0);
+        const int splits = splits_of(l.pages, c), n = l.tiles * splits, upto = wave_scan(n);
         if (b < b0 + 64) {
-            it.splits = __builtin_amdgcn_readlane(splits, (int)(b - b0));
-            it.c = chunk_pages(__builtin_amdgcn_readlane(l.pages, (int)(b - b0)), it.splits);
+            const int at = uni((int)(b - b0));
+            it.first += __builtin_amdgcn_readlane(upto - n, at);
+            it.splits = __builtin_amdgcn_readlane(splits, at);
+            it.c = chunk_pages(__builtin_amdgcn_readlane(l.pages, at), it.splits);
+            it.seq = sequence_of_lane(l.seq, at);
+        } else {
+            it.first += __builtin_amdgcn_readlane(upto, 63);
         }
     }
     return it;
 }
-
-// A value that is the same in every lane, as a scalar.
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // A tile's rows and pages.
 struct Tile {
@@ -261,12 +279,8 @@ __device__ __forceinline__ TileRow row_of_tile(const Attend& a, const Tile& t, i
     const int x = t.head0 + r, q = (int)(((float)x + 0.5f) * a.inv_group);
     return TileRow{t.tok0 + q, x - q * a.group};
 }
-// An item's sequence and tile, their numbers as scalars: the page loop's
-// addresses and branches then cost no vector instructions.
-__device__ __forceinline__ Sequence item_sequence(const Attend& a, const Item& it) {
-    const Sequence s = sequence_of(a, it.b);
-    return Sequence{uni(s.q0), uni(s.n), uni(s.nq), uni(s.len)};
-}
+// An item's tile, its numbers as scalars (as its sequence's are): the page
+// loop's addresses and branches then cost no vector instructions.
 __device__ __forceinline__ Tile item_tile(const Attend& a, const Sequence& s, int tile) {
     Tile t;
     t.rows = uni(s.nq * a.group);

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
     const int64_t item = blockIdx.x / a.heads;
     Item it;
     if (!item_of(a, item, it)) return;
-    const Sequence seq = item_sequence(a, it);
+    const Sequence seq = it.seq;
     const Tile tile = item_tile(a, seq, it.tile);
     const int rows = tile.rows;
     if (tile.row0 >= rows) return;

@@ -214,6 +214,7 @@ struct Attend {
     // one of several of their rows go to the workspace, [item][tile_rows][D] and
     // (maximum, sum) pairs [item][tile_rows], and are joined.
     int tile_rows, tiles_max, least, target;
+    int order;      // whole tiles: the longest sequence's first (B <= 64)
     int64_t items;  // work items a head, at most
     float* part;
     float2* ml;
@@ -221,6 +222,7 @@ struct Attend {
 struct AttendPlan {
     bool tiles;  // the 128- or 64-row tile of prompts; else the 16-row kernel
     bool split;  // some sequence may be split
+    bool order;  // else: the longest sequence's tiles first
     int tile_rows, tiles_max, least, target;
     int waves, slices;  // of the 16-row kernel
     int64_t items, ws_bytes;
