@@ -275,18 +275,26 @@ def _on(dev, what, t, dtype=None):
     """Device pointer of a tensor argument on GPU ``dev`` (None -> NULL, an int passes through)."""
     if t.__class__ is int or t is None:
         return t
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{what} is {t.dtype}, {dtype} is taken")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
+    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
+        _refuse(dev, what, t, dtype)
     return t.data_ptr()
 
 
 def _flat(dev, what, t, dtype=None):
     """_on of a tensor whose strides the call is not told."""
-    if t.__class__ is not int and t is not None and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return _on(dev, what, t, dtype)
+    if t.__class__ is int or t is None:
+        return t
+    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
+        _refuse(dev, what, t, dtype)
+    return t.data_ptr()
+
+
+def _refuse(dev, what, t, dtype):
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what} is {t.dtype}, {dtype} is taken")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _device() -> int:

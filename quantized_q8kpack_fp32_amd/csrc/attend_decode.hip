@@ -8,8 +8,8 @@
 // in one pass with a running maximum m.  It is bound by the cache's bytes
 // (2 D + 8 a token and head), which go from memory to the registers that the
 // matrix instructions read: 8 x 65537 tokens of 8 heads of 128 in 171 us, 6.4
-// TB/s (a streaming read of as many bytes reaches 6.7), 16 of up to 8191 in 38.5,
-// 4.3 TB/s, 5 us of it the join.  Short sequences are bound by the chain of loads
+// TB/s (a streaming read of as many bytes reaches 6.7), 16 of up to 8191 in 37.7,
+// 4.4 TB/s, 5 us of it the join.  Short sequences are bound by the chain of loads
 // before the first product and by what one compute unit draws: 513 tokens 8.7 us.
 #include "attend.h"
 

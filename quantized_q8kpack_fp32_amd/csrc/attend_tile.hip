@@ -3,7 +3,7 @@
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
 // Three chunks of 1000 tokens over up to 16001 (32 heads of 128 over 4, bf16,
-// turned): 803 us, 574 TFLOP/s of the formula's, where a large matrix product
+// turned): 790 us, 584 TFLOP/s of the formula's, where a large matrix product
 // reaches 1140.  A query of two fp16 pieces makes the first product twice as long
 // as the formula's, so that the matrix work alone would take 607 us at that rate;
 // matrix instructions are busy for 36% of the cycles and vector ones (some twelve a
