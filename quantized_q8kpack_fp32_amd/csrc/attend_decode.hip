@@ -460,7 +460,7 @@ static AttendPlan plan_for(int64_t B, int64_t max_q, int64_t max_len, int q_head
     };
     const int64_t sixteens = (rows + ROWS - 1) / ROWS * B * heads, few = live_of(ROWS);
     p.tiles = few <= SHORT_PAGES ? rows > 3 * ROWS && sixteens > SIXTEENS
-                                 : rows > 6 * ROWS && sixteens * few > SIXTEENS_PAGES;
+                                 : rows > 6 * ROWS && sixteens > SIXTEENS_PAGES / few;
     p.tile_rows = ROWS;
     if (p.tiles) {
         const int64_t large = (rows + ATTEND_TILE_ROWS - 1) / ATTEND_TILE_ROWS * B * heads;

@@ -485,6 +485,25 @@ def test_attend_many_sequences(q, B, D, H, Hq, window):
     assert_within(gl, lse, bl, "lse")
 
 
+@pytest.mark.parametrize("B,D,H,Hq,max_len", [(130, 64, 1, 2, 2600), (256, 128, 2, 2, 2600), (65, 256, 1, 1, 2000),
+                                              (64, 64, 32, 32, 2100), (63, 128, 33, 33, 2100)])
+def test_attend_many_sequences_of_long_limits(q, B, D, H, Hq, max_len):
+    """Chunks found among more than 64 sequences, some of them cut; and whole
+    tiles taken by length, equal lengths among them."""
+    g = np.random.default_rng(B + D)
+    lens = [int(v) for v in g.integers(0, 150, B)]
+    news = [min(v, 1 + v % 2) for v in lens]
+    lens[1], lens[B // 2], lens[B - 1] = (2500, 1300, 700) if H < 8 and D < 256 else (700, 150, 700) if H < 8 else (140, 300, 140)
+    news[1] = news[B // 2] = news[B - 1] = 1
+    g, raw, table, cu = attend_case(D, H, lens, news, B)
+    table = np.concatenate([table, np.full((B, 41), -1, np.int32)], 1)
+    qx = round_to(g.standard_normal((int(cu[-1]), Hq, D)), "f32")
+    want, lse, bo, bl = sh.attend(qx, cu, raw, table, lens, D ** -0.5, 0, None, None, "half", D, "f32")
+    got, gl = run_attend(q, raw, table, cu, lens, qx, D, "f32", 0, None, None, "half", max_len=max_len, max_q=2)
+    assert_within(got, want, bo, "out")
+    assert_within(gl, lse, bl, "lse")
+
+
 def test_attend_far_pages(q):
     """Pages beyond 4 GiB of the cache."""
     import torch
@@ -802,3 +821,72 @@ def test_results_repeat(q):
     t = np.zeros(9, np.int32)
     a, b = run_logprobs(q, x, "f32", t, 7), run_logprobs(q, x, "f32", t, 7)
     assert all(np.array_equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.parametrize("D,dtype,H,Hq,n", [(128, "f32", 2, 8, 1), (64, "bf16", 1, 16, 2), (128, "bf16", 16, 32, 60)])
+def test_captured_step_as_sequences_grow(q, D, dtype, H, Hq, n):
+    """One captured call serves whatever lengths lie on the device when it is
+    replayed, up to the limit that it was captured for."""
+    import torch
+
+    B, most = 2, 4480
+    g, raw, table, cu = attend_case(D, H, [most, most], [n, n], D + n)
+    kv, tabled, cud = cache_of(q, raw, D), to_dev(table), to_dev(cu)
+    lens = to_dev(np.array([n, n], np.int32))
+    qx = round_to(g.standard_normal((B * n, Hq, D)), dtype)
+    qd = to_dev_as(qx, dtype)
+    out = torch.zeros(B * n, Hq, D, dtype=torch_dtype(dtype), device="cuda")
+    lse = torch.zeros(B * n, Hq, device="cuda")
+    need = q.qattend_workspace_bytes(kv, Hq, B, B * n, n, most)
+    ws = poisoned(need)
+
+    def call(o, l):
+        q.qattend(q_dtype(q, dtype), qd, Hq * D, Hq, kv, B, cud, B * n, n, tabled, table.shape[1], lens, most, D ** -0.5,
+                  0, None, None, o, l, ws, need)
+
+    call(out, lse)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        call(out, lse)
+    for now in ([n, n + 3], [2100, 64 + n], [most, 700], [most, most]):
+        lens.copy_(to_dev(np.array(now, np.int32)))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got, gl = back(out), back(lse)
+        want, wl, bo, bl = sh.attend(qx, cu, raw, table, now, D ** -0.5, 0, None, None, "half", D, dtype)
+        assert_within(got, want, bo, f"out {now}")
+        assert_within(gl, wl, bl, f"lse {now}")
+        o, l = torch.zeros_like(out), torch.zeros_like(lse)
+        call(o, l)
+        assert np.array_equal(back(o), got) and np.array_equal(back(l), gl)
+
+
+def test_two_calls_at_once(q):
+    """Calls on two streams, each with its own workspace."""
+    import torch
+
+    D, H, Hq = 128, 4, 8
+    cases = []
+    for seed, lens in ((1, [5000, 900]), (2, [300, 4000])):
+        g, raw, table, cu = attend_case(D, H, lens, [1, 1], seed)
+        qx = round_to(g.standard_normal((2, Hq, D)), "f32")
+        kv = cache_of(q, raw, D)
+        need = q.qattend_workspace_bytes(kv, Hq, 2, 2, 1, max(lens))
+        cases.append(dict(kv=kv, table=to_dev(table), most=table.shape[1], cu=to_dev(cu), lens=to_dev(np.array(lens, np.int32)),
+                          n=max(lens), q=to_dev(qx), out=torch.zeros(2, Hq, D, device="cuda"), need=need, ws=poisoned(need),
+                          lse=torch.zeros(2, Hq, device="cuda"), s=torch.cuda.Stream(),
+                          want=sh.attend(qx, cu, raw, table, lens, D ** -0.5, 0, None, None, "half", D, "f32")))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c in cases:
+            q.qattend(q.Q8K_F32, c["q"], Hq * D, Hq, c["kv"], 2, c["cu"], 2, 1, c["table"], c["most"], c["lens"], c["n"],
+                      D ** -0.5, 0, None, None, c["out"], c["lse"], c["ws"], c["need"], c["s"])
+    for c in cases:
+        c["s"].synchronize()
+        want, wl, bo, bl = c["want"]
+        assert_within(host(c["out"]), want, bo, "out")
+        assert_within(host(c["lse"]), wl, bl, "lse")
