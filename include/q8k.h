@@ -328,10 +328,12 @@ int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t
  * int32 [B][max_pages]: its pages in order; pages may be shared between
  * sequences; a page outside [0, pages) is not read and its tokens count as
  * unseen.  max_q, max_len: what no sequence's new tokens and length exceed
- * (max_len <= 64 * max_pages); a longer length is cut to max_len, new tokens
- * beyond max_q are left out.
- * out: [Tq][q_heads][head_dim] of dtype, 16-byte aligned; lse: NULL or fp32
- * [Tq][q_heads], natural logarithms.
+ * (max_len <= 64 * max_pages; max_q <= Tq and max_q * q_heads / kv_heads <=
+ * 2^30); a longer length is cut to max_len, new tokens beyond max_q are left
+ * out.
+ * out: [Tq][q_heads][head_dim] of dtype, 16-byte aligned, not overlapping q (a
+ * row of q is read by several workgroups); lse: NULL or fp32 [Tq][q_heads],
+ * natural logarithms.
  * ws / ws_bytes: caller-owned workspace, 16-byte aligned, of at least
  * qattend_workspace_bytes(...) bytes (0: may be NULL): the fp32 results of
  * splits over the keys, joined in a fixed order.  Its contents are scratch:
@@ -355,7 +357,8 @@ int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q
  * Logits of -inf (banned tokens) are served; a row of nothing else has lse and
  * log probabilities -inf and entropy 0.  A row with +inf or NaN has NaN for
  * every real result; its top ids rank NaN below every number.
- * ws / ws_bytes: as qattend's, qlogprobs_workspace_bytes(T, V, topn) bytes. */
+ * ws / ws_bytes: as qattend's, qlogprobs_workspace_bytes(T, V, topn) bytes (0
+ * where rows are not cut into parts). */
 size_t qlogprobs_workspace_bytes(int64_t T, int64_t V, int32_t topn);
 int qlogprobs(int dtype, const void* logits, int64_t stride, int64_t T, int64_t V, const int32_t* targets,
               float* logprob, float* entropy, float* lse, int32_t topn, int32_t* top_ids, float* top_logprob,
