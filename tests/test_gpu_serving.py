@@ -890,3 +890,14 @@ def test_two_calls_at_once(q):
         want, wl, bo, bl = c["want"]
         assert_within(host(c["out"]), want, bo, "out")
         assert_within(host(c["lse"]), wl, bl, "lse")
+
+
+@pytest.mark.parametrize("n", [2, 200])
+def test_attend_nothing_cached(q, n):
+    """A limit of no tokens at all: every row is one that sees nothing."""
+    for D, H, Hq in ((64, 1, 3), (128, 64, 64), (256, 2, 2)):
+        g, raw, table, cu = attend_case(D, H, [0, 0], [n, 1], 1)
+        qx = round_to(g.standard_normal((n + 1, Hq, D)), "f32")
+        got, gl = run_attend(q, raw, table, cu, [0, 0], qx, D, "f32", 0, None, None, "half")
+        assert_exact(got, np.zeros_like(got), "out")
+        assert np.isneginf(gl).all()
