@@ -20,9 +20,11 @@ namespace {
 constexpr int ROWS = 16;
 
 // Probabilities enter the second product as fp16 pieces of p * vscale / R *
-// 2^15, R a power of two at least the largest vscale a wave has met: at most
-// 2^15 (fp16 ends at 65504), and what fp16's smallest step then loses of a
-// token is 2^-40 of the largest one's share.
+// 2^15, R a power of two at least the largest vscale that the row has seen in
+// this wave: at most 2^15 (fp16 ends at 65504), and what fp16's smallest step
+// then loses of a token is 2^-40 of the largest one's share.  R is the row's own
+// (its accumulators lie in the lanes that hold it): what other rows of the tile
+// see, of whatever size, infinite or NaN, does not touch it.
 constexpr float P_UP = 32768.0f, P_DOWN = 1.0f / 32768.0f;
 
 // A product's steps go round four accumulators, so that no instruction waits
@@ -188,8 +190,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             const float mn = fmaxf(m, groups_max(tmax));
             float Rn = R;
             if (__any(vmax > R)) {
-                const float v = wave_max_dpp(vmax);
-                Rn = fmaxf(R, pow2f(exponent_of(v) + 1));
+                const float v = groups_max(vmax);
+                Rn = v > R ? pow2f(exponent_of(v) + 1) : R;
             }
             const float base = mn == -INFINITY ? 0.0f : mn;
             const float down = __builtin_amdgcn_exp2f(m - base);
