@@ -16,7 +16,12 @@ namespace q8k {
 
 namespace {
 
-constexpr float P_UP = 32768.0f, P_DOWN = 1.0f / 32768.0f;  // attend_decode.hip
+// Probabilities enter the second product as fp16 pieces of p * vscale / U, U a
+// row's own power of two: R / 2^15 of attend_decode.hip.  1 / U lies in the
+// exponent, e^(s - m) / U = 2^(s log2 e - m + K), so that it costs no
+// instruction a score; m is kept whole, so that K - m is exact, and the sum of the
+// probabilities has the same unit.  From 2^-100 on, so that no sum overflows.
+constexpr int K_FIRST = 100;
 
 // One page's operands in LDS, in the order in which the lanes of a wave read
 // them: every read and write of 16 bytes a lane is 1 KB of consecutive bytes.
@@ -25,8 +30,10 @@ struct PageOps {
     uint4 k[4][D / 32][64];  // [16 tokens][k step][lane]
     uint4 v[D / 16][2][64];  // [16 values][32 tokens][lane]
     float ks[KV_PAGE], vs[KV_PAGE];
-    float vmax;  // the largest of the vs that some row of the tile sees
-    float pad[3];
+    // The largest of the vs that some row of the tile sees; NaN where one of these is
+    // infinite or NaN: such ones are zeros in vs, and bits in `odd`.
+    float vmax;
+    uint32_t odd[2], pad;
 };
 
 // One workgroup: 64 RT rows of one key head over its split's pages, 16 RT rows
@@ -39,7 +46,7 @@ struct PageOps {
 // one half; tiles that are split into chunks lose by it: 500 tokens over 16001
 // 283 us, 275).
 template <int D, int WAVES, int HALVES, int RT, int NQ, int NP>
-__global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Attend a) {
+__global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) void attend_tile_kernel(Attend a) {
     constexpr int KS = D / 32, DB = D / 16, ROWS = 16 * RT * WAVES;
     constexpr int KC = D / 16 / WAVES;  // 1 KB pieces of a page's keys (and of its values) a wave brings
     __shared__ union {
@@ -69,7 +76,8 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
     // through its part of LDS into the registers that the products take.
     h8_t qf[RT][NQ][KS];
     float unit[RT];
-    Span span[RT];
+    int last[RT];  // the last token that the row sees; it sees those less than `window` before it
+    const uint32_t window = a.window > 0 ? (uint32_t)a.window : 0x7fffffffu;
     {
         constexpr int NI = D / 32;  // items of 16 rows a lane
         float(*qs)[D + 4] = sm.q[wave_of_all];
@@ -93,7 +101,7 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
                 put_q(a, i % (D / 8), qi[rt][n], qs[i / (D / 8)]);
             }
             unit[rt] = query_operand<D, NQ>(a, qs[col], g, qf[rt]);
-            span[rt] = span_of(a, seq, row_of_tile(a, tile, min((wave * RT + rt) * 16 + col, rows - 1 - tile.row0)).tok);
+            last[rt] = span_of(a, seq, row_of_tile(a, tile, min((wave * RT + rt) * 16 + col, rows - 1 - tile.row0)).tok).last;
         }
     }
     __syncthreads();
@@ -140,18 +148,24 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
         if (wave == 1) {
             // what lies in places that no row sees may be anything, NaN scales included
             const int j = at_p * KV_PAGE + lane;
-            const float v = j >= tile.lo.first && j <= tile.hi.last ? sc_raw : 0.0f;
+            float v = j >= tile.lo.first && j <= tile.hi.last ? sc_raw : 0.0f;
+            const uint64_t odd = __ballot(!(fabsf(v) < INFINITY));
+            v = fabsf(v) < INFINITY ? v : 0.0f;
             o.vs[lane] = v;
             const float most = wave_max_dpp(v);
-            if (lane == 0) o.vmax = most;
+            if (lane == 0) {
+                o.vmax = odd ? __builtin_nanf("") : most;
+                o.odd[0] = (uint32_t)odd;
+                o.odd[1] = (uint32_t)(odd >> 32);
+            }
         }
     };
 
-    float m[RT], l[RT], R = pow2f(-100), Rinv = pow2f(100) * P_UP;
+    float m[RT], l[RT], U[RT], c[RT];  // l: the sum / U; c: K - m
     f4_t acc[RT][DB];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = -INFINITY, l[rt] = 0.0f;
+        m[rt] = -INFINITY, l[rt] = 0.0f, U[rt] = pow2f(-K_FIRST), c[rt] = K_FIRST;
 #pragma unroll
         for (int d = 0; d < DB; ++d) acc[rt][d] = f4_t{0, 0, 0, 0};
     }
@@ -200,7 +214,8 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
                 }
             }
             // pages that some row sees only in part
-            if (p * KV_PAGE < tile.hi.first || p * KV_PAGE + KV_PAGE - 1 > tile.lo.last) {
+            const bool in_part = p * KV_PAGE < tile.hi.first || p * KV_PAGE + KV_PAGE - 1 > tile.lo.last;
+            if (in_part) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -208,12 +223,12 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
                         const int j = p * KV_PAGE + 16 * q + 4 * g + i;
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
-                            s4[rt][q][i] = j >= span[rt].first && j <= span[rt].last ? s4[rt][q][i] : -INFINITY;
+                            s4[rt][q][i] = (uint32_t)(last[rt] - j) < window ? s4[rt][q][i] : -INFINITY;
                     }
             }
             const float vmax = o.vmax;
             float tmax[RT];
-            bool grew = vmax > R;
+            bool grew = false, more = false;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 tmax[rt] = s4[rt][0][0];
@@ -222,23 +237,47 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmax[rt] = fmaxf(tmax[rt], s4[rt][q][i]);
                 tmax[rt] *= unit[rt];
+                more |= !(vmax * 0x1p-15f <= U[rt]);
                 grew |= tmax[rt] > m[rt];
             }
-            if (__any(grew)) {
-                const float Rn = vmax > R ? pow2f(exponent_of(vmax) + 1) : R;
+            if (__any(grew || more)) {
+                // The page's largest value scale that the row sees (not one that only other
+                // rows of the tile see: it would take this row's bits); NaN or infinite where
+                // it sees one that is not finite, and its result is NaN from here on.
+                float most[RT];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) most[rt] = in_part ? 0.0f : vmax;
+                if (in_part && __any(more)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f4_t v = *reinterpret_cast<const f4_t*>(&o.vs[16 * q + 4 * g]);
+                        const uint32_t odd = o.odd[q / 2] >> (16 * (q & 1) + 4 * g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = p * KV_PAGE + 16 * q + 4 * g + i;
+                            const float w = odd >> i & 1u ? INFINITY : v[i];
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt)
+                                most[rt] = (uint32_t)(last[rt] - j) < window ? fmaxf(most[rt], w) : most[rt];
+                        }
+                    }
+                }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const float mn = fmaxf(m[rt], groups_max(tmax[rt]));
+                    const float mn = fmaxf(m[rt], ceilf(groups_max(tmax[rt])));
                     const float base = mn == -INFINITY ? 0.0f : mn;
                     const float down = __builtin_amdgcn_exp2f(m[rt] - base);
-                    l[rt] *= down;
-                    const float both = down * (R / Rn);
+                    const float v = groups_max(most[rt]);
+                    const bool odd = !(v < INFINITY);
+                    const float Un = v > U[rt] * 0x1p15f && !odd ? pow2f(exponent_of(v) - 14) : U[rt];
+                    const float both = down * (U[rt] / Un);
+                    l[rt] *= both;
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) acc[rt][d] *= both;
+                    for (int d = 0; d < DB; ++d) acc[rt][d] *= odd ? __builtin_nanf("") : both;
                     m[rt] = mn;
+                    U[rt] = Un;
+                    c[rt] = (float)(127 - (int)(__builtin_bit_cast(uint32_t, Un) >> 23)) - base;
                 }
-                R = Rn;
-                Rinv = P_UP / Rn;
             }
             // The second product by halves of the page's tokens (all probabilities
             // first: 1.4% longer), its values two row blocks ahead.
@@ -253,15 +292,14 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const int q = 2 * t + b;
-                    const float4 vq = *reinterpret_cast<const float4*>(&o.vs[16 * q + 4 * g]);
-                    const float v[4] = {vq.x * Rinv, vq.y * Rinv, vq.z * Rinv, vq.w * Rinv};
+                    if (b && D == 64) __builtin_amdgcn_sched_barrier(0);  // keeps to three waves' registers
+                    const f4_t v = *reinterpret_cast<const f4_t*>(&o.vs[16 * q + 4 * g]);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
-                        const float mb = m[rt] == -INFINITY ? 0.0f : m[rt];
                         float e[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[rt][q][i], unit[rt], -mb));
+                            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[rt][q][i], unit[rt], c[rt]));
                             l[rt] += e[i];
                             e[i] *= v[i];
                         }
@@ -298,14 +336,13 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
     if (HALVES == 2) {
         auto& join = sm.join[wave];
         if (half == 1) {
-            const float f = R * P_DOWN;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    join.acc[rt][d][lane] = make_float4(acc[rt][d][0] * f, acc[rt][d][1] * f, acc[rt][d][2] * f,
-                                                        acc[rt][d][3] * f);
-                join.ml[rt][lane] = make_float2(m[rt], l[rt]);
+                    join.acc[rt][d][lane] = make_float4(acc[rt][d][0] * U[rt], acc[rt][d][1] * U[rt],
+                                                        acc[rt][d][2] * U[rt], acc[rt][d][3] * U[rt]);
+                join.ml[rt][lane] = make_float2(m[rt], l[rt] * U[rt]);
             }
         }
         __syncthreads();
@@ -315,16 +352,15 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
             const float2 ml = join.ml[rt][lane];
             const float mn = fmaxf(m[rt], ml.x), base = mn == -INFINITY ? 0.0f : mn;
             const float f0 = __builtin_amdgcn_exp2f(m[rt] - base), f1 = __builtin_amdgcn_exp2f(ml.x - base);
-            l[rt] = l[rt] * f0 + ml.y * f1;
+            l[rt] = l[rt] * U[rt] * f0 + ml.y * f1;
             m[rt] = mn;
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 const float4 v = join.acc[rt][d][lane];
-                acc[rt][d] = acc[rt][d] * (f0 * R * P_DOWN) + f4_t{v.x, v.y, v.z, v.w} * f1;
+                acc[rt][d] = acc[rt][d] * (f0 * U[rt]) + f4_t{v.x, v.y, v.z, v.w} * f1;
             }
         }
     }
-    const float unscale = HALVES == 2 ? 1.0f : R * P_DOWN;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int r = (wave * RT + rt) * 16 + col;
@@ -332,21 +368,21 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, 2) void attend_tile_kernel(Att
         if (tile.row0 + r >= rows) continue;
         const int64_t qr = q_row_of(a, seq, h, row_of_tile(a, tile, r));
         const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
-        float f = unscale;
+        const float u = HALVES == 2 ? 1.0f : U[rt];
         if (it.splits > 1) {
             const int64_t at = (item * a.heads + h) * ROWS + r;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
                 *reinterpret_cast<float4*>(a.part + at * D + 16 * d + 4 * g) =
-                    make_float4(acc[rt][d][0] * f, acc[rt][d][1] * f, acc[rt][d][2] * f, acc[rt][d][3] * f);
-            if (g == 0) a.ml[at] = make_float2(m[rt], lr);
+                    make_float4(acc[rt][d][0] * u, acc[rt][d][1] * u, acc[rt][d][2] * u, acc[rt][d][3] * u);
+            if (g == 0) a.ml[at] = make_float2(m[rt], lr * u);
         } else {
-            f = lr == 0.0f ? 0.0f : f / lr;
+            const float f = lr == 0.0f ? 0.0f : 1.0f / lr;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
                 store4f(a.out, qr * D + 16 * d + 4 * g, a.dtype,
                         make_float4(acc[rt][d][0] * f, acc[rt][d][1] * f, acc[rt][d][2] * f, acc[rt][d][3] * f));
-            if (g == 0 && a.lse) a.lse[qr] = lr == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(lr)) * LN2;
+            if (g == 0 && a.lse) a.lse[qr] = lr == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(lr * u)) * LN2;
         }
     }
 }

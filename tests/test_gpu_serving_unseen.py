@@ -59,3 +59,30 @@ FEW = [
 @pytest.mark.parametrize("D,dtype,H,group,lens,news", FEW)
 def test_few_rows(q, D, dtype, H, group, lens, news, window, kind):
     unseen_case(q, D, dtype, H, group, lens, news, window, kind)
+
+
+# tiles of 64 rows, whole and in chunks, and of 128, whole and in chunks
+MANY = [
+    ([200, 140], [150, 70], 32, 1, 200),
+    ([330], [140], 8, 4, 330),
+    ([900, 300], [65, 33], 16, 1, 2200),
+    ([129, 140], [128, 70], 64, 1, 140),
+    ([240, 140], [128, 70], 16, 8, 240),
+    ([900, 300], [128, 100], 32, 1, 3200),
+]
+
+
+@pytest.mark.parametrize("kind", ["large", "huge", "inf", "nan"])
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("D,dtype", [(64, "f32"), (64, "bf16"), (128, "f32"), (128, "bf16"), (256, "f32"), (256, "bf16")])
+@pytest.mark.parametrize("lens,news,H,group,max_len", MANY)
+def test_many_rows(q, D, dtype, H, group, lens, news, window, kind, max_len):
+    unseen_case(q, D, dtype, H, group, lens, news, window, kind, max_len)
+
+
+@pytest.mark.parametrize("kind", ["inf", "nan"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,news,H,group,max_len", MANY + [([70, 130], [3, 5], 2, 4, 130)])
+def test_half_precision(q, D, H, group, lens, news, kind, max_len):
+    """fp16 results cannot hold values of 1e-12: what the rows that do not see the token have is compared with zeros' bound."""
+    unseen_case(q, D, "f16", H, group, lens, news, 0, kind, max_len)
