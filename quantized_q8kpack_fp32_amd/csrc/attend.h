@@ -94,6 +94,7 @@ __device__ __forceinline__ int exponent_of(float v) {
 
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uni_f(float v) { return __builtin_bit_cast(float, uni(__builtin_bit_cast(int, v))); }
 
 // A sequence's new tokens and length, with what the device-side values say
 // cut to what the call's sizes allow, so that no access leaves its buffer.
@@ -341,6 +342,17 @@ __device__ __forceinline__ void put_q(const Attend& a, int item, const QueryItem
 __device__ __forceinline__ float score_unit(const Attend& a, int e) {
     const float s = fabsf(a.scale);
     return fmaxf((s > 0.0f ? s * LOG2E : 1.0f) * pow2f(-e), 1.17549435e-38f);
+}
+
+// A running maximum m so far from zero that its steps are a half and more: the
+// fused t unit - m, exact before its one rounding, would then be off zero at the
+// maximum itself by as much, and its power of two by that factor.  Such a row's
+// products are rounded first, as the maximum was, and their distances from it
+// taken for the scores, in the same unit.
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= 8388608.0f && m > -INFINITY; }
+__device__ __forceinline__ float far_score(float t, float unit, float inv_unit, float m) {
+#pragma clang fp contract(off)
+    return (t * unit - m) * inv_unit;
 }
 
 // The operand of a query row from LDS, in pieces times 2^(12 - e), e the

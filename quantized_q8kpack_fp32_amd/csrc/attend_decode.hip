@@ -121,6 +121,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     const float unit = query_operand<D, NQ>(a, qs[col], g, qf);
     const Span span = span_of(a, seq, row_of_tile(a, tile, min(col, tile.rows - 1 - tile.row0)).tok);
     float m = -INFINITY, l = 0.0f, R = pow2f(-100), Rinv = pow2f(100) * P_UP;
+    bool far = false;  // some row's m is: is_far
     f4_t acc[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d) acc[d] = f4_t{0, 0, 0, 0};
@@ -202,8 +203,17 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             m = mn;
             R = Rn;
             Rinv = P_UP / Rn;
+            far |= __any(is_far(mn));
         }
-        const float mb = m == -INFINITY ? 0.0f : m;
+        float mb = m == -INFINITY ? 0.0f : m;
+        if (far && is_far(m)) {
+            const float inv = 1.0f / unit;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[q][i] = far_score(t[q][i], unit, inv, m);
+            mb = 0.0f;
+        }
         uint32_t pw[NP][4][2];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {

@@ -161,11 +161,15 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
         }
     };
 
-    float m[RT], l[RT], U[RT], c[RT];  // l: the sum / U; c: K - m
+    float m[RT], l[RT], c[RT];  // l: the sum / U; c: K - m, or K where m is -inf or far
+    bool far = false;           // some row's m is: is_far
+    float U_least = pow2f(-K_FIRST);  // of the wave's rows
+    const auto shift_of = [](float m) { return m == -INFINITY || is_far(m) ? 0.0f : m; };
+    const auto unit_of = [&](int rt) { return pow2f(-(int)(c[rt] + shift_of(m[rt]))); };
     f4_t acc[RT][DB];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = -INFINITY, l[rt] = 0.0f, U[rt] = pow2f(-K_FIRST), c[rt] = K_FIRST;
+        m[rt] = -INFINITY, l[rt] = 0.0f, c[rt] = K_FIRST;
 #pragma unroll
         for (int d = 0; d < DB; ++d) acc[rt][d] = f4_t{0, 0, 0, 0};
     }
@@ -228,7 +232,8 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
             }
             const float vmax = o.vmax;
             float tmax[RT];
-            bool grew = false, more = false;
+            const bool more = !(vmax * 0x1p-15f <= U_least);
+            bool grew = more || far;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 tmax[rt] = s4[rt][0][0];
@@ -237,47 +242,71 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmax[rt] = fmaxf(tmax[rt], s4[rt][q][i]);
                 tmax[rt] *= unit[rt];
-                more |= !(vmax * 0x1p-15f <= U[rt]);
                 grew |= tmax[rt] > m[rt];
             }
-            if (__any(grew || more)) {
-                // The page's largest value scale that the row sees (not one that only other
-                // rows of the tile see: it would take this row's bits); NaN or infinite where
-                // it sees one that is not finite, and its result is NaN from here on.
-                float most[RT];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) most[rt] = in_part ? 0.0f : vmax;
-                if (in_part && __any(more)) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const f4_t v = *reinterpret_cast<const f4_t*>(&o.vs[16 * q + 4 * g]);
-                        const uint32_t odd = o.odd[q / 2] >> (16 * (q & 1) + 4 * g);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = p * KV_PAGE + 16 * q + 4 * g + i;
-                            const float w = odd >> i & 1u ? INFINITY : v[i];
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt)
-                                most[rt] = (uint32_t)(last[rt] - j) < window ? fmaxf(most[rt], w) : most[rt];
-                        }
-                    }
-                }
+            if (__any(grew)) {
+                float both[RT];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     const float mn = fmaxf(m[rt], ceilf(groups_max(tmax[rt])));
-                    const float base = mn == -INFINITY ? 0.0f : mn;
-                    const float down = __builtin_amdgcn_exp2f(m[rt] - base);
-                    const float v = groups_max(most[rt]);
-                    const bool odd = !(v < INFINITY);
-                    const float Un = v > U[rt] * 0x1p15f && !odd ? pow2f(exponent_of(v) - 14) : U[rt];
-                    const float both = down * (U[rt] / Un);
-                    l[rt] *= both;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) acc[rt][d] *= odd ? __builtin_nanf("") : both;
+                    both[rt] = __builtin_amdgcn_exp2f(m[rt] - (mn == -INFINITY ? 0.0f : mn));
+                    c[rt] += shift_of(m[rt]) - shift_of(mn);
                     m[rt] = mn;
-                    U[rt] = Un;
-                    c[rt] = (float)(127 - (int)(__builtin_bit_cast(uint32_t, Un) >> 23)) - base;
+                    far |= __any(is_far(mn));
                 }
+                if (__any(more)) {
+                    // The page's largest value scale that the row sees (not one that only other
+                    // rows of the tile see: it would take this row's bits); NaN or infinite where
+                    // it sees one that is not finite, and its result is NaN from here on.
+                    float most[RT], least = INFINITY;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) most[rt] = in_part ? 0.0f : vmax;
+                    if (in_part) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f4_t v = *reinterpret_cast<const f4_t*>(&o.vs[16 * q + 4 * g]);
+                            const uint32_t odd = o.odd[q / 2] >> (16 * (q & 1) + 4 * g);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int j = p * KV_PAGE + 16 * q + 4 * g + i;
+                                const float w = odd >> i & 1u ? INFINITY : v[i];
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt)
+                                    most[rt] = (uint32_t)(last[rt] - j) < window ? fmaxf(most[rt], w) : most[rt];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float v = groups_max(most[rt]), U = unit_of(rt);
+                        const bool odd = !(v < INFINITY);
+                        if (__any(odd))
+#pragma unroll
+                            for (int d = 0; d < DB; ++d) acc[rt][d] *= odd ? __builtin_nanf("") : 1.0f;
+                        const int e = exponent_of(v) - 14;
+                        const bool raise = v > U * 0x1p15f && !odd;
+                        both[rt] *= raise ? U * pow2f(-e) : 1.0f;
+                        c[rt] = raise ? (float)-e - shift_of(m[rt]) : c[rt];
+                        least = fminf(least, unit_of(rt));
+                    }
+                    U_least = uni_f(-wave_max_dpp(-least));
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    l[rt] *= both[rt];
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) acc[rt][d] *= both[rt];
+                }
+                if (far)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float inv = 1.0f / unit[rt];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s4[rt][q][i] = is_far(m[rt]) ? far_score(s4[rt][q][i], unit[rt], inv, m[rt]) : s4[rt][q][i];
+                    }
             }
             // The second product by halves of the page's tokens (all probabilities
             // first: 1.4% longer), its values two row blocks ahead.
@@ -338,11 +367,12 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
         if (half == 1) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
+                const float u = unit_of(rt);
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
-                    join.acc[rt][d][lane] = make_float4(acc[rt][d][0] * U[rt], acc[rt][d][1] * U[rt],
-                                                        acc[rt][d][2] * U[rt], acc[rt][d][3] * U[rt]);
-                join.ml[rt][lane] = make_float2(m[rt], l[rt] * U[rt]);
+                    join.acc[rt][d][lane] = make_float4(acc[rt][d][0] * u, acc[rt][d][1] * u, acc[rt][d][2] * u,
+                                                        acc[rt][d][3] * u);
+                join.ml[rt][lane] = make_float2(m[rt], l[rt] * u);
             }
         }
         __syncthreads();
@@ -351,13 +381,13 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
         for (int rt = 0; rt < RT; ++rt) {
             const float2 ml = join.ml[rt][lane];
             const float mn = fmaxf(m[rt], ml.x), base = mn == -INFINITY ? 0.0f : mn;
-            const float f0 = __builtin_amdgcn_exp2f(m[rt] - base), f1 = __builtin_amdgcn_exp2f(ml.x - base);
-            l[rt] = l[rt] * U[rt] * f0 + ml.y * f1;
+            const float f0 = __builtin_amdgcn_exp2f(m[rt] - base) * unit_of(rt), f1 = __builtin_amdgcn_exp2f(ml.x - base);
+            l[rt] = l[rt] * f0 + ml.y * f1;
             m[rt] = mn;
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 const float4 v = join.acc[rt][d][lane];
-                acc[rt][d] = acc[rt][d] * (f0 * U[rt]) + f4_t{v.x, v.y, v.z, v.w} * f1;
+                acc[rt][d] = acc[rt][d] * f0 + f4_t{v.x, v.y, v.z, v.w} * f1;
             }
         }
     }
@@ -368,7 +398,7 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
         if (tile.row0 + r >= rows) continue;
         const int64_t qr = q_row_of(a, seq, h, row_of_tile(a, tile, r));
         const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
-        const float u = HALVES == 2 ? 1.0f : U[rt];
+        const float u = HALVES == 2 ? 1.0f : unit_of(rt);
         if (it.splits > 1) {
             const int64_t at = (item * a.heads + h) * ROWS + r;
 #pragma unroll
