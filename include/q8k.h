@@ -267,6 +267,9 @@ int qmatmul_prefill_moe_noalloc(int qtype, const void* w, int64_t E, int64_t row
  *       (t>>2 & 3) << 4 | (t>>5) << 3 | (t>>4 & 1) << 2 | (t & 3)
  *   fp32 key scales [64 tokens], fp32 value scales [64 tokens].
  * A fresh cache may hold anything.
+ * As in q8k_pack, a head's row that holds NaN takes its scale from its other
+ * values (0 without any) and code 0 for them, so that they read back as 0; one
+ * that holds an infinity has codes 0 and an infinite scale and reads back as NaN.
  * head_dim: 64, 128 or 256.  kv_heads <= 4096; pages <= 2^24. */
 typedef struct {
     void* data; /* 16-byte aligned */

@@ -131,7 +131,8 @@ __device__ __forceinline__ float max4(float4 v) {
     return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 }
 
-// Maximum over aligned groups of N lanes (8, 16 or 32), in every lane of the group.
+// Maximum over aligned groups of N lanes (8, 16 or 32), in every lane of the group,
+// of magnitudes: NaN are passed over, and nothing but NaN counts as 0 (q8_K's rule).
 template <int N>
 __device__ __forceinline__ float group_max(float v) {
     static_assert(N == 8 || N == 16 || N == 32, "lanes of a head's row");
@@ -141,20 +142,22 @@ __device__ __forceinline__ float group_max(float v) {
     v = fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, false)));  // row_half_mirror
     if (N >= 16) v = fmaxf(v, dpp_f(v, 3));  // row_ror:8
     if (N == 32) v = fmaxf(v, __shfl_xor(v, 16, WAVE));
-    return v;
+    return fmaxf(v, 0.0f);
 }
 
 // Codes of four values: q8_K's rule with the row's scale (q8k_quant.h),
 // round-half-even(x * (127/amax)) clamped to [-127, 127].  Adding 1.5 * 2^23
 // rounds a product to a whole number, half to even, and leaves it in the low
 // bits of the sum.  A finite 127/amax needs no clamp; where it overflows (amax
-// zero or nearly), nonzero values saturate and zeros stay zero.
+// zero or nearly), nonzero values saturate and zeros stay zero.  A NaN's code is 0
+// (the maximum takes the place of its sum: whatever bits it came with), and so are
+// all codes beside an infinity (127/amax is 0, and 0 times inf NaN).
 __device__ __forceinline__ uint32_t kv_codes4(float4 v, float iscale) {
 #pragma clang fp contract(off)
     const float x[4] = {v.x, v.y, v.z, v.w};
     uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(uint32_t, x[e] * iscale + 12582912.0f);
+    for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(uint32_t, fmaxf(x[e] * iscale + 12582912.0f, 0.0f));
     if (!(iscale < INFINITY))
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = x[e] > 0.0f ? 127u : x[e] < 0.0f ? 129u : 0u;
