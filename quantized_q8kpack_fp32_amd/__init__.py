@@ -289,6 +289,38 @@ def _flat(dev, what, t, dtype=None):
     return t.data_ptr()
 
 
+def _rows(dev, what, t, dtype, T, stride, row):
+    """_on of T rows of ``row`` values each, ``stride`` elements apart."""
+    if t.__class__ is int or t is None:
+        return t
+    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
+        _refuse(dev, what, t, dtype)
+    n, s = t.shape, t.stride()
+    if not (len(s) == 3 and s[0] == stride and s[1] == n[2] and s[2] == 1 and n[1] * n[2] >= row):
+        _check_rows(what, t, T, stride, row)
+    return t.data_ptr()
+
+
+def _check_rows(what, t, T, stride, row):
+    """Any tensor's rows: a row lies in the last axes whose elements follow each other, and rows begin where one of
+    the axes before has its next element (or a whole number of them on).  Axes of one element, the rows of a flat
+    buffer and a single row's stride are free."""
+    axes = [(n, s) for n, s in zip(t.shape, t.stride()) if n != 1]
+    run, starts = 1, [1]
+    while axes and axes[-1][1] == run:
+        run *= axes.pop()[0]
+        starts.append(run)
+    if axes:
+        n, step = axes[-1]
+        one = all(outer[1] == inner[0] * inner[1] for outer, inner in zip(axes, axes[1:]))
+        fine = run >= row and (T <= 1 or (step > 0 and stride % step == 0 and (one or (T - 1) * stride < n * step)))
+    else:
+        fine = T <= 1 or t.dim() == 1 or any(n >= row and stride % n == 0 for n in starts)
+    if not fine:
+        raise ValueError(f"{what}, of shape {tuple(t.shape)} and strides {t.stride()}, does not hold rows of {row} "
+                         f"values, {stride} elements apart")
+
+
 def _refuse(dev, what, t, dtype):
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} is {t.dtype}, {dtype} is taken")
@@ -361,7 +393,9 @@ def q8k_kv_bytes(pages: int, kv_heads: int, head_dim: int) -> int:
 
 def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
-    _check(lib.q8k_kv_append(dtype, _on(dev, "k", k, t), k_stride, _on(dev, "v", v, t), v_stride, T,
+    row = kv.kv_heads * kv.head_dim
+    _check(lib.q8k_kv_append(dtype, _rows(dev, "k", k, t, T, k_stride, row), k_stride,
+                             _rows(dev, "v", v, t, T, v_stride, row), v_stride, T,
                              _flat(dev, "pos", pos, torch.int32), _rope(dev, rope),
                              _flat(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream_of(dev, stream)))
 
@@ -381,8 +415,9 @@ def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: in
             ws_bytes: int = 0, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
     i32 = torch.int32
-    _check(lib.qattend(dtype, _on(dev, "q", q, t), q_stride, q_heads, _kv(dev, kv), B, _flat(dev, "cu_q", cu_q, i32), Tq,
-                       max_q, _flat(dev, "page_table", page_table, i32), max_pages, _flat(dev, "kv_len", kv_len, i32),
+    _check(lib.qattend(dtype, _rows(dev, "q", q, t, Tq, q_stride, q_heads * kv.head_dim), q_stride, q_heads,
+                       _kv(dev, kv), B, _flat(dev, "cu_q", cu_q, i32), Tq, max_q,
+                       _flat(dev, "page_table", page_table, i32), max_pages, _flat(dev, "kv_len", kv_len, i32),
                        max_len, scale, window, _flat(dev, "pos", pos, i32), _rope(dev, rope), _flat(dev, "out", out, t),
                        _flat(dev, "lse", lse, torch.float32), _flat(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
 
@@ -394,7 +429,7 @@ def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:
 def qlogprobs(dtype: int, logits, stride: int, T: int, V: int, targets, logprob, entropy=None, lse=None, topn: int = 0,
               top_ids=None, top_logprob=None, ws=None, ws_bytes: int = 0, stream=None) -> None:
     dev, f32 = _device(), torch.float32
-    _check(lib.qlogprobs(dtype, _on(dev, "logits", logits, _TYPES.get(dtype)), stride, T, V,
+    _check(lib.qlogprobs(dtype, _rows(dev, "logits", logits, _TYPES.get(dtype), T, stride, V), stride, T, V,
                          _flat(dev, "targets", targets, torch.int32), _flat(dev, "logprob", logprob, f32),
                          _flat(dev, "entropy", entropy, f32), _flat(dev, "lse", lse, f32), topn,
                          _flat(dev, "top_ids", top_ids, torch.int32), _flat(dev, "top_logprob", top_logprob, f32),
