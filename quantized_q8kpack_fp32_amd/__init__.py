@@ -270,33 +270,42 @@ def qmatmul_prefill_moe_noalloc(qtype: int, w, E: int, rows: int, K: int, xq, T:
 
 
 # ---- the key/value cache, attention and log probabilities.  These check their
-# tensors' devices, types and strides, which the C side cannot see.
-def _on(dev, what, t, dtype=None):
-    """Device pointer of a tensor argument on GPU ``dev`` (None -> NULL, an int passes through)."""
+# tensors' devices, types, strides and sizes, which the C side cannot see (it
+# takes addresses; so do these functions, as ints, unchecked).
+def _flat(dev, what, t, dtype, need):
+    """Device pointer of a contiguous tensor of at least ``need`` elements on GPU ``dev`` (None -> NULL, an int
+    passes through)."""
     if t.__class__ is int or t is None:
         return t
-    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
-        _refuse(dev, what, t, dtype)
+    if t.get_device() != dev or t.numel() < need or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
+        _refuse(dev, what, t, dtype, need)
     return t.data_ptr()
 
 
-def _flat(dev, what, t, dtype=None):
-    """_on of a tensor whose strides the call is not told."""
+def _bytes(dev, what, t, need):
+    """_flat of a workspace of at least ``need`` bytes."""
     if t.__class__ is int or t is None:
         return t
-    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
-        _refuse(dev, what, t, dtype)
-    return t.data_ptr()
+    return _flat(dev, what, t, None, -(-need // t.element_size()))
 
 
 def _rows(dev, what, t, dtype, T, stride, row):
-    """_on of T rows of ``row`` values each, ``stride`` elements apart."""
+    """Device pointer of T rows of ``row`` values each, ``stride`` elements apart (None and ints as in _flat)."""
     if t.__class__ is int or t is None:
         return t
     if t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
         _refuse(dev, what, t, dtype)
-    n, s = t.shape, t.stride()
-    if not (len(s) == 3 and s[0] == stride and s[1] == n[2] and s[2] == 1 and n[1] * n[2] >= row):
+    s = t.stride()
+    if len(s) == 2:
+        n, m = t.shape
+        fine = s[0] == stride and s[1] == 1
+    elif len(s) == 3:
+        n, heads, m = t.shape
+        fine = s[0] == stride and s[1] == m and s[2] == 1
+        m *= heads
+    else:
+        fine = False
+    if not fine or n < T or m < row:
         _check_rows(what, t, T, stride, row)
     return t.data_ptr()
 
@@ -316,17 +325,20 @@ def _check_rows(what, t, T, stride, row):
         fine = run >= row and (T <= 1 or (step > 0 and stride % step == 0 and (one or (T - 1) * stride < n * step)))
     else:
         fine = T <= 1 or t.dim() == 1 or any(n >= row and stride % n == 0 for n in starts)
-    if not fine:
-        raise ValueError(f"{what}, of shape {tuple(t.shape)} and strides {t.stride()}, does not hold rows of {row} "
-                         f"values, {stride} elements apart")
+    reach = run + sum((n - 1) * s for n, s in axes) if t.numel() else 0
+    if not fine or (T - 1) * stride + row > reach and T > 0:
+        raise ValueError(f"{what}, of shape {tuple(t.shape)} and strides {t.stride()}, does not hold {T} rows of "
+                         f"{row} values, {stride} elements apart")
 
 
-def _refuse(dev, what, t, dtype):
+def _refuse(dev, what, t, dtype, need=0):
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} is {t.dtype}, {dtype} is taken")
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
-    raise ValueError(f"{what} must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    raise ValueError(f"{what} has {t.numel()} elements, {need} are needed")
 
 
 def _device() -> int:
@@ -358,6 +370,7 @@ class KVCache:
             if not data.is_contiguous() or data.numel() * data.element_size() < need:
                 raise ValueError(f"a cache of {pages} pages, {kv_heads} heads of {head_dim} is {need} contiguous bytes")
         self.data, self.pages, self.kv_heads, self.head_dim = data, pages, kv_heads, head_dim
+        self.device = data.get_device() if isinstance(data, torch.Tensor) else None
         self.struct = _KVStruct(_ptr(data), pages, kv_heads, head_dim)
         self.ref = ctypes.addressof(self.struct)
 
@@ -371,19 +384,22 @@ class Rope:
             if table.dtype is not torch.float32 or not table.is_contiguous() or table.numel() < positions * dim:
                 raise ValueError(f"a rotation table is contiguous fp32 [{positions}][{dim}]")
         self.table, self.positions, self.dim, self.pairs = table, positions, dim, pairs
+        self.device = table.get_device() if isinstance(table, torch.Tensor) else None
         self.struct = _RopeStruct(_ptr(table), positions, dim, pairs)
         self.ref = ctypes.addressof(self.struct)
 
 
 def _kv(dev, kv):
-    _on(dev, "kv", kv.data)
+    if kv.device != dev and kv.device is not None:
+        _refuse(dev, "kv", kv.data, None)
     return kv.ref
 
 
 def _rope(dev, rope):
     if rope is None:
         return None
-    _on(dev, "rope", rope.table)
+    if rope.device != dev and rope.device is not None:
+        _refuse(dev, "rope", rope.table, None)
     return rope.ref
 
 
@@ -396,14 +412,15 @@ def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, r
     row = kv.kv_heads * kv.head_dim
     _check(lib.q8k_kv_append(dtype, _rows(dev, "k", k, t, T, k_stride, row), k_stride,
                              _rows(dev, "v", v, t, T, v_stride, row), v_stride, T,
-                             _flat(dev, "pos", pos, torch.int32), _rope(dev, rope),
-                             _flat(dev, "slots", slots, torch.int32), _kv(dev, kv), _stream_of(dev, stream)))
+                             _flat(dev, "pos", pos, torch.int32, 0 if rope is None else T), _rope(dev, rope),
+                             _flat(dev, "slots", slots, torch.int32, T), _kv(dev, kv), _stream_of(dev, stream)))
 
 
 def q8k_kv_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
-    _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _flat(dev, "slots", slots, torch.int32), T, _flat(dev, "k", k, t),
-                           _flat(dev, "v", v, t), _stream_of(dev, stream)))
+    n = T * kv.kv_heads * kv.head_dim
+    _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _flat(dev, "slots", slots, torch.int32, T), T, _flat(dev, "k", k, t, n),
+                           _flat(dev, "v", v, t, n), _stream_of(dev, stream)))
 
 
 def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
@@ -415,11 +432,14 @@ def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: in
             ws_bytes: int = 0, stream=None) -> None:
     dev, t = _device(), _TYPES.get(dtype)
     i32 = torch.int32
-    _check(lib.qattend(dtype, _rows(dev, "q", q, t, Tq, q_stride, q_heads * kv.head_dim), q_stride, q_heads,
-                       _kv(dev, kv), B, _flat(dev, "cu_q", cu_q, i32), Tq, max_q,
-                       _flat(dev, "page_table", page_table, i32), max_pages, _flat(dev, "kv_len", kv_len, i32),
-                       max_len, scale, window, _flat(dev, "pos", pos, i32), _rope(dev, rope), _flat(dev, "out", out, t),
-                       _flat(dev, "lse", lse, torch.float32), _flat(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
+    row = q_heads * kv.head_dim
+    _check(lib.qattend(dtype, _rows(dev, "q", q, t, Tq, q_stride, row), q_stride, q_heads, _kv(dev, kv), B,
+                       _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
+                       _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+                       _flat(dev, "kv_len", kv_len, i32, B), max_len, scale, window,
+                       _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
+                       _flat(dev, "out", out, t, Tq * row), _flat(dev, "lse", lse, torch.float32, Tq * q_heads),
+                       _bytes(dev, "ws", ws, ws_bytes), ws_bytes, _stream_of(dev, stream)))
 
 
 def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:
@@ -430,10 +450,11 @@ def qlogprobs(dtype: int, logits, stride: int, T: int, V: int, targets, logprob,
               top_ids=None, top_logprob=None, ws=None, ws_bytes: int = 0, stream=None) -> None:
     dev, f32 = _device(), torch.float32
     _check(lib.qlogprobs(dtype, _rows(dev, "logits", logits, _TYPES.get(dtype), T, stride, V), stride, T, V,
-                         _flat(dev, "targets", targets, torch.int32), _flat(dev, "logprob", logprob, f32),
-                         _flat(dev, "entropy", entropy, f32), _flat(dev, "lse", lse, f32), topn,
-                         _flat(dev, "top_ids", top_ids, torch.int32), _flat(dev, "top_logprob", top_logprob, f32),
-                         _flat(dev, "ws", ws), ws_bytes, _stream_of(dev, stream)))
+                         _flat(dev, "targets", targets, torch.int32, T), _flat(dev, "logprob", logprob, f32, T),
+                         _flat(dev, "entropy", entropy, f32, T), _flat(dev, "lse", lse, f32, T), topn,
+                         _flat(dev, "top_ids", top_ids, torch.int32, T * topn),
+                         _flat(dev, "top_logprob", top_logprob, f32, T * topn), _bytes(dev, "ws", ws, ws_bytes), ws_bytes,
+                         _stream_of(dev, stream)))
 
 
 def q8k_debug_subblock_sums(qtype: int, w, rows: int, K: int, xq, y, S, stream=None) -> None:
