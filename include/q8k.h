@@ -340,7 +340,10 @@ int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t
  * ws / ws_bytes: caller-owned workspace, 16-byte aligned, of at least
  * qattend_workspace_bytes(...) bytes (0: may be NULL): the fp32 results of
  * splits over the keys, joined in a fixed order.  Its contents are scratch:
- * stream-ordered calls may share it, calls that overlap in time may not. */
+ * stream-ordered calls may share it, calls that overlap in time may not.  The
+ * size goes by how a call is split and not by its limits alone: a call with
+ * smaller ones may need more (256 sequences are split, 257 are not).  A
+ * workspace for several shapes is as large as the largest of their sizes. */
 size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
                                int64_t max_len);
 int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
