@@ -253,7 +253,12 @@ int qmatmul_prefill_moe_noalloc(int qtype, const void* w, int64_t E, int64_t row
  * held in 8 bits, the attention that reads it, and the log probabilities of
  * the output head's logits.  Activations are fp32 (as qmatvec* and
  * qmatmul_prefill* write and q8k_pack reads them), fp16 or bf16 (dtype, a
- * q8k_dtype); every sum, softmax statistic and accumulator is fp32.
+ * q8k_dtype); every sum, softmax statistic and accumulator is fp32.  The
+ * attention's products take fp16 operands: codes exactly, a query and a
+ * probability as two pieces, within 2^-21 of the value (a bf16 query that is not
+ * turned exactly); where results are bf16 a probability is one piece, within
+ * 2^-11, an eighth of the result's own half step.  lse comes from the
+ * probabilities before that.
  *
  * The cache (the page layout is the library's; other code reads it with
  * q8k_kv_read): `pages` pages of Q8K_KV_PAGE tokens, q8k_kv_bytes(...) bytes.
@@ -324,7 +329,11 @@ int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t
  * query head a reading key head a / (q_heads / kv_heads).  rope (with pos int32
  * [Tq]): q is turned by its positions on the way; NULL: q is taken as it is.
  * A token whose position is outside the table gets NaN.  q must be finite and
- * below 2^100 in magnitude after the scale.
+ * below 2^100 in magnitude, also after the scale, and a token's scores finite in
+ * fp32; keys below 2^100; values below 2^100 and, where they are not zeros, not
+ * below 2^-90 (smaller ones lose bits).  What a token does not see has no part in
+ * its results, whatever it holds: values of any size, infinities, NaN.  A token
+ * that sees a value row of infinite or NaN scale has a result that is not finite.
  * cu_q int32 [B + 1]: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1]-1,
  * ascending; Tq rows in all; rows of no sequence are left as they were in out
  * and lse.  kv_len int32 [B]: its length, the new tokens included.  page_table
