@@ -8,9 +8,9 @@
 // in one pass with a running maximum m.  It is bound by the cache's bytes
 // (2 D + 8 a token and head), which go from memory to the registers that the
 // matrix instructions read: 8 x 65537 tokens of 8 heads of 128 in 171 us, 6.4
-// TB/s (a streaming read of as many bytes reaches 6.7), 16 of up to 8191 in 37.7,
+// TB/s (a streaming read of as many bytes reaches 6.7), 16 of up to 8191 in 37.9,
 // 4.4 TB/s, 5 us of it the join.  Short sequences are bound by the chain of loads
-// before the first product and by what one compute unit draws: 513 tokens 8.7 us.
+// before the first product and by what one compute unit draws: 513 tokens 8.8 us.
 #include "attend.h"
 
 namespace q8k {
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     // the keys' registers are loaded again as soon as the scores are there, the
     // values' as soon as the second product is.
     // The codes are read once, which the loads say (non-temporal: 8 x 65537
-    // tokens at 6.1 TB/s, 5.4 without).
+    // tokens at 6.1 TB/s and 5.4 without, when this was chosen; 6.4 now).
     // Reads go through a buffer descriptor of one record; a page that selects
     // nothing has an empty one, whose reads return zeros and touch no memory.
     uint4 kraw[4][KS / 2], vraw[DB];
@@ -421,7 +421,12 @@ hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
 // smaller ones measured slower (each has its queries to bring and its results
 // to join), fewer leave units idle where lengths differ.  A call that has
 // several times as many tiles is not split, nor is one of more sequences than
-// the workgroups care to look through.
+// the workgroups care to look through: of lengths spread from a tenth to the
+// longest (8 query heads over one), 64 of up to 8191 tokens take 26 us in chunks
+// and 48 whole, 256 of up to 4000 take 50 and 38, 512 of them 113 and 64, of up to
+// 16000 272 and 216.  What the limit gives away is a sequence far longer than the
+// rest: 65537 tokens among 255 of up to 2000 take 50 us, among 256 of them, whole,
+// 412 (in chunks 52).
 constexpr int64_t TARGET_WGS = 512;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
 // A chunk has at least this many pages (4096 tokens of one sequence: 15.6 us;
@@ -441,7 +446,10 @@ constexpr int64_t UNSPLIT_PAGES = 32, UNSPLIT_PAGES_256 = 24;
 constexpr int64_t FOUR_SLICES_TO = 64, TWO_SLICES_TO = 128;
 // Where one workgroup a compute unit is all there is, it has eight waves if there are
 // pages for them (12 sequences of 1000 tokens, five tokens each: 12.3 us, of
-// four waves 13.6); where there are more, four (64 x 2000: 36 us, of eight 43).
+// four waves 13.6; 24 of 500: 13.2 and 11.8, of 640 13.8 and 13.4, of 768 and up
+// within 3% of each other; heads of 64 values, 640: 9.9 and 10.2, 832: 11.1 and
+// 11.7, 1500: 13.9 and 15.6); where there are more, four (64 x 2000: 36 us, of
+// eight 43).
 constexpr int64_t EIGHT_WAVES_TO = 256, EIGHT_WAVES_FROM_PAGES = 13;
 // Rows of one key head by the sixteen, each 16 with the whole cache before
 // them, or by the 64 or 128 that share a page's conversion but leave compute

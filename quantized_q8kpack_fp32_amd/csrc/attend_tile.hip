@@ -2,14 +2,17 @@
 // them.  The formula of attend_decode.hip; here the arithmetic bounds it, so the
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
-// Three chunks of 1000 tokens over up to 16001 (32 heads of 128 over 4, bf16,
-// turned): 790 us, 584 TFLOP/s of the formula's, where a large matrix product
-// reaches 1140.  A query of two fp16 pieces makes the first product twice as long
-// as the formula's, so that the matrix work alone would take 607 us at that rate;
-// matrix instructions are busy for 36% of the cycles and vector ones (some twelve a
-// score) for 43%, and little of the two overlaps, neither from wave to wave nor
-// where the instructions are put between each other.  756 tiles on 512 places
-// leave the last round unfilled: four of 1024 over 8192 reach 674.
+// Chunks of up to 1000 tokens of three prompts over up to 16001 (32 heads of 128
+// over 4, bf16, turned): 802 us, 575 TFLOP/s of the formula's, where a large matrix
+// product reaches 1140.  A query of two fp16 pieces makes the first product twice as
+// long as the formula's, so that the matrix work alone would take 607 us at that
+// rate; matrix instructions are busy for 36% of the cycles and vector ones (some
+// twelve a score) for 41%, and little of the two overlaps: each wave does a page's
+// scores, probabilities and values in turn, and the waves of a unit are in the same
+// phase behind one barrier a page (scheduling groups that put the instructions
+// between each other, and wave priorities, gained nothing).  The 1000, 443 and 787
+// tokens make 564 tiles with work, of unequal length, on 512 places, the longest
+// first; four of 1024 over 8192, 1024 tiles of nearly one length, reach 695.
 #include "attend.h"
 
 namespace q8k {
@@ -42,8 +45,8 @@ struct PageOps {
 // on its way from memory: one barrier a page.  HALVES == 2: as many waves again
 // take every other page, with buffers of their own, and the two results are
 // joined through LDS: for calls of few short tiles, where a tile's own time
-// counts (512 tokens of one prompt, 32 heads of 128 over 8: 21.6 us, 24.3 with
-// one half; tiles that are split into chunks lose by it: 500 tokens over 16001
+// counts (512 tokens of one prompt, 32 heads of 128 over 8: 21.6 us when this was
+// chosen and 24.3 with one half, 19.8 now; tiles that are split into chunks lose by it: 500 tokens over 16001
 // 283 us, 275).
 template <int D, int WAVES, int HALVES, int RT, int NQ, int NP>
 __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) void attend_tile_kernel(Attend a) {

@@ -7,10 +7,10 @@
 // scale a token (not a page): an append touches no other token's codes, so
 // tokens appended one by one and in one call leave the same bytes.
 //
-// Bound by bytes: 4 D or 8 D a token and head in, 2 D + 8 out (8191 tokens of 8
-// heads of 128, bf16: 51 MB in 17.5 us, 2.9 TB/s; the read back 14.8 us, 3.4
-// TB/s), and for few tokens by the launch and the slot's, the row's and the
-// table's loads (one token 2.6 us, its read back 2.1).
+// Bound by bytes and by how they are cut: 4 D or 8 D a token and head in, 2 D + 8
+// out (8191 tokens of 8 heads of 128, bf16: 51 MB in 17.7 us, 2.9 TB/s; the read
+// back 14.7 us, 3.5 TB/s), and for few tokens by the launch and the slot's, the row's
+// and the table's loads (one token 2.7 us, its read back 2.1).
 #include "kv_cache.h"
 #include "q8k_launch.h"
 
@@ -73,11 +73,15 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppend a) {
 // Many tokens: one workgroup takes 32 tokens of one head.  Keys go as above.
 // The values' codes first meet in LDS.  Four tokens that follow each other from
 // a multiple of four on have places that follow each other, and a wave then
-// stores the four codes of eight such groups to four rows of places at a time, 32
-// consecutive bytes of each; the tokens that are left (a run's ends, or slots
-// in no order) go byte by byte.  8191 tokens of 8 heads of 128, bf16, take 17.5 us
-// for the simple form's 49; tiles of 64 tokens take as long there, and longer
-// where tokens are fewer.
+// stores the four codes of eight such groups to four rows of places at a time: of
+// 32 tokens that begin at a multiple of 32, four pieces of eight consecutive bytes
+// of each row.  The tokens that are left (a run's ends, or slots in no order) go byte
+// by byte.  Tiles are cut by the call's order and not by pages: a run that begins in
+// the middle of four has such tokens in every tile (1024 tokens of 8 heads of 128,
+// bf16: 6.6 us, from the start of a page 5.8), and a page's values, 64 D consecutive
+// bytes, are written by two or three workgroups.  8191 tokens take 17.7 us for the
+// simple form's 49; tiles of 64 tokens, cut the same way, take as long there, and
+// longer where tokens are fewer.
 constexpr int TILE = 32, FOURS = TILE / 4;
 // Tokens of a tile (lane t: token t's slot, -1: none) that begin a group of
 // four, and those in none.
@@ -325,8 +329,14 @@ __global__ __launch_bounds__(256) void kv_read_tile_kernel(KvRead a) {
     }
 }
 
-// Tokens times heads from which on the tiles take less time (512 x 8: 10.8 us
-// with the read back, 12.1 the simple form; 256 x 8: 10.7 and 9.8).
+// Tokens times heads from which on the tiles take less time where slots run on:
+// appends of 512 tokens of 8 heads of 128, fp32, take 6.6 us, 7.5 in the simple
+// form, 256 tokens 6.0 and 4.9; heads of 64, bf16, 512: 4.1 and 4.8; heads of 256,
+// fp32, 512: 10.6 and 14.7.  A step of many sequences has its slots apart, one a
+// page, and every value code goes by itself either way: 61 tokens (simple) 4.2 us,
+// 512 of 8 heads of 128, fp32, 19.6 in tiles and 17.7 in the simple form, bf16 17.7
+// and 16.0, 1024 39.8 both, 2048 73.5 and 75.2, heads of 64 7.9 and 6.9, of 256 43.3
+// and 44.6.  The host does not know the slots, so the rule goes by the runs.
 constexpr int64_t TILE_FROM_ROWS = 4096;
 
 template <int D>
