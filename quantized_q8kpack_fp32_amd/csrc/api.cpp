@@ -51,6 +51,14 @@ int check_grid(const char* fn, int64_t workgroups) {
     return Q8K_OK;
 }
 
+// A launch counts its threads in 32 bits.
+int check_threads(const char* fn, int64_t workgroups, int64_t threads) {
+    if (workgroups > (int64_t)0xffffffff / threads)
+        return fail(Q8K_ERR_SHAPE, "%s: problem needs %lld workgroups of %lld threads (fewer than 2^32 threads in all)",
+                    fn, (long long)workgroups, (long long)threads);
+    return Q8K_OK;
+}
+
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 int check_k(const char* fn, int64_t K) {
@@ -528,6 +536,7 @@ int q8k_kv_append(int dtype, const void* k, int64_t k_stride, const void* v, int
                kv->kv_heads, dtype};
     Q8K_TRY(check_rope(fn, rope, pos, kv->head_dim, &a.rope));
     Q8K_TRY(check_grid(fn, (2 * T * row + 2047) / 2048));
+    Q8K_TRY(check_threads(fn, kv_workgroups(T, kv->kv_heads), 256));
     if (T == 0 || kv->pages == 0) return Q8K_OK;
     return launched(fn, launch_kv_append(kv->head_dim, a, (hipStream_t)stream));
 }
@@ -542,6 +551,7 @@ int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t
     Q8K_TRY(check_ptr(fn, "k", k, 16));
     Q8K_TRY(check_ptr(fn, "v", v, 16));
     Q8K_TRY(check_grid(fn, (T * kv->kv_heads * kv->head_dim + 2047) / 2048));
+    Q8K_TRY(check_threads(fn, kv_workgroups(T, kv->kv_heads), 256));
     if (T == 0) return Q8K_OK;
     const KvRead a{static_cast<const uint8_t*>(kv->data), kv->pages, kv->kv_heads, dtype, slots, T, k, v};
     return launched(fn, launch_kv_read(kv->head_dim, a, (hipStream_t)stream));
@@ -602,6 +612,7 @@ int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q
     const AttendPlan p = attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, window);
     const int64_t group = q_heads / kv->kv_heads;
     Q8K_TRY(check_grid(fn, p.items * kv->kv_heads));
+    Q8K_TRY(check_threads(fn, p.items * kv->kv_heads * p.slices, p.threads));
     a.q = q;
     a.q_stride = q_stride;
     a.q_heads = (int)q_heads;
@@ -660,6 +671,7 @@ int qlogprobs(int dtype, const void* logits, int64_t stride, int64_t T, int64_t 
         return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
     Q8K_TRY(check_grid(fn, T * ((V + 1023) / 1024)));
+    Q8K_TRY(check_threads(fn, T, logprobs_threads(T, V)));
     if (T == 0) return Q8K_OK;
     const LogProbs a{logits, stride, T, V, dtype, targets, logprob, entropy, lse, topn, top_ids, top_logprob};
     return launched(fn, launch_logprobs(a, ws, (hipStream_t)stream));

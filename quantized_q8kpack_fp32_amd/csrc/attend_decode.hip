@@ -498,11 +498,13 @@ static AttendPlan plan_for(int64_t B, int64_t max_q, int64_t max_len, int q_head
         p.items = tiles + p.target < most ? tiles + p.target : most;
     }
     const int64_t wgs = p.items * heads;
-    p.slices = wgs <= FOUR_SLICES_TO && D > 64 ? 4 : wgs <= TWO_SLICES_TO ? 2 : 1;
+    p.slices = p.tiles ? 1 : wgs <= FOUR_SLICES_TO && D > 64 ? 4 : wgs <= TWO_SLICES_TO ? 2 : 1;
     // finding the longest takes a workgroup up to 1 us (58 sequences of 513 tokens,
     // eight new ones each: 30.6 us, 35.0 ordered; 64 of 8191, 16 each: 287 and 251)
     p.order = !p.split && B > 1 && B <= 64 && (p.tiles || live > UNSPLIT_PAGES);
     p.waves = D < 256 && p.slices == 1 && wgs <= EIGHT_WAVES_TO && !p.split && live >= EIGHT_WAVES_FROM_PAGES ? 8 : 4;
+    // (decode_d, tile_d: two halves or eight waves of a tile)
+    p.threads = !p.tiles ? 64 * p.waves : (p.tile_rows == ATTEND_TILE_FEW ? D < 256 && !p.split : D == 256) ? 512 : 256;
     p.ws_bytes = 0;
     if (p.split) {
         const int64_t parts = p.items * heads * p.tile_rows;

@@ -342,7 +342,7 @@ constexpr int64_t TILE_FROM_ROWS = 4096;
 template <int D>
 hipError_t append_d(const KvAppend& a, hipStream_t s) {
     if (a.T * a.heads >= TILE_FROM_ROWS) {
-        Q8K_LAUNCH((kv_append_tile_kernel<D>), dim3((unsigned)((a.T + TILE - 1) / TILE * a.heads)), dim3(256), 0, s, a);
+        Q8K_LAUNCH((kv_append_tile_kernel<D>), dim3((unsigned)kv_workgroups(a.T, a.heads)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     const int64_t rows = a.T * 2 * a.heads, per = 256 / (D / 8);
@@ -352,7 +352,7 @@ hipError_t append_d(const KvAppend& a, hipStream_t s) {
 template <int D>
 hipError_t read_d(const KvRead& a, hipStream_t s) {
     if (a.T * a.heads >= TILE_FROM_ROWS) {
-        Q8K_LAUNCH((kv_read_tile_kernel<D>), dim3((unsigned)((a.T + TILE - 1) / TILE * a.heads)), dim3(256), 0, s, a);
+        Q8K_LAUNCH((kv_read_tile_kernel<D>), dim3((unsigned)kv_workgroups(a.T, a.heads)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     const int64_t rows = a.T * a.heads, per = 256 / (D / 8);
@@ -361,6 +361,8 @@ hipError_t read_d(const KvRead& a, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t kv_workgroups(int64_t T, int64_t heads) { return (T + TILE - 1) / TILE * heads; }
 
 hipError_t launch_kv_append(int D, const KvAppend& a, hipStream_t s) {
     return D == 64 ? append_d<64>(a, s) : D == 128 ? append_d<128>(a, s) : append_d<256>(a, s);

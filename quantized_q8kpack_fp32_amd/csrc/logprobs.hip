@@ -449,13 +449,16 @@ Parts parts_of(void* ws, int64_t T, int64_t V) {
     return p;
 }
 
+// Threads that hold a row of V logits in one round, if 256 do, else 1024.
+int threads_of(int64_t V) { return V <= 256 * PER ? 256 : 1024; }
+
 template <int DT>
 hipError_t logprobs_dt(const LogProbs& a, void* ws, hipStream_t s) {
     const Parts p = parts_of(ws, a.T, a.V);
     if (p.parts > 1) {
         Q8K_LAUNCH((logprobs_kernel<DT, 1024, true>), dim3((unsigned)(a.T * p.parts)), dim3(1024), 0, s, a, p);
         Q8K_LAUNCH(logprobs_join_kernel<DT>, dim3((unsigned)a.T), dim3(64), 0, s, a, p);
-    } else if (a.V <= 256 * PER) {  // a row that 256 threads hold in one round
+    } else if (threads_of(a.V) == 256) {
         Q8K_LAUNCH((logprobs_kernel<DT, 256, false>), dim3((unsigned)a.T), dim3(256), 0, s, a, p);
     } else {
         Q8K_LAUNCH((logprobs_kernel<DT, 1024, false>), dim3((unsigned)a.T), dim3(1024), 0, s, a, p);
@@ -469,6 +472,8 @@ int64_t logprobs_ws_bytes(int64_t T, int64_t V, int topn) {
     const Parts p = parts_of(nullptr, T, V);
     return p.parts > 1 ? align256((int64_t)sizeof(Sums) * T * p.parts) + 8 * T * p.parts * topn : 0;
 }
+
+int64_t logprobs_threads(int64_t T, int64_t V) { return (int64_t)parts_of(nullptr, T, V).parts * threads_of(V); }
 
 hipError_t launch_logprobs(const LogProbs& a, void* ws, hipStream_t s) {
     return a.dtype == DT_F32   ? logprobs_dt<DT_F32>(a, ws, s)

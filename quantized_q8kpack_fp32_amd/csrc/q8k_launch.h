@@ -185,6 +185,7 @@ struct KvRead {
     void* v;
 };
 hipError_t launch_kv_read(int D, const KvRead& a, hipStream_t s);
+int64_t kv_workgroups(int64_t T, int64_t heads);  // of 256 threads that a call of many tokens takes
 
 // Attention.  A key head's q_heads / heads query heads of a sequence's new
 // tokens are its rows: row r is token r / group, head h * group + r % group.
@@ -225,6 +226,7 @@ struct AttendPlan {
     bool order;  // else: the longest sequence's tiles first
     int tile_rows, tiles_max, least, target;
     int waves, slices;  // of the 16-row kernel
+    int threads;        // of a workgroup
     int64_t items, ws_bytes;
 };
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
@@ -247,6 +249,7 @@ struct LogProbs {
     float* top_logprob;
 };
 int64_t logprobs_ws_bytes(int64_t T, int64_t V, int topn);
+int64_t logprobs_threads(int64_t T, int64_t V);  // a row's, over all its workgroups
 hipError_t launch_logprobs(const LogProbs& a, void* ws, hipStream_t s);
 
 // ---- test support: the shipped kernels' integer sums (template flags of the
