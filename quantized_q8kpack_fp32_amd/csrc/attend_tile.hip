@@ -46,8 +46,10 @@ struct PageOps {
 // take every other page, with buffers of their own, and the two results are
 // joined through LDS: for calls of few short tiles, where a tile's own time
 // counts (512 tokens of one prompt, 32 heads of 128 over 8: 21.6 us when this was
-// chosen and 24.3 with one half, 19.8 now; tiles that are split into chunks lose by it: 500 tokens over 16001
-// 283 us, 275).
+// chosen and 24.3 with one half, 19.8 now; tiles that are split into chunks lose
+// by it: 500 tokens over 16001 283 us, 275).  Heads of 64 values in 128-row tiles
+// keep to the registers of three waves a SIMD (chunks of 1000 over 8000: 230 us, of
+// two waves 300).
 template <int D, int WAVES, int HALVES, int RT, int NQ, int NP>
 __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) void attend_tile_kernel(Attend a) {
     constexpr int KS = D / 32, DB = D / 16, ROWS = 16 * RT * WAVES;
