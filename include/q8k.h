@@ -360,6 +360,95 @@ int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q
             const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
             const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* -------------------------------------------------------- long contexts --
+ * The cache in 4 bits, and what keeps a cache short.
+ *
+ * The 4-bit cache is a q8k_kv_cache too (the calls that take both are told by
+ * `bits`, 8 or 4; a cache is read in the bits it was written in): pages of
+ * Q8K_KV_PAGE tokens, q8k_kv4_bytes(...) bytes, D/2 + D/32 + 4 a key or value of D =
+ * head_dim values.  A key's or value's row of one head is cut into groups of 32:
+ *   scale = amax / 7 of the row, fp32;
+ *   factor of a group = the least 8-bit float (four exponent and four mantissa bits:
+ *       the fp16 whose bits are the byte << 6; 0 to 1, 2^-14 the least normal one,
+ *       steps of 2^-18 below) that is not below the group's amax / the row's;
+ *   code = round-half-even(x * (1 / (factor * scale))), -7 to 7;
+ * every quotient, product and rounding in fp32.  A value reads back as (code *
+ * factor) * scale, the first product exact: within half of factor * scale.  Where 1 /
+ * (factor * scale) overflows, nonzero values have code 7 or -7.  NaN and infinities: as
+ * in the 8-bit cache (a NaN reads back as 0, beside an infinity all are NaN).
+ * For each (page, head) a record of 68 * D + 512 bytes:
+ *   key codes     [D/32][16][4][2][8 bytes]    block i, token % 16, quarter h, piece 2 i + b:
+ *       piece p is of tokens 16 (p / (D/64)) and on, values 64 (p % (D/64)) + 16 h and on,
+ *       two words of eight; code + 8 of a word's value j at its bits from
+ *       4 (j/2 + 4 (j%2)) + 2 on, round the word's end
+ *   value codes   [D/32][16][64 places]        values 32 e + c (low half of the byte) and
+ *       32 e + 16 + c, code + 8; token t at place (t>>2 & 3) << 4 | (t>>5) << 3 |
+ *       (t>>4 & 1) << 2 | (t & 1) << 1 | (t>>1 & 1)
+ *   key factors   [16][2][4][D/64]             token % 16, group % 2, token / 16, group / 2
+ *   value factors [D/32][64 places]
+ *   fp32 key scales [64 tokens], fp32 value scales [64 tokens]. */
+size_t q8k_kv4_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim); /* 0 on a bad shape */
+
+/* q8k_kv4_append, q8k_kv4_read, qattend_kv4: q8k_kv_append, q8k_kv_read and qattend
+ * on the 4-bit cache; arguments, rules and limits are theirs.  (qattend's limits of
+ * a value's magnitude are those of the row's scale times 7.) */
+int q8k_kv4_append(int dtype, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+                   const int32_t* pos, const q8k_rope* rope, const int32_t* slots, const q8k_kv_cache* kv,
+                   void* stream);
+int q8k_kv4_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T, void* k, void* v, void* stream);
+size_t qattend_kv4_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                                   int64_t max_len);
+int qattend_kv4(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
+                const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table, int64_t max_pages,
+                const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
+                const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* qattend_weights: the attention that each cached token of a sequence gets from its
+ * new tokens, added up over them and the query heads of a key head, beside what it got
+ * before:
+ *   weights[b][h][j] = keep * old[b][h][j] + sum over new tokens i that see j and query
+ *                      heads a of key head h of e^(s_j - lse[i][a])
+ * for the tokens j < len, s_j as in qattend.  Arguments up to rope: qattend's, over a
+ * cache of `bits` 8 or 4.  lse fp32 [Tq][q_heads]: what attention returned for these
+ * rows (a row of -inf adds nothing).
+ * old, weights: rows of at least max_len fp32, one for each sequence and key head [B]
+ * [kv_heads], w_stride elements apart; they may be the same.  old NULL: none.  old is
+ * not read for the new tokens, which have got nothing before, nor from len on; weights
+ * is not written from len on.  keep: finite.  A token on a page outside [0, pages) gets
+ * nothing.  s_j - lse enters the exponential in fp32: scores and lse below 2^20.
+ * The sums are taken in a fixed order.  ws / ws_bytes: as qattend's. */
+size_t qattend_weights_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                                       int64_t max_len);
+int qattend_weights(int dtype, int bits, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv,
+                    int64_t B, const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table,
+                    int64_t max_pages, const int32_t* kv_len, int64_t max_len, float scale, int64_t window,
+                    const int32_t* pos, const q8k_rope* rope, const float* lse, const float* old, float keep,
+                    float* weights, int64_t w_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* q8k_kv_evict: cuts sequences to `budget` tokens.  Of one that is longer, each key
+ * head by itself keeps its first `first` and last `last` tokens (first + last <=
+ * budget) and, of those between, the ones of the largest weights: equal weights by
+ * ascending index, NaN below every number.  The kept tokens move, in order, to places
+ * 0 .. budget - 1 of the sequence's new pages, as they are (keys stay turned by the
+ * positions they were appended with); a sequence that is no longer than budget keeps
+ * all of its tokens.
+ * kv, bits: a cache of 8 or 4 bits.  page_table, max_pages, kv_len, max_len: as
+ * qattend's.  weights: as qattend_weights', rows w_stride apart.
+ * out_table int32 [B][out_pages], budget <= 64 * out_pages: the new pages.  The same
+ * table (the same address): the move is in place, and the pages of the sequences must
+ * be theirs alone; else no new page may be a page that page_table names or another new
+ * page.  A token on a page outside [0, pages) of page_table arrives as zeros; one for
+ * such a page of out_table is not written.  Nothing else of the cache changes.
+ * out_weights: NULL, or rows of at least budget fp32, out_stride apart, for the kept
+ * tokens' weights; may be weights with its stride, else apart from it.
+ * kept int32 [B][kv_heads][budget]: the kept tokens' old indices, ascending, then -1.
+ * new_len int32 [B]: min(kv_len, budget); apart from kv_len.
+ * out_weights is not written behind a sequence's kept tokens. */
+int q8k_kv_evict(int bits, const q8k_kv_cache* kv, int64_t B, const int32_t* page_table, int64_t max_pages,
+                 const int32_t* kv_len, int64_t max_len, const float* weights, int64_t w_stride, int64_t budget,
+                 int64_t first, int64_t last, const int32_t* out_table, int64_t out_pages, float* out_weights,
+                 int64_t out_stride, int32_t* kept, int32_t* new_len, void* stream);
+
 /* qlogprobs: of each of T rows of V logits (stride elements apart, any
  * alignment of whole elements; 1 <= V <= 2^20)
  *   lse = log sum_i e^(x_i),  logprob = x[target] - lse,

@@ -22,7 +22,9 @@ __all__ = [
     "qmatmul_prefill_moe_workspace_bytes", "qmatmul_prefill_moe", "qmatmul_prefill_moe_noalloc",
     "Q8K_NOALLOC_SCRATCH_BYTES", "Q8K_F32", "Q8K_F16", "Q8K_BF16", "Q8K_KV_PAGE", "Q8K_TOP_MAX", "Q8K_ROPE_HALF",
     "Q8K_ROPE_ADJACENT", "KVCache", "Rope", "q8k_kv_bytes", "q8k_kv_append", "q8k_kv_read", "qattend_workspace_bytes",
-    "qattend", "qlogprobs_workspace_bytes", "qlogprobs", "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
+    "qattend", "qlogprobs_workspace_bytes", "qlogprobs", "q8k_kv4_bytes", "q8k_kv4_append", "q8k_kv4_read",
+    "qattend_kv4_workspace_bytes", "qattend_kv4", "qattend_weights_workspace_bytes", "qattend_weights", "q8k_kv_evict",
+    "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
     "q8k_debug_wave_sums", "q8k_debug_last_launches", "q8k_status_str", "q8k_last_error", "EXPORTED",
 ]
 
@@ -51,7 +53,9 @@ EXPORTED = (
     "qmatmul_prefill_f32_workspace_bytes", "qmatmul_prefill_f32",
     "qmatmul_prefill_moe_workspace_bytes", "qmatmul_prefill_moe", "qmatmul_prefill_moe_noalloc",
     "q8k_kv_bytes", "q8k_kv_append", "q8k_kv_read", "qattend_workspace_bytes", "qattend", "qlogprobs_workspace_bytes",
-    "qlogprobs", "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
+    "qlogprobs", "q8k_kv4_bytes", "q8k_kv4_append", "q8k_kv4_read", "qattend_kv4_workspace_bytes", "qattend_kv4",
+    "qattend_weights_workspace_bytes", "qattend_weights", "q8k_kv_evict",
+    "q8k_debug_subblock_sums", "q8k_debug_prefill_block_sums", "q8k_debug_moe_subblock_sums",
     "q8k_debug_wave_sums", "q8k_debug_last_launches", "q8k_status_str", "q8k_last_error",
 )
 
@@ -131,6 +135,24 @@ lib.qlogprobs_workspace_bytes.restype = _SZ
 lib.qlogprobs_workspace_bytes.argtypes = [_I64, _I64, ctypes.c_int32]
 lib.qlogprobs.restype = _INT
 lib.qlogprobs.argtypes = [_INT, _P, _I64, _I64, _I64, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _SZ, _P]
+lib.q8k_kv4_bytes.restype = _SZ
+lib.q8k_kv4_bytes.argtypes = lib.q8k_kv_bytes.argtypes
+lib.q8k_kv4_append.restype = _INT
+lib.q8k_kv4_append.argtypes = lib.q8k_kv_append.argtypes
+lib.q8k_kv4_read.restype = _INT
+lib.q8k_kv4_read.argtypes = lib.q8k_kv_read.argtypes
+lib.qattend_kv4_workspace_bytes.restype = _SZ
+lib.qattend_kv4_workspace_bytes.argtypes = lib.qattend_workspace_bytes.argtypes
+lib.qattend_kv4.restype = _INT
+lib.qattend_kv4.argtypes = lib.qattend.argtypes
+lib.qattend_weights_workspace_bytes.restype = _SZ
+lib.qattend_weights_workspace_bytes.argtypes = lib.qattend_workspace_bytes.argtypes
+lib.qattend_weights.restype = _INT
+lib.qattend_weights.argtypes = [_INT, _INT, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, ctypes.c_float,
+                                _I64, _P, _P, _P, _P, ctypes.c_float, _P, _I64, _P, _SZ, _P]
+lib.q8k_kv_evict.restype = _INT
+lib.q8k_kv_evict.argtypes = [_INT, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P,
+                             _P]
 lib.q8k_debug_subblock_sums.restype = _INT
 lib.q8k_debug_subblock_sums.argtypes = [_INT, _P, _I64, _I64, _P, _P, _P, _P]
 lib.q8k_debug_prefill_block_sums.restype = _INT
@@ -361,15 +383,17 @@ _TYPES = {Q8K_F32: torch.float32, Q8K_F16: torch.float16, Q8K_BF16: torch.bfloat
 
 
 class KVCache:
-    """A paged 8-bit key/value cache (q8k_kv_cache): ``data`` is a device buffer of
-    ``q8k_kv_bytes(pages, kv_heads, head_dim)`` bytes, kept alive by this object."""
+    """A paged key/value cache (q8k_kv_cache): ``data`` is a device buffer of ``q8k_kv_bytes(pages, kv_heads, head_dim)``
+    bytes, or of ``q8k_kv4_bytes(...)`` with ``bits=4``, kept alive by this object."""
 
-    def __init__(self, data, pages: int, kv_heads: int, head_dim: int):
-        need = q8k_kv_bytes(pages, kv_heads, head_dim)
+    def __init__(self, data, pages: int, kv_heads: int, head_dim: int, bits: int = 8):
+        if bits not in (8, 4):
+            raise ValueError(f"a cache is held in 8 or 4 bits, not {bits}")
+        need = (q8k_kv_bytes if bits == 8 else q8k_kv4_bytes)(pages, kv_heads, head_dim)
         if not isinstance(data, int) and data is not None:
             if not data.is_contiguous() or data.numel() * data.element_size() < need:
                 raise ValueError(f"a cache of {pages} pages, {kv_heads} heads of {head_dim} is {need} contiguous bytes")
-        self.data, self.pages, self.kv_heads, self.head_dim = data, pages, kv_heads, head_dim
+        self.data, self.pages, self.kv_heads, self.head_dim, self.bits = data, pages, kv_heads, head_dim, bits
         self.device = data.get_device() if isinstance(data, torch.Tensor) else None
         self.struct = _KVStruct(_ptr(data), pages, kv_heads, head_dim)
         self.ref = ctypes.addressof(self.struct)
@@ -389,7 +413,9 @@ class Rope:
         self.ref = ctypes.addressof(self.struct)
 
 
-def _kv(dev, kv):
+def _kv(dev, kv, bits=8):
+    if kv.bits != bits:
+        raise ValueError(f"the call takes a cache of {bits} bits, kv is one of {kv.bits}")
     if kv.device != dev and kv.device is not None:
         _refuse(dev, "kv", kv.data, None)
     return kv.ref
@@ -407,39 +433,112 @@ def q8k_kv_bytes(pages: int, kv_heads: int, head_dim: int) -> int:
     return int(lib.q8k_kv_bytes(pages, kv_heads, head_dim))
 
 
-def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
+def q8k_kv4_bytes(pages: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.q8k_kv4_bytes(pages, kv_heads, head_dim))
+
+
+def _append(call, bits, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream):
     dev, t = _device(), _TYPES.get(dtype)
     row = kv.kv_heads * kv.head_dim
-    _check(lib.q8k_kv_append(dtype, _rows(dev, "k", k, t, T, k_stride, row), k_stride,
-                             _rows(dev, "v", v, t, T, v_stride, row), v_stride, T,
-                             _flat(dev, "pos", pos, torch.int32, 0 if rope is None else T), _rope(dev, rope),
-                             _flat(dev, "slots", slots, torch.int32, T), _kv(dev, kv), _stream_of(dev, stream)))
+    _check(call(dtype, _rows(dev, "k", k, t, T, k_stride, row), k_stride,
+                _rows(dev, "v", v, t, T, v_stride, row), v_stride, T,
+                _flat(dev, "pos", pos, torch.int32, 0 if rope is None else T), _rope(dev, rope),
+                _flat(dev, "slots", slots, torch.int32, T), _kv(dev, kv, bits), _stream_of(dev, stream)))
+
+
+def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
+    _append(lib.q8k_kv_append, 8, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream)
+
+
+def q8k_kv4_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
+    _append(lib.q8k_kv4_append, 4, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream)
+
+
+def _read(call, bits, dtype, kv, slots, T, k, v, stream):
+    dev, t = _device(), _TYPES.get(dtype)
+    n = T * kv.kv_heads * kv.head_dim
+    _check(call(dtype, _kv(dev, kv, bits), _flat(dev, "slots", slots, torch.int32, T), T, _flat(dev, "k", k, t, n),
+                _flat(dev, "v", v, t, n), _stream_of(dev, stream)))
 
 
 def q8k_kv_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
-    dev, t = _device(), _TYPES.get(dtype)
-    n = T * kv.kv_heads * kv.head_dim
-    _check(lib.q8k_kv_read(dtype, _kv(dev, kv), _flat(dev, "slots", slots, torch.int32, T), T, _flat(dev, "k", k, t, n),
-                           _flat(dev, "v", v, t, n), _stream_of(dev, stream)))
+    _read(lib.q8k_kv_read, 8, dtype, kv, slots, T, k, v, stream)
+
+
+def q8k_kv4_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
+    _read(lib.q8k_kv4_read, 4, dtype, kv, slots, T, k, v, stream)
 
 
 def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
     return int(lib.qattend_workspace_bytes(kv.ref, q_heads, B, Tq, max_q, max_len))
 
 
-def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
-            max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
-            ws_bytes: int = 0, stream=None) -> None:
+def qattend_kv4_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
+    return int(lib.qattend_kv4_workspace_bytes(kv.ref, q_heads, B, Tq, max_q, max_len))
+
+
+def _attend(call, bits, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len, max_len,
+            scale, window, pos, rope, out, lse, ws, ws_bytes, stream):
     dev, t = _device(), _TYPES.get(dtype)
     i32 = torch.int32
     row = q_heads * kv.head_dim
-    _check(lib.qattend(dtype, _rows(dev, "q", q, t, Tq, q_stride, row), q_stride, q_heads, _kv(dev, kv), B,
-                       _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
-                       _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
-                       _flat(dev, "kv_len", kv_len, i32, B), max_len, scale, window,
-                       _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
-                       _flat(dev, "out", out, t, Tq * row), _flat(dev, "lse", lse, torch.float32, Tq * q_heads),
-                       _bytes(dev, "ws", ws, ws_bytes), ws_bytes, _stream_of(dev, stream)))
+    _check(call(dtype, _rows(dev, "q", q, t, Tq, q_stride, row), q_stride, q_heads, _kv(dev, kv, bits), B,
+                _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
+                _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+                _flat(dev, "kv_len", kv_len, i32, B), max_len, scale, window,
+                _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
+                _flat(dev, "out", out, t, Tq * row), _flat(dev, "lse", lse, torch.float32, Tq * q_heads),
+                _bytes(dev, "ws", ws, ws_bytes), ws_bytes, _stream_of(dev, stream)))
+
+
+def qattend_kv4(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
+                max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
+                ws_bytes: int = 0, stream=None) -> None:
+    _attend(lib.qattend_kv4, 4, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len, max_len,
+            scale, window, pos, rope, out, lse, ws, ws_bytes, stream)
+
+
+def qattend_weights_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
+    return int(lib.qattend_weights_workspace_bytes(kv.ref, q_heads, B, Tq, max_q, max_len))
+
+
+def qattend_weights(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
+                    max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, lse, old, keep: float,
+                    weights, w_stride: int, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    """The C call without ``bits``, which ``kv`` knows."""
+    dev, t = _device(), _TYPES.get(dtype)
+    i32, f32 = torch.int32, torch.float32
+    rows = B * kv.kv_heads
+    _check(lib.qattend_weights(
+        dtype, kv.bits, _rows(dev, "q", q, t, Tq, q_stride, q_heads * kv.head_dim), q_stride, q_heads,
+        _kv(dev, kv, kv.bits), B, _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
+        _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages, _flat(dev, "kv_len", kv_len, i32, B),
+        max_len, scale, window, _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
+        _flat(dev, "lse", lse, f32, Tq * q_heads), _rows(dev, "old", old, f32, rows, w_stride, max_len), keep,
+        _rows(dev, "weights", weights, f32, rows, w_stride, max_len), w_stride, _bytes(dev, "ws", ws, ws_bytes), ws_bytes,
+        _stream_of(dev, stream)))
+
+
+def q8k_kv_evict(kv, B: int, page_table, max_pages: int, kv_len, max_len: int, weights, w_stride: int, budget: int,
+                 first: int, last: int, out_table, out_pages: int, out_weights, out_stride: int, kept, new_len,
+                 stream=None) -> None:
+    """The C call without ``bits``, which ``kv`` knows."""
+    dev = _device()
+    i32, f32 = torch.int32, torch.float32
+    rows = B * kv.kv_heads
+    _check(lib.q8k_kv_evict(
+        kv.bits, _kv(dev, kv, kv.bits), B, _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+        _flat(dev, "kv_len", kv_len, i32, B), max_len, _rows(dev, "weights", weights, f32, rows, w_stride, max_len),
+        w_stride, budget, first, last, _flat(dev, "out_table", out_table, i32, B * out_pages), out_pages,
+        _rows(dev, "out_weights", out_weights, f32, rows, out_stride, budget), out_stride,
+        _flat(dev, "kept", kept, i32, rows * budget), _flat(dev, "new_len", new_len, i32, B), _stream_of(dev, stream)))
+
+
+def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
+            max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
+            ws_bytes: int = 0, stream=None) -> None:
+    _attend(lib.qattend, 8, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len, max_len,
+            scale, window, pos, rope, out, lse, ws, ws_bytes, stream)
 
 
 def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:

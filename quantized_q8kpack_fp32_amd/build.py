@@ -24,7 +24,8 @@ OUT = os.path.join(HERE, "libq8k.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "pack.hip", "matvec.hip", "moe.hip", "moe_mfma.hip", "prefill.hip", "prefill_regw.hip", "kv.hip",
-           "attend_decode.hip", "attend_tile.hip", "logprobs.hip"]
+           "attend_decode.hip", "attend_tile.hip", "logprobs.hip", "kv4.hip",
+           "attend_weights.hip", "kv_evict.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "-x", "hip", "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -8,7 +8,7 @@
 #include <stdio.h>
 
 #include "../../include/q8k.h"
-#include "q8k_device.h"
+#include "kv4_cache.h"
 #include "q8k_launch.h"
 
 using namespace q8k;
@@ -511,18 +511,21 @@ static int check_stride(const char* fn, const char* what, int64_t stride, int64_
     return Q8K_OK;
 }
 
-size_t q8k_kv_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim) {
+// The calls of the caches of 8 and of 4 bits differ in the record alone.
+static size_t kv_bytes(int bits, int64_t pages, int64_t kv_heads, int64_t head_dim) {
     if (pages < 0 || pages > MAX_PAGES || kv_heads < 1 || kv_heads > MAX_HEADS ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
-    return (size_t)pages * (size_t)kv_heads * (size_t)kv_record((int)head_dim);
+    return (size_t)pages * (size_t)kv_heads * (size_t)kv_record_of(bits, (int)head_dim);
 }
 
-int q8k_kv_append(int dtype, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
-                  const int32_t* pos, const q8k_rope* rope, const int32_t* slots, const q8k_kv_cache* kv,
-                  void* stream) {
+size_t q8k_kv_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim) { return kv_bytes(8, pages, kv_heads, head_dim); }
+size_t q8k_kv4_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim) { return kv_bytes(4, pages, kv_heads, head_dim); }
+
+static int kv_append(const char* fn, int bits, int dtype, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, int64_t T, const int32_t* pos, const q8k_rope* rope, const int32_t* slots,
+                     const q8k_kv_cache* kv, void* stream) {
     begin_call();
-    const char* fn = "q8k_kv_append";
     Q8K_TRY(check_dtype(fn, dtype));
     Q8K_TRY(check_kv(fn, kv));
     Q8K_TRY(check_count(fn, "T", T, MAX_TOKENS));
@@ -538,12 +541,25 @@ int q8k_kv_append(int dtype, const void* k, int64_t k_stride, const void* v, int
     Q8K_TRY(check_grid(fn, (2 * T * row + 2047) / 2048));
     Q8K_TRY(check_threads(fn, kv_workgroups(T, kv->kv_heads), 256));
     if (T == 0 || kv->pages == 0) return Q8K_OK;
-    return launched(fn, launch_kv_append(kv->head_dim, a, (hipStream_t)stream));
+    return launched(fn, bits == 8 ? launch_kv_append(kv->head_dim, a, (hipStream_t)stream)
+                                  : launch_kv4_append(kv->head_dim, a, (hipStream_t)stream));
 }
 
-int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T, void* k, void* v, void* stream) {
+int q8k_kv_append(int dtype, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+                  const int32_t* pos, const q8k_rope* rope, const int32_t* slots, const q8k_kv_cache* kv,
+                  void* stream) {
+    return kv_append("q8k_kv_append", 8, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream);
+}
+
+int q8k_kv4_append(int dtype, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T,
+                   const int32_t* pos, const q8k_rope* rope, const int32_t* slots, const q8k_kv_cache* kv,
+                   void* stream) {
+    return kv_append("q8k_kv4_append", 4, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream);
+}
+
+static int kv_read(const char* fn, int bits, int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T,
+                   void* k, void* v, void* stream) {
     begin_call();
-    const char* fn = "q8k_kv_read";
     Q8K_TRY(check_dtype(fn, dtype));
     Q8K_TRY(check_kv(fn, kv));
     Q8K_TRY(check_count(fn, "T", T, MAX_TOKENS));
@@ -554,7 +570,16 @@ int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t
     Q8K_TRY(check_threads(fn, kv_workgroups(T, kv->kv_heads), 256));
     if (T == 0) return Q8K_OK;
     const KvRead a{static_cast<const uint8_t*>(kv->data), kv->pages, kv->kv_heads, dtype, slots, T, k, v};
-    return launched(fn, launch_kv_read(kv->head_dim, a, (hipStream_t)stream));
+    return launched(fn, bits == 8 ? launch_kv_read(kv->head_dim, a, (hipStream_t)stream)
+                                  : launch_kv4_read(kv->head_dim, a, (hipStream_t)stream));
+}
+
+int q8k_kv_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T, void* k, void* v, void* stream) {
+    return kv_read("q8k_kv_read", 8, dtype, kv, slots, T, k, v, stream);
+}
+
+int q8k_kv4_read(int dtype, const q8k_kv_cache* kv, const int32_t* slots, int64_t T, void* k, void* v, void* stream) {
+    return kv_read("q8k_kv4_read", 4, dtype, kv, slots, T, k, v, stream);
 }
 
 static int check_attend_sizes(const char* fn, const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq,
@@ -571,21 +596,30 @@ static int check_attend_sizes(const char* fn, const q8k_kv_cache* kv, int64_t q_
     return check_count(fn, "max_len", max_len, MAX_LEN);
 }
 
-size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
-                               int64_t max_len) {
-    const char* fn = "qattend_workspace_bytes";
+static size_t attend_workspace_bytes(const char* fn, const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq,
+                                     int64_t max_q, int64_t max_len) {
     if (!kv || !kv_dim(kv->head_dim) || kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS ||
         check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len) != Q8K_OK || B == 0 || max_q == 0)
         return 0;
     return (size_t)attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, 0).ws_bytes;
 }
 
-int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
-            const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table, int64_t max_pages,
-            const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
-            const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
-    begin_call();
-    const char* fn = "qattend";
+size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                               int64_t max_len) {
+    return attend_workspace_bytes("qattend_workspace_bytes", kv, q_heads, B, Tq, max_q, max_len);
+}
+
+size_t qattend_kv4_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                                   int64_t max_len) {
+    return attend_workspace_bytes("qattend_kv4_workspace_bytes", kv, q_heads, B, Tq, max_q, max_len);
+}
+
+// What attention and its weights are asked of queries, pages and lengths: the
+// checks, and these in *a.
+static int check_attend(const char* fn, int dtype, const void* q, int64_t q_stride, int64_t q_heads,
+                        const q8k_kv_cache* kv, int64_t B, const int32_t* cu_q, int64_t Tq, int64_t max_q,
+                        const int32_t* page_table, int64_t max_pages, const int32_t* kv_len, int64_t max_len,
+                        float scale, int64_t window, const int32_t* pos, const q8k_rope* rope, Attend* a) {
     Q8K_TRY(check_dtype(fn, dtype));
     Q8K_TRY(check_kv(fn, kv));
     Q8K_TRY(check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len));
@@ -600,41 +634,167 @@ int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q
     Q8K_TRY(check_ptr(fn, "cu_q", cu_q, 4));
     Q8K_TRY(check_ptr(fn, "page_table", page_table, 4));
     Q8K_TRY(check_ptr(fn, "kv_len", kv_len, 4));
+    Q8K_TRY(check_rope(fn, rope, pos, kv->head_dim, &a->rope));
+    a->q = q;
+    a->q_stride = q_stride;
+    a->q_heads = (int)q_heads;
+    a->heads = kv->kv_heads;
+    a->group = (int)(q_heads / kv->kv_heads);
+    a->dtype = dtype;
+    a->cache = static_cast<const uint8_t*>(kv->data);
+    a->pages = kv->pages;
+    a->B = B;
+    a->cu_q = cu_q;
+    a->Tq = Tq;
+    a->max_q = max_q;
+    a->table = page_table;
+    a->max_pages = max_pages;
+    a->kv_len = kv_len;
+    a->max_len = max_len;
+    a->scale = scale;
+    a->window = window;
+    a->pos = pos;
+    return Q8K_OK;
+}
+
+static int attend(const char* fn, int bits, int dtype, const void* q, int64_t q_stride, int64_t q_heads,
+                  const q8k_kv_cache* kv, int64_t B, const int32_t* cu_q, int64_t Tq, int64_t max_q,
+                  const int32_t* page_table, int64_t max_pages, const int32_t* kv_len, int64_t max_len, float scale,
+                  int64_t window, const int32_t* pos, const q8k_rope* rope, void* out, float* lse, void* ws,
+                  size_t ws_bytes, void* stream) {
+    begin_call();
+    Attend a{};
+    Q8K_TRY(check_attend(fn, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len,
+                         max_len, scale, window, pos, rope, &a));
     Q8K_TRY(check_ptr(fn, "out", out, 16));
     if (lse) Q8K_TRY(check_ptr(fn, "lse", lse, 4));
-    Attend a{};
-    Q8K_TRY(check_rope(fn, rope, pos, kv->head_dim, &a.rope));
-    const size_t need = qattend_workspace_bytes(kv, q_heads, B, Tq, max_q, max_len);
+    const size_t need = attend_workspace_bytes(fn, kv, q_heads, B, Tq, max_q, max_len);
     if (ws_bytes < need)
         return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
     if (B == 0 || max_q == 0) return Q8K_OK;
     const AttendPlan p = attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, window);
-    const int64_t group = q_heads / kv->kv_heads;
     Q8K_TRY(check_grid(fn, p.items * kv->kv_heads));
     Q8K_TRY(check_threads(fn, p.items * kv->kv_heads * p.slices, p.threads));
-    a.q = q;
-    a.q_stride = q_stride;
-    a.q_heads = (int)q_heads;
-    a.heads = kv->kv_heads;
-    a.group = (int)group;
-    a.dtype = dtype;
-    a.cache = static_cast<const uint8_t*>(kv->data);
-    a.pages = kv->pages;
-    a.B = B;
-    a.cu_q = cu_q;
-    a.Tq = Tq;
-    a.max_q = max_q;
-    a.table = page_table;
-    a.max_pages = max_pages;
-    a.kv_len = kv_len;
-    a.max_len = max_len;
-    a.scale = scale;
-    a.window = window;
-    a.pos = pos;
     a.out = out;
     a.lse = lse;
-    return launched(fn, launch_attend(kv->head_dim, p, a, ws, (hipStream_t)stream));
+    return launched(fn, launch_attend(bits, kv->head_dim, p, a, ws, (hipStream_t)stream));
+}
+
+int qattend(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
+            const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table, int64_t max_pages,
+            const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
+            const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    return attend("qattend", 8, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len,
+                  max_len, scale, window, pos, rope, out, lse, ws, ws_bytes, stream);
+}
+
+int qattend_kv4(int dtype, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv, int64_t B,
+                const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table, int64_t max_pages,
+                const int32_t* kv_len, int64_t max_len, float scale, int64_t window, const int32_t* pos,
+                const q8k_rope* rope, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    return attend("qattend_kv4", 4, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages,
+                  kv_len, max_len, scale, window, pos, rope, out, lse, ws, ws_bytes, stream);
+}
+
+static int check_bits(const char* fn, int bits) {
+    if (bits != 8 && bits != 4) return fail(Q8K_ERR_ARG, "%s: bits=%d: a cache is held in 8 or 4", fn, bits);
+    return Q8K_OK;
+}
+
+size_t qattend_weights_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
+                                       int64_t max_len) {
+    const char* fn = "qattend_weights_workspace_bytes";
+    if (!kv || !kv_dim(kv->head_dim) || kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS ||
+        check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len) != Q8K_OK || B == 0 || max_len == 0)
+        return 0;
+    return (size_t)weights_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim).ws_bytes;
+}
+
+int qattend_weights(int dtype, int bits, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv,
+                    int64_t B, const int32_t* cu_q, int64_t Tq, int64_t max_q, const int32_t* page_table,
+                    int64_t max_pages, const int32_t* kv_len, int64_t max_len, float scale, int64_t window,
+                    const int32_t* pos, const q8k_rope* rope, const float* lse, const float* old, float keep,
+                    float* weights, int64_t w_stride, void* ws, size_t ws_bytes, void* stream) {
+    begin_call();
+    const char* fn = "qattend_weights";
+    AttendWeights w{};
+    Q8K_TRY(check_bits(fn, bits));
+    Q8K_TRY(check_attend(fn, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len,
+                         max_len, scale, window, pos, rope, &w.a));
+    Q8K_TRY(check_ptr(fn, "lse", lse, 4));
+    if (old) Q8K_TRY(check_ptr(fn, "old", old, 4));
+    Q8K_TRY(check_ptr(fn, "weights", weights, 4));
+    if (!(keep - keep == 0.0f)) return fail(Q8K_ERR_ARG, "%s: keep=%g must be finite", fn, (double)keep);
+    if (w_stride < max_len || w_stride > ((int64_t)1 << 32))
+        return fail(Q8K_ERR_SHAPE, "%s: w_stride=%lld must be at least max_len=%lld", fn, (long long)w_stride,
+                    (long long)max_len);
+    const size_t need = qattend_weights_workspace_bytes(kv, q_heads, B, Tq, max_q, max_len);
+    if (ws_bytes < need)
+        return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+    if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
+    if (B == 0 || max_len == 0) return Q8K_OK;
+    const WeightsPlan p = weights_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim);
+    Q8K_TRY(check_grid(fn, p.workgroups));
+    Q8K_TRY(check_threads(fn, p.workgroups, p.threads));
+    w.lse = lse;
+    w.old = old;
+    w.keep = keep;
+    w.weights = weights;
+    w.stride = w_stride;
+    return launched(fn, launch_attend_weights(bits, kv->head_dim, p, w, ws, (hipStream_t)stream));
+}
+
+int q8k_kv_evict(int bits, const q8k_kv_cache* kv, int64_t B, const int32_t* page_table, int64_t max_pages,
+                 const int32_t* kv_len, int64_t max_len, const float* weights, int64_t w_stride, int64_t budget,
+                 int64_t first, int64_t last, const int32_t* out_table, int64_t out_pages, float* out_weights,
+                 int64_t out_stride, int32_t* kept, int32_t* new_len, void* stream) {
+    begin_call();
+    const char* fn = "q8k_kv_evict";
+    Q8K_TRY(check_bits(fn, bits));
+    Q8K_TRY(check_kv(fn, kv));
+    Q8K_TRY(check_count(fn, "B", B, MAX_BATCH));
+    Q8K_TRY(check_count(fn, "max_pages", max_pages, MAX_PAGES));
+    Q8K_TRY(check_count(fn, "max_len", max_len, MAX_LEN));
+    Q8K_TRY(check_count(fn, "out_pages", out_pages, MAX_PAGES));
+    if (max_len > max_pages * KV_PAGE)
+        return fail(Q8K_ERR_SHAPE, "%s: max_len=%lld exceeds the page table's %lld pages of %d tokens", fn,
+                    (long long)max_len, (long long)max_pages, KV_PAGE);
+    if (budget < 1 || budget > MAX_LEN || budget > out_pages * KV_PAGE)
+        return fail(Q8K_ERR_SHAPE, "%s: budget=%lld must be at least 1 and fit the new page table's %lld pages of %d tokens",
+                    fn, (long long)budget, (long long)out_pages, KV_PAGE);
+    if (first < 0 || last < 0 || first > budget || last > budget - first)
+        return fail(Q8K_ERR_ARG, "%s: first=%lld and last=%lld tokens exceed budget=%lld", fn, (long long)first,
+                    (long long)last, (long long)budget);
+    if (w_stride < max_len || w_stride > ((int64_t)1 << 32))
+        return fail(Q8K_ERR_SHAPE, "%s: w_stride=%lld must be at least max_len=%lld", fn, (long long)w_stride,
+                    (long long)max_len);
+    Q8K_TRY(check_ptr(fn, "page_table", page_table, 4));
+    Q8K_TRY(check_ptr(fn, "kv_len", kv_len, 4));
+    Q8K_TRY(check_ptr(fn, "weights", weights, 4));
+    Q8K_TRY(check_ptr(fn, "out_table", out_table, 4));
+    if (out_weights) {
+        Q8K_TRY(check_ptr(fn, "out_weights", out_weights, 4));
+        if (out_stride < budget || out_stride > ((int64_t)1 << 32))
+            return fail(Q8K_ERR_SHAPE, "%s: out_stride=%lld must be at least budget=%lld", fn, (long long)out_stride,
+                        (long long)budget);
+        if (out_weights == weights && out_stride != w_stride)
+            return fail(Q8K_ERR_ARG, "%s: weights kept in place need out_stride=%lld to be w_stride=%lld", fn,
+                        (long long)out_stride, (long long)w_stride);
+    }
+    Q8K_TRY(check_ptr(fn, "kept", kept, 4));
+    Q8K_TRY(check_ptr(fn, "new_len", new_len, 4));
+    if (new_len == kv_len) return fail(Q8K_ERR_ARG, "%s: new_len must not be kv_len, which the call reads to its end", fn);
+    const bool in_place = out_table == page_table;
+    if (in_place && out_pages != max_pages)
+        return fail(Q8K_ERR_ARG, "%s: a move in place needs out_pages=%lld to be max_pages=%lld", fn,
+                    (long long)out_pages, (long long)max_pages);
+    Q8K_TRY(check_threads(fn, B * kv->kv_heads, evict_threads()));
+    Q8K_TRY(check_threads(fn, evict_workgroups(bits, kv->head_dim, B, kv->kv_heads, budget, in_place), 64));
+    if (B == 0) return Q8K_OK;
+    const KvEvict a{static_cast<uint8_t*>(kv->data), kv->pages, kv->kv_heads, B, page_table, max_pages, kv_len, max_len,
+                    weights, w_stride, budget, first, last, out_table, out_pages, out_weights, out_stride, kept, new_len};
+    return launched(fn, launch_kv_evict(bits, kv->head_dim, a, in_place, (hipStream_t)stream));
 }
 
 size_t qlogprobs_workspace_bytes(int64_t T, int64_t V, int32_t topn) {

@@ -1,13 +1,11 @@
 // What the attention kernels share: the operands' arithmetic and the ranges
 // of a sequence's rows.
 #pragma once
-#include "kv_cache.h"
+#include "kv4_cache.h"
 #include "q8k_launch.h"
 
 namespace q8k {
 
-typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
 // Eight int8 codes as eight fp16 values, exactly: a code's byte with its sign

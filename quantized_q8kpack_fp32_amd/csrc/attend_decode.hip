@@ -1,4 +1,4 @@
-// Attention of few rows over the paged 8-bit cache: decode steps, a few drafted
+// Attention of few rows over the paged cache of 8 or 4 bits: decode steps, a few drafted
 // tokens, and prompts too short to fill the device with tiles of 64 rows; the
 // join of chunks; and the choice between the kernels (attend_plan).
 //
@@ -36,7 +36,7 @@ constexpr float P_UP = 32768.0f, P_DOWN = 1.0f / 32768.0f;
 // but the running maximum, and that only where it grew.
 // Of SLICES workgroups each makes its part of the row's values, the scores all of them.
 // NQ and NP: fp16 pieces of the queries and of the probabilities (f16_pieces).
-template <int D, int WAVES, int SLICES, int NQ, int NP>
+template <int D, int BITS, int WAVES, int SLICES, int NQ, int NP>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_kernel(Attend a) {
     constexpr int KS = D / 32;  // k steps of the first product
     constexpr int DV = D / SLICES;  // values of the result
@@ -46,6 +46,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     __shared__ float red[WAVES][ROWS][2];
     __shared__ float acc_s[WAVES][ROWS][DV + 4];
     __shared__ float scales[WAVES][2 * KV_PAGE];
+    __shared__ __attribute__((aligned(16))) uint32_t factors[WAVES][BITS == 4 ? DV / 2 : 4];  // of a page's values
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int h = (int)(blockIdx.x % a.heads);
@@ -78,25 +79,44 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     // tokens at 6.1 TB/s and 5.4 without, when this was chosen; 6.4 now).
     // Reads go through a buffer descriptor of one record; a page that selects
     // nothing has an empty one, whose reads return zeros and touch no memory.
+    // 4 bits: KB blocks of two pieces of the keys, one of two row blocks of the values; the
+    // factors of a lane's pieces, and those of the values, a word or two a lane, by LDS.
+    constexpr int KB = D / 32, VF = DV / 128 < 1 ? 1 : DV / 128;
     uint4 kraw[4][KS / 2], vraw[DB];
+    uint4 kraw4[KB], vraw4[DB / 2];
+    uint32_t kfac[KB / 2], vfac[VF];
     float ksc, vsc;
     bool ok, next_ok;
     const auto record_of = [&](int p, bool& good) {
         const int page = __builtin_amdgcn_readfirstlane(p < p1 ? pages[p] : -1);
         good = page >= 0 && page < a.pages;
-        return make_rsrc(a.cache + ((int64_t)(good ? page : 0) * a.heads + h) * kv_record(D), good ? kv_record(D) : 0);
+        constexpr int bytes = kv_record_of(BITS, D);
+        return make_rsrc(a.cache + ((int64_t)(good ? page : 0) * a.heads + h) * bytes, good ? bytes : 0);
     };
+    constexpr int SCALES = kv_record_of(BITS, D) - 8 * KV_PAGE;
     const auto load_keys = [&](rsrc_t rec) {
+        if constexpr (BITS == 8) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int s = 0; s < KS / 2; ++s) kraw[q][s] = load16_nt(rec, lane_off + s * 4096 + q * 1024);
-        ksc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D));
+                for (int s = 0; s < KS / 2; ++s) kraw[q][s] = load16_nt(rec, lane_off + s * 4096 + q * 1024);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KB; ++i) kraw4[i] = load16_nt(rec, lane_off + i * 1024);
+            load_words<KB / 2>(rec, KV4_KF(D) + (col * 2 + (g >> 1)) * (D / 16), kfac);
+        }
+        ksc = __builtin_bit_cast(float, load4(rec, 4 * lane + SCALES));
     };
     const auto load_values = [&](rsrc_t rec) {
+        if constexpr (BITS == 8) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d) vraw[d] = load16_nt(rec, lane_off + KV_PAGE * D + (slice * DB + d) * 1024);
-        vsc = __builtin_bit_cast(float, load4(rec, 4 * lane + 2 * KV_PAGE * D + 4 * KV_PAGE));
+            for (int d = 0; d < DB; ++d) vraw[d] = load16_nt(rec, lane_off + KV_PAGE * D + (slice * DB + d) * 1024);
+        } else {
+#pragma unroll
+            for (int e = 0; e < DB / 2; ++e) vraw4[e] = load16_nt(rec, lane_off + KV4_V(D) + (slice * (DB / 2) + e) * 1024);
+            load_words<VF>(rec, KV4_VF(D) + slice * 2 * DV + 4 * VF * (lane % (DV / 2 / VF)), vfac);
+        }
+        vsc = __builtin_bit_cast(float, load4(rec, 4 * lane + SCALES + 4 * KV_PAGE));
     };
     float* sc = scales[wave];
     {
@@ -138,9 +158,17 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
                 h8_t kf[4][2];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint4 c = kraw[q][s];
-                    kf[q][0] = codes_f16(c.x, c.y);
-                    kf[q][1] = codes_f16(c.z, c.w);
+                    if constexpr (BITS == 8) {
+                        const uint4 c = kraw[q][s];
+                        kf[q][0] = codes_f16(c.x, c.y);
+                        kf[q][1] = codes_f16(c.z, c.w);
+                    } else {
+                        const int e = q * (D / 64) + s;
+                        const uint4 c = kraw4[e >> 1];
+                        const Factors f = kv4_key_factors(kfac[e >> 2] >> (8 * (e & 3)) & 255u);
+                        kf[q][0] = kv4_widen_keys(e & 1 ? c.z : c.x, f);
+                        kf[q][1] = kv4_widen_keys(e & 1 ? c.w : c.y, f);
+                    }
                 }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -162,6 +190,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
         load_keys(rec);
         __builtin_amdgcn_sched_barrier(0);
         sc[KV_PAGE + lane] = vsc;
+        if constexpr (BITS == 4) {
+#pragma unroll
+            for (int i = 0; i < VF; ++i) factors[wave][VF * (lane % (DV / 2 / VF)) + i] = vfac[i];
+        }
         float vs[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -235,8 +267,15 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
             h8_t vf[VB][2];
 #pragma unroll
             for (int d = 0; d < VB; ++d) {
-                vf[d][0] = codes_f16(vraw[d0 + d].x, vraw[d0 + d].y);
-                vf[d][1] = codes_f16(vraw[d0 + d].z, vraw[d0 + d].w);
+                if constexpr (BITS == 8) {
+                    vf[d][0] = codes_f16(vraw[d0 + d].x, vraw[d0 + d].y);
+                    vf[d][1] = codes_f16(vraw[d0 + d].z, vraw[d0 + d].w);
+                } else if (d % 2 == 0) {
+                    const uint4 c = vraw4[(d0 + d) / 2];
+                    const uint4 f = *reinterpret_cast<const uint4*>(&factors[wave][(d0 + d) * 8 + 4 * g]);
+                    kv4_widen_values(c.x, c.y, f.x, f.y, vf[d][0], vf[d + 1][0]);
+                    kv4_widen_values(c.z, c.w, f.z, f.w, vf[d][1], vf[d + 1][1]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -381,26 +420,30 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Attend a) {
     if (lane == 0 && a.lse) a.lse[qr] = l == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-template <int D, int WAVES, int SLICES, int NQ, int NP>
+template <int D, int BITS, int WAVES, int SLICES, int NQ, int NP>
 hipError_t decode_n(const Attend& a, hipStream_t s) {
-    Q8K_LAUNCH((attend_decode_kernel<D, WAVES, SLICES, NQ, NP>), dim3((unsigned)(a.items * a.heads * SLICES)),
+    Q8K_LAUNCH((attend_decode_kernel<D, BITS, WAVES, SLICES, NQ, NP>), dim3((unsigned)(a.items * a.heads * SLICES)),
                dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
-template <int D, int WAVES, int SLICES>
+template <int D, int BITS, int WAVES, int SLICES>
 hipError_t decode_w(const Attend& a, hipStream_t s) {
-    if (a.dtype != DT_BF16) return decode_n<D, WAVES, SLICES, 2, 2>(a, s);
-    return a.rope.table ? decode_n<D, WAVES, SLICES, 2, 1>(a, s) : decode_n<D, WAVES, SLICES, 1, 1>(a, s);
+    if (a.dtype != DT_BF16) return decode_n<D, BITS, WAVES, SLICES, 2, 2>(a, s);
+    return a.rope.table ? decode_n<D, BITS, WAVES, SLICES, 2, 1>(a, s) : decode_n<D, BITS, WAVES, SLICES, 1, 1>(a, s);
 }
-template <int D>
+template <int D, int BITS>
 hipError_t decode_d(const Attend& a, const AttendPlan& p, hipStream_t s) {
     // eight waves' accumulators of 256 values would not fit; 64 values by four
     // are one row block each
     if constexpr (D < 256)
-        if (p.waves == 8) return decode_w<D, 8, 1>(a, s);
+        if (p.waves == 8) return decode_w<D, BITS, 8, 1>(a, s);
     if constexpr (D > 64)
-        if (p.slices == 4) return decode_w<D, 4, 4>(a, s);
-    return p.slices == 2 ? decode_w<D, 4, 2>(a, s) : decode_w<D, 4, 1>(a, s);
+        if (p.slices == 4) return decode_w<D, BITS, 4, 4>(a, s);
+    return p.slices == 2 ? decode_w<D, BITS, 4, 2>(a, s) : decode_w<D, BITS, 4, 1>(a, s);
+}
+template <int BITS>
+hipError_t decode_of(int D, const Attend& a, const AttendPlan& p, hipStream_t s) {
+    return D == 64 ? decode_d<64, BITS>(a, p, s) : D == 128 ? decode_d<128, BITS>(a, p, s) : decode_d<256, BITS>(a, p, s);
 }
 template <int D>
 hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
@@ -522,7 +565,7 @@ AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, i
     return p.ws_bytes > all.ws_bytes ? all : p;
 }
 
-hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s) {
+hipError_t launch_attend(int bits, int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s) {
     a.tile_rows = p.tile_rows;
     a.tiles_max = p.tiles_max;
     a.least = p.least;
@@ -533,10 +576,9 @@ hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStre
     a.part = static_cast<float*>(ws);
     if (p.split)
         a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(p.items * a.heads * p.tile_rows * D * 4));
-    const hipError_t e = p.tiles     ? launch_attend_tiles(D, a, s)
-                         : D == 64   ? decode_d<64>(a, p, s)
-                         : D == 128  ? decode_d<128>(a, p, s)
-                                     : decode_d<256>(a, p, s);
+    const hipError_t e = p.tiles     ? launch_attend_tiles(bits, D, a, s)
+                         : bits == 8 ? decode_of<8>(D, a, p, s)
+                                     : decode_of<4>(D, a, p, s);
     if (e != hipSuccess || !p.split) return e;
     return D == 64    ? join_d<64>(a, p.tiles, s)
            : D == 128 ? join_d<128>(a, p.tiles, s)

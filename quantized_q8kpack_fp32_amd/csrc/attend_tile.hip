@@ -1,4 +1,4 @@
-// Attention of many rows over the paged 8-bit cache: prompts and chunks of
+// Attention of many rows over the paged cache of 8 or 4 bits: prompts and chunks of
 // them.  The formula of attend_decode.hip; here the arithmetic bounds it, so the
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
@@ -50,7 +50,7 @@ struct PageOps {
 // by it: 500 tokens over 16001 283 us, 275).  Heads of 64 values in 128-row tiles
 // keep to the registers of three waves a SIMD (chunks of 1000 over 8000: 230 us, of
 // two waves 300).
-template <int D, int WAVES, int HALVES, int RT, int NQ, int NP>
+template <int D, int BITS, int WAVES, int HALVES, int RT, int NQ, int NP>
 __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) void attend_tile_kernel(Attend a) {
     constexpr int KS = D / 32, DB = D / 16, ROWS = 16 * RT * WAVES;
     constexpr int KC = D / 16 / WAVES;  // 1 KB pieces of a page's keys (and of its values) a wave brings
@@ -119,7 +119,10 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
     const int32_t* pages = a.table + it.b * a.max_pages;
     int ids = p0 + lane < p1 ? pages[p0 + lane] : -1;
     const int lane_off = col * 64 + g * 16;
-    uint4 kraw[KC], vraw[KC];
+    // (4 bits: keys and values together are D/16 such pieces, of D/32 blocks each, with the
+    // factors that the lane's codes need)
+    constexpr int PC = D / 16 / WAVES;
+    uint4 kraw[KC], vraw[KC], raw4[PC], fac[PC];
     float sc_raw;
     int at_p;  // the page that the registers hold
     bool raw_ok;
@@ -130,18 +133,56 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
         const int page = __builtin_amdgcn_readlane(ids, n & 63);
         at_p = p;
         raw_ok = p < p1 && page >= 0 && page < a.pages;
-        const rsrc_t rec = make_rsrc(a.cache + ((int64_t)(raw_ok ? page : 0) * a.heads + h) * kv_record(D),
-                                     raw_ok ? kv_record(D) : 0);
+        constexpr int bytes = kv_record_of(BITS, D);
+        const rsrc_t rec = make_rsrc(a.cache + ((int64_t)(raw_ok ? page : 0) * a.heads + h) * bytes, raw_ok ? bytes : 0);
+        if constexpr (BITS == 8) {
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-            kraw[c] = load16(rec, lane_off + (wave + WAVES * c) * 1024);
-            vraw[c] = load16(rec, lane_off + KV_PAGE * D + (wave + WAVES * c) * 1024);
+            for (int c = 0; c < KC; ++c) {
+                kraw[c] = load16(rec, lane_off + (wave + WAVES * c) * 1024);
+                vraw[c] = load16(rec, lane_off + KV_PAGE * D + (wave + WAVES * c) * 1024);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < PC; ++c) {
+                const int i = wave + WAVES * c;
+                raw4[c] = load16(rec, lane_off + i * 1024);  // the values' blocks follow the keys'
+                if (i < D / 32)
+                    fac[c].x = load2(rec, KV4_KF(D) + (col * 2 + (g >> 1)) * (D / 16) + 2 * i);
+                else
+                    fac[c] = load16(rec, KV4_VF(D) + (i - D / 32) * KV_PAGE + g * 16);
+            }
         }
-        sc_raw = __builtin_bit_cast(float, load4(rec, 2 * KV_PAGE * D + 4 * (threadIdx.x & 127)));
+        sc_raw = __builtin_bit_cast(float, load4(rec, bytes - 8 * KV_PAGE + 4 * (threadIdx.x & 127)));
     };
     const auto put = [&](PageOps<D>& o) {
+        if constexpr (BITS == 4) {
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
+            for (int c = 0; c < PC; ++c) {
+                const int i = wave + WAVES * c;
+                const uint4 r = raw4[c], f = fac[c];
+                if (i < D / 32) {
+                    // block i of the keys: pieces 2 i and 2 i + 1, piece p of tokens 16 (p / (D/64)) and on, plane p % (D/64)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int p = 2 * i + b, q = p / (D / 64), s = p % (D / 64);
+                        const Factors x = kv4_key_factors(b ? f.x >> 8 : f.x & 255u);
+                        o.k[q][2 * s][lane] = __builtin_bit_cast(uint4, kv4_widen_keys(b ? r.z : r.x, x));
+                        o.k[q][2 * s + 1][lane] = __builtin_bit_cast(uint4, kv4_widen_keys(b ? r.w : r.y, x));
+                    }
+                } else {
+                    const int e = i - D / 32;
+                    h8_t va, vb;
+                    kv4_widen_values(r.x, r.y, f.x, f.y, va, vb);
+                    o.v[2 * e][0][lane] = __builtin_bit_cast(uint4, va);
+                    o.v[2 * e + 1][0][lane] = __builtin_bit_cast(uint4, vb);
+                    kv4_widen_values(r.z, r.w, f.z, f.w, va, vb);
+                    o.v[2 * e][1][lane] = __builtin_bit_cast(uint4, va);
+                    o.v[2 * e + 1][1][lane] = __builtin_bit_cast(uint4, vb);
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < (BITS == 8 ? KC : 0); ++c) {
             // piece i of the keys: plane i / 4, tokens 16 (i % 4) and on
             const int i = wave + WAVES * c;
             o.k[i & 3][2 * (i >> 2)][lane] = __builtin_bit_cast(uint4, codes_f16(kraw[c].x, kraw[c].y));
@@ -422,33 +463,34 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
     }
 }
 
-template <int D, int WAVES, int HALVES, int RT>
+template <int D, int BITS, int WAVES, int HALVES, int RT>
 hipError_t tile_w(const Attend& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.items * a.heads)), block(64 * WAVES * HALVES);
     if (a.dtype != DT_BF16)
-        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, HALVES, RT, 2, 2>), grid, block, 0, s, a);
+        Q8K_LAUNCH((attend_tile_kernel<D, BITS, WAVES, HALVES, RT, 2, 2>), grid, block, 0, s, a);
     else if (a.rope.table)
-        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, HALVES, RT, 2, 1>), grid, block, 0, s, a);
+        Q8K_LAUNCH((attend_tile_kernel<D, BITS, WAVES, HALVES, RT, 2, 1>), grid, block, 0, s, a);
     else
-        Q8K_LAUNCH((attend_tile_kernel<D, WAVES, HALVES, RT, 1, 1>), grid, block, 0, s, a);
+        Q8K_LAUNCH((attend_tile_kernel<D, BITS, WAVES, HALVES, RT, 1, 1>), grid, block, 0, s, a);
     return hipGetLastError();
 }
-template <int D>
+template <int D, int BITS>
 hipError_t tile_d(const Attend& a, hipStream_t s) {
     if (a.tile_rows == ATTEND_TILE_FEW) {
         // two pages at a time in tiles that are not split; 256 values' operands fill LDS
         if constexpr (D < 256)
-            if (a.target == 0) return tile_w<D, 4, 2, 1>(a, s);
-        return tile_w<D, 4, 1, 1>(a, s);
+            if (a.target == 0) return tile_w<D, BITS, 4, 2, 1>(a, s);
+        return tile_w<D, BITS, 4, 1, 1>(a, s);
     }
     // heads of 256 values: eight waves of 16 rows (four of 32 do not fit the register file)
-    return tile_w<D, D == 256 ? 8 : 4, 1, D == 256 ? 1 : 2>(a, s);
+    return tile_w<D, BITS, D == 256 ? 8 : 4, 1, D == 256 ? 1 : 2>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_attend_tiles(int D, const Attend& a, hipStream_t s) {
-    return D == 64 ? tile_d<64>(a, s) : D == 128 ? tile_d<128>(a, s) : tile_d<256>(a, s);
+hipError_t launch_attend_tiles(int bits, int D, const Attend& a, hipStream_t s) {
+    if (bits == 8) return D == 64 ? tile_d<64, 8>(a, s) : D == 128 ? tile_d<128, 8>(a, s) : tile_d<256, 8>(a, s);
+    return D == 64 ? tile_d<64, 4>(a, s) : D == 128 ? tile_d<128, 4>(a, s) : tile_d<256, 4>(a, s);
 }
 
 }  // namespace q8k

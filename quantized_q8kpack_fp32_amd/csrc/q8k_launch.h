@@ -185,6 +185,8 @@ struct KvRead {
     void* v;
 };
 hipError_t launch_kv_read(int D, const KvRead& a, hipStream_t s);
+hipError_t launch_kv4_append(int D, const KvAppend& a, hipStream_t s);
+hipError_t launch_kv4_read(int D, const KvRead& a, hipStream_t s);
 int64_t kv_workgroups(int64_t T, int64_t heads);  // of 256 threads that a call of many tokens takes
 
 // Attention.  A key head's q_heads / heads query heads of a sequence's new
@@ -232,8 +234,50 @@ struct AttendPlan {
 AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
                        int64_t window);
 constexpr int ATTEND_TILE_ROWS = 128, ATTEND_TILE_FEW = 64;
-hipError_t launch_attend_tiles(int D, const Attend& a, hipStream_t s);  // attend_tile.hip
-hipError_t launch_attend(int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s);
+hipError_t launch_attend_tiles(int bits, int D, const Attend& a, hipStream_t s);  // attend_tile.hip
+hipError_t launch_attend(int bits, int D, const AttendPlan& p, Attend a, void* ws, hipStream_t s);  // a cache of 8 or 4 bits
+
+// Accumulated attention weights.
+struct AttendWeights {
+    Attend a;  // queries, pages and lengths
+    const float* lse;  // [Tq][q_heads]
+    const float* old;  // [B][heads] rows of `stride`, or nullptr
+    float keep;
+    float* weights;
+    int64_t stride;
+    int page_groups, splits;  // of the pages, of the rows
+    float* part;              // [splits][B][heads][page_groups * 256] where splits > 1
+};
+struct WeightsPlan {
+    int64_t page_groups, workgroups, ws_bytes;
+    int splits, threads;
+};
+WeightsPlan weights_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D);
+hipError_t launch_attend_weights(int bits, int D, const WeightsPlan& p, AttendWeights w, void* ws, hipStream_t s);
+
+// Eviction.
+struct KvEvict {
+    uint8_t* cache;
+    int64_t pages;
+    int heads;
+    int64_t B;
+    const int32_t* table;  // [B][max_pages]
+    int64_t max_pages;
+    const int32_t* kv_len;
+    int64_t max_len;
+    const float* weights;  // [B][heads] rows of w_stride
+    int64_t w_stride;
+    int64_t budget, first, last;
+    const int32_t* out_table;  // [B][out_pages]
+    int64_t out_pages;
+    float* out_weights;  // [B][heads] rows of out_stride, or nullptr
+    int64_t out_stride;
+    int32_t* kept;  // [B][heads][budget]
+    int32_t* new_len;
+};
+int64_t evict_workgroups(int bits, int D, int64_t B, int64_t heads, int64_t budget, bool in_place);
+int evict_threads();  // of a workgroup that chooses
+hipError_t launch_kv_evict(int bits, int D, const KvEvict& a, bool in_place, hipStream_t s);
 
 // Log probabilities.
 struct LogProbs {
