@@ -708,7 +708,7 @@ size_t qattend_weights_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, 
     if (!kv || !kv_dim(kv->head_dim) || kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS ||
         check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len) != Q8K_OK || B == 0 || max_len == 0)
         return 0;
-    return (size_t)weights_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim).ws_bytes;
+    return (size_t)weights_plan(B, Tq, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim).ws_bytes;
 }
 
 int qattend_weights(int dtype, int bits, const void* q, int64_t q_stride, int64_t q_heads, const q8k_kv_cache* kv,
@@ -734,9 +734,10 @@ int qattend_weights(int dtype, int bits, const void* q, int64_t q_stride, int64_
         return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
     if (B == 0 || max_len == 0) return Q8K_OK;
-    const WeightsPlan p = weights_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim);
+    const WeightsPlan p = weights_plan(B, Tq, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim);
     Q8K_TRY(check_grid(fn, p.workgroups));
     Q8K_TRY(check_threads(fn, p.workgroups, p.threads));
+    Q8K_TRY(check_threads(fn, B * kv->kv_heads * p.tiles_max, 64));
     w.lse = lse;
     w.old = old;
     w.keep = keep;

@@ -4,6 +4,8 @@
 // as attention left them.  With lse known no row needs its other tokens, so the
 // sum over rows stays where the tokens are: a wave holds the keys of one page, widened
 // once, and adds up its 64 tokens while the rows go by.  No atomics: one order always.
+#include <type_traits>
+
 #include "attend.h"
 
 namespace q8k {
@@ -12,55 +14,266 @@ namespace {
 
 constexpr int WAVES = 4, ROWS = 16;
 
-// A page's keys of one head as the product's operand.
+// A page's keys of one head: on their way, and as the product's operand.
 template <int D, int BITS>
-__device__ __forceinline__ void page_keys(rsrc_t rec, int lane, h8_t (&kf)[4][D / 32]) {
-    const int col = lane & 15, g = lane >> 4, off = col * 64 + g * 16;
-    if constexpr (BITS == 8) {
-        uint4 raw[4][D / 64];
+struct PageKeys {
+    uint4 raw[BITS == 8 ? D / 16 : D / 32];
+    uint32_t fac[D / 64];
+    float scale;  // of token `lane`
+    __device__ __forceinline__ void fetch(rsrc_t rec, int lane) {
+        const int col = lane & 15, g = lane >> 4, off = col * 64 + g * 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) raw[q][s] = load16_nt(rec, off + s * 4096 + q * 1024);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int s = 0; s < D / 64; ++s) {
-                kf[q][2 * s] = codes_f16(raw[q][s].x, raw[q][s].y);
-                kf[q][2 * s + 1] = codes_f16(raw[q][s].z, raw[q][s].w);
-            }
-    } else {
-        uint4 raw[D / 32];
-        uint32_t fac[D / 64];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) raw[i] = load16_nt(rec, off + i * 1024);
-        load_words<D / 64>(rec, KV4_KF(D) + (col * 2 + (g >> 1)) * (D / 16), fac);
-#pragma unroll
-        for (int p = 0; p < D / 16; ++p) {
-            const int q = p / (D / 64), s = p % (D / 64);
+        for (int i = 0; i < (BITS == 8 ? D / 16 : D / 32); ++i) raw[i] = load16_nt(rec, off + i * 1024);
+        if constexpr (BITS == 4) load_words<D / 64>(rec, KV4_KF(D) + (col * 2 + (g >> 1)) * (D / 16), fac);
+        scale = __builtin_bit_cast(float, load4(rec, kv_record_of(BITS, D) - 8 * KV_PAGE + 4 * lane));
+    }
+    // of 16 tokens 16 q and on, steps 2 s and 2 s + 1
+    __device__ __forceinline__ void widen(int q, int s, h8_t& a, h8_t& b) const {
+        if constexpr (BITS == 8) {
+            const uint4 c = raw[4 * s + q];
+            a = codes_f16(c.x, c.y);
+            b = codes_f16(c.z, c.w);
+        } else {
+            const int p = q * (D / 64) + s;
             const uint4 c = raw[p >> 1];
             const Factors f = kv4_key_factors(fac[p >> 2] >> (8 * (p & 3)) & 255u);
-            kf[q][2 * s] = kv4_widen_keys(p & 1 ? c.z : c.x, f);
-            kf[q][2 * s + 1] = kv4_widen_keys(p & 1 ? c.w : c.y, f);
+            a = kv4_widen_keys(p & 1 ? c.z : c.x, f);
+            b = kv4_widen_keys(p & 1 ? c.w : c.y, f);
+        }
+    }
+};
+
+// A row: the unit of its products, log2 of its sum (inf where it sees nothing), and
+// the tokens that it sees.
+struct RowInfo {
+    float unit, lse;
+    int first, last;
+};
+
+// Sixteen rows of a head as the product's operand, by way of LDS, and their RowInfo
+// (in lane group 0).
+template <int D, int NQ>
+__device__ __forceinline__ RowInfo stage_rows(const AttendWeights& w, const Sequence& seq, int h, int t, int lane,
+                                              float (*q_s)[D + 4], h8_t (&qf)[NQ][D / 32]) {
+    const Attend& a = w.a;
+    const int col = lane & 15, g = lane >> 4, rows = seq.nq * a.group;
+    const Tile tile = item_tile(a, seq, t);
+    QueryItem qi[D / 32];
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n) {
+        const int i = lane + 64 * n;
+        fetch_q<D>(a, seq, h, row_of_tile(a, tile, min(i / (D / 8), rows - 1 - tile.row0)), i % (D / 8), qi[n]);
+    }
+    RowInfo o{1.0f, INFINITY, 0, -1};
+    if (tile.row0 + col < rows) {
+        const TileRow tr = row_of_tile(a, tile, col);
+        const Span sp = span_of(a, seq, tr.tok);
+        const float lse = w.lse[q_row_of(a, seq, h, tr)];
+        // (a row of -inf sees nothing that counts)
+        o = RowInfo{1.0f, lse == -INFINITY ? INFINITY : lse * LOG2E, sp.first, sp.last};
+    }
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n) fetch_turn(a, (lane + 64 * n) % (D / 8), qi[n]);
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n) {
+        const int i = lane + 64 * n;
+        put_q(a, i % (D / 8), qi[n], q_s[i / (D / 8)]);
+    }
+    __builtin_amdgcn_wave_barrier();
+    o.unit = query_operand<D, NQ>(a, q_s[col], g, qf);
+    __builtin_amdgcn_wave_barrier();
+    return o;
+}
+
+// What 16 rows add to a page's tokens: lane (col, g) holds row col's part of tokens
+// 16 q + 4 g + e.
+__device__ __forceinline__ void add_row(const f4_t (&s4)[4], const float* scales, const RowInfo& row, int j0, int g,
+                                        float (&sum)[4][4]) {
+    const bool whole = !__any(row.first > j0 || row.last < j0 + KV_PAGE - 1);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const f4_t ks = *reinterpret_cast<const f4_t*>(scales + 16 * q + 4 * g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[q][e] * ks[e], row.unit, -row.lse));
+            const int j = j0 + 16 * q + 4 * g + e;
+            sum[q][e] += whole || (j >= row.first && j <= row.last) ? x : 0.0f;
         }
     }
 }
+// Over the sixteen lanes of a row, halving what a lane holds at each step: lane (col, g)
+// is left with token 16 q + 4 g + e, q = 2 (col / 4 % 2) + col / 8, e = col % 4.
+__device__ __forceinline__ float rows_sum(const float (&sum)[4][4], int col) {
+    const auto swap = [](float v, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    const bool b2 = col & 4, b3 = col & 8, b1 = col & 2, b0 = col & 1;
+    float x[2][4], y[4], z[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[q][e] = (b2 ? sum[q + 2][e] : sum[q][e]) +
+                      swap(b2 ? sum[q][e] : sum[q + 2][e], std::integral_constant<int, 0x141>{});  // row_half_mirror
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        y[e] = (b3 ? x[1][e] : x[0][e]) + swap(b3 ? x[0][e] : x[1][e], std::integral_constant<int, 0x128>{});  // row_ror:8
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        z[e] = (b1 ? y[e + 2] : y[e]) + swap(b1 ? y[e] : y[e + 2], std::integral_constant<int, 0x4E>{});  // quad_perm 2,3,0,1
+    return (b0 ? z[1] : z[0]) + swap(b0 ? z[0] : z[1], std::integral_constant<int, 0xB1>{});  // quad_perm 1,0,3,2
+}
+__device__ __forceinline__ int token_of(int col, int g) { return 16 * (2 * (col >> 2 & 1) + (col >> 3)) + 4 * g + (col & 3); }
 
-struct RowInfo {
-    float unit, lse;  // of the products, and log2 of the sum; inf where the row sees nothing
-    int first, last;  // the tokens that it sees
-};
+__device__ __forceinline__ rsrc_t page_record(const Attend& a, int page, int h, int bytes, bool& ok) {
+    ok = page >= 0 && page < a.pages;
+    return make_rsrc(a.cache + ((int64_t)(ok ? page : 0) * a.heads + h) * bytes, ok ? bytes : 0);
+}
 
-// One workgroup: four pages of one sequence and head, and its share of the rows.
-// Sixteen rows a wave become operands in LDS, which all waves then multiply.
-template <int D, int BITS, int NQ>
-__global__ __launch_bounds__(64 * WAVES, 1) void attend_weights_kernel(AttendWeights w) {
-    constexpr int KS = D / 32;
+// Few rows, up to 16 or 64 (ONE: their operand stays in registers, else in LDS): each
+// workgroup brings them once and then streams its share of a sequence's pages, a
+// page a wave, the next one's codes on their way.
+template <int D, int BITS, int NQ, bool ONE>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kernel(AttendWeights w) {
+    constexpr int KS = D / 32, TILES = ONE ? 1 : 4;
     const Attend& a = w.a;
     __shared__ float qs[WAVES][ROWS][D + 4];
-    __shared__ uint4 op[WAVES][NQ][KS][64];
-    __shared__ RowInfo info[WAVES][ROWS];
+    __shared__ uint4 op[TILES][NQ][ONE ? 1 : KS][64];
+    __shared__ RowInfo info[TILES][ROWS];
     __shared__ float scales[WAVES][KV_PAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int h = (int)(blockIdx.x % a.heads);
+    const int64_t id = blockIdx.x / a.heads, b = id / w.groups;
+    const int c0 = (int)(id % w.groups) * w.group_pages;
+    const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
+    const int pages = (seq.len + KV_PAGE - 1) / KV_PAGE, c1 = min(pages, c0 + w.group_pages);
+    if (c0 >= c1) return;
+    constexpr int bytes = kv_record_of(BITS, D);
+    const int32_t* table = a.table + b * a.max_pages;
+    PageKeys<D, BITS> keys;
+    bool ok = false, next_ok;
+    int p = c0 + wave;
+    const auto page_at = [&](int p) { return __builtin_amdgcn_readfirstlane(p < c1 ? table[p] : -1); };
+    keys.fetch(page_record(a, page_at(p), h, bytes, ok), lane);
+    const int tiles = (seq.nq * a.group + ROWS - 1) / ROWS;
+    h8_t qf[NQ][KS];
+    RowInfo mine{1.0f, INFINITY, 0, -1};
+    if constexpr (ONE) {
+        if (tiles > 0) mine = stage_rows<D, NQ>(w, seq, h, 0, lane, qs[wave], qf);
+        if (tiles == 0)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) qf[n][s] = h8_t{};
+        if (g == 0 && wave == 0) info[0][col] = mine;
+    } else if (wave < tiles) {
+        mine = stage_rows<D, NQ>(w, seq, h, wave, lane, qs[wave], qf);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) op[wave][n][s][lane] = __builtin_bit_cast(uint4, qf[n][s]);
+        if (g == 0) info[wave][col] = mine;
+    }
+    __syncthreads();
+    const int64_t row = (b * a.heads + h) * w.stride;
+    for (; p < c1; p += WAVES) {
+        const int j0 = p * KV_PAGE, j = j0 + token_of(col, g);
+        const float before = w.old && j < seq.len - seq.n ? w.old[row + j] : 0.0f;
+        scales[wave][lane] = keys.scale;
+        float sum[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[q][i] = 0.0f;
+        const rsrc_t rec = page_record(a, page_at(p + WAVES), h, bytes, next_ok);
+        if constexpr (ONE) {
+            f4_t s4[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s4[q] = f4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < KS / 2; ++s) {
+                h8_t kf[4][2];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) keys.widen(q, s, kf[q][0], kf[q][1]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q][t], qf[n][2 * s + t], s4[q], 0, 0, 0);
+            }
+            keys.fetch(rec, lane);
+            if (ok) add_row(s4, scales[wave], info[0][col], j0, g, sum);
+        } else {
+            h8_t kf[4][KS];
+#pragma unroll
+            for (int s = 0; s < KS / 2; ++s)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) keys.widen(q, s, kf[q][2 * s], kf[q][2 * s + 1]);
+            keys.fetch(rec, lane);
+            if (ok)
+                for (int i = 0; i < tiles; ++i) {
+                    f4_t s4[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) s4[q] = f4_t{0, 0, 0, 0};
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            const h8_t x = __builtin_bit_cast(h8_t, op[i][n][s][lane]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q][s], x, s4[q], 0, 0, 0);
+                        }
+                    add_row(s4, scales[wave], info[i][col], j0, g, sum);
+                }
+        }
+        const float got = rows_sum(sum, col);
+        if (j < seq.len) w.weights[row + j] = __builtin_fmaf(before, w.keep, got);
+        ok = next_ok;
+    }
+}
+
+// Many rows: they become operands once, in the workspace, sixteen to a piece of
+// NQ D/32 + 1 KB (the last: their RowInfo, four times over).
+template <int D, int NQ>
+constexpr int piece_kb() { return NQ * (D / 32) + 1; }
+__device__ __forceinline__ int64_t first_piece(const Attend& a, const Sequence& seq, int64_t b) {
+    return (int64_t)seq.q0 * a.group / ROWS + b;  // sequences' rows are ascending: pieces do not meet
+}
+template <int D, int NQ>
+__global__ __launch_bounds__(64 * WAVES) void weights_rows_kernel(AttendWeights w) {
+    const Attend& a = w.a;
+    __shared__ float qs[WAVES][ROWS][D + 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = (int64_t)blockIdx.x * WAVES + wave;
+    const int h = (int)(id % a.heads);
+    const int t = (int)(id / a.heads % a.tiles_max);
+    const int64_t b = id / a.heads / a.tiles_max;
+    if (b >= a.B) return;
+    const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
+    if (t * ROWS >= seq.nq * a.group) return;
+    h8_t qf[NQ][D / 32];
+    const RowInfo o = stage_rows<D, NQ>(w, seq, h, t, lane, qs[wave], qf);
+    uint4* to = w.rows + ((first_piece(a, seq, b) + t) * a.heads + h) * (64 * piece_kb<D, NQ>()) + lane;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) to[64 * (n * (D / 32) + s)] = __builtin_bit_cast(uint4, qf[n][s]);
+    to[64 * NQ * (D / 32)] = __builtin_bit_cast(uint4, o);
+}
+
+// Then each workgroup holds the keys of PAGES pages a wave, widened once, and its share
+// of the rows goes by: pieces by the buffer into LDS, TS at a time, the next ones on
+// their way while these are multiplied, one barrier for TS.
+template <int D, int BITS, int NQ>
+__global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeights w) {
+    constexpr int KS = D / 32, PAGES = D == 256 ? 1 : 2, KB = piece_kb<D, NQ>(), TS = D == 256 ? 2 : 4;
+    const Attend& a = w.a;
+    __shared__ uint4 ops[2][TS][KB][64];
+    __shared__ float scales[WAVES][PAGES][KV_PAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     int64_t id = blockIdx.x;
@@ -68,141 +281,178 @@ __global__ __launch_bounds__(64 * WAVES, 1) void attend_weights_kernel(AttendWei
     id /= a.heads;
     const int split = (int)(id % w.splits);
     id /= w.splits;
-    const int64_t b = id / w.page_groups;
-    const int p0 = (int)(id % w.page_groups) * WAVES;
+    const int64_t b = id / w.groups;
+    const int c0 = (int)(id % w.groups) * (WAVES * PAGES);
     const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
-    if (p0 * KV_PAGE >= seq.len) return;
-    const int p = p0 + wave, j0 = p * KV_PAGE;
-    const int page = __builtin_amdgcn_readfirstlane(j0 < seq.len ? a.table[b * a.max_pages + p] : -1);
-    const bool ok = page >= 0 && page < a.pages;
+    if (c0 * KV_PAGE >= seq.len) return;
     constexpr int bytes = kv_record_of(BITS, D);
-    const rsrc_t rec = make_rsrc(a.cache + ((int64_t)(ok ? page : 0) * a.heads + h) * bytes, ok ? bytes : 0);
-    h8_t kf[4][KS];
-    page_keys<D, BITS>(rec, lane, kf);
-    scales[wave][lane] = __builtin_bit_cast(float, load4(rec, bytes - 8 * KV_PAGE + 4 * lane));
-    float ks[4][4], sum[4][4];
+    const int32_t* table = a.table + b * a.max_pages;
+    // rows that may see one of these pages
+    const int past = seq.len - seq.n, i0 = max(0, c0 * KV_PAGE - past);
+    int64_t i1 = seq.nq;
+    if (a.window > 0) i1 = min(i1, (int64_t)(c0 + WAVES * PAGES) * KV_PAGE - 1 + a.window - past);
+    const int r0 = uni(i0 * a.group / ROWS), r1 = uni(i1 > i0 ? (int)((i1 * a.group + ROWS - 1) / ROWS) : r0);
+    const int each = (r1 - r0 + w.splits - 1) / w.splits, t0 = r0 + split * each, t1 = min(r1, t0 + each);
+    const uint4* pieces = w.rows + (first_piece(a, seq, b) * a.heads + h) * (64 * KB);
+    const int64_t step = (int64_t)a.heads * (64 * KB);
+    const auto bring = [&](int t, int buf) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 k = *reinterpret_cast<const float4*>(&scales[wave][16 * q + 4 * g]);
-        ks[q][0] = k.x, ks[q][1] = k.y, ks[q][2] = k.z, ks[q][3] = k.w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[q][i] = 0.0f;
-    }
-    const int rows = seq.nq * a.group, tiles = (rows + ROWS - 1) / ROWS;
-    const int each = (tiles + w.splits - 1) / w.splits, t0 = split * each, t1 = min(tiles, t0 + each);
-    for (int t = t0; t < t1; t += WAVES) {
-        if (t + wave < t1) {
-            const Tile tile = item_tile(a, seq, t + wave);
-            float(*q_s)[D + 4] = qs[wave];
-#pragma unroll
-            for (int n = 0; n < D / 32; ++n) {
-                const int i = lane + 64 * n, r = i / (D / 8), it = i % (D / 8);
-                QueryItem qi;
-                fetch_q<D>(a, seq, h, row_of_tile(a, tile, min(r, rows - 1 - tile.row0)), it, qi);
-                fetch_turn(a, it, qi);
-                put_q(a, it, qi, q_s[r]);
-            }
-            __builtin_amdgcn_wave_barrier();
-            h8_t qf[NQ][KS];
-            const float unit = query_operand<D, NQ>(a, q_s[col], g, qf);
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) op[wave][n][s][lane] = __builtin_bit_cast(uint4, qf[n][s]);
-            if (g == 0) {
-                RowInfo o{unit, INFINITY, 0, -1};
-                if (tile.row0 + col < rows) {
-                    const TileRow tr = row_of_tile(a, tile, col);
-                    const Span sp = span_of(a, seq, tr.tok);
-                    const float lse = w.lse[q_row_of(a, seq, h, tr)];
-                    // (a row of -inf sees nothing that counts)
-                    o = RowInfo{unit, lse == -INFINITY ? INFINITY : lse * LOG2E, sp.first, sp.last};
-                }
-                info[wave][col] = o;
-            }
+        for (int i = 0; i < (TS * KB + WAVES - 1) / WAVES; ++i) {
+            const int x = wave + WAVES * i;
+            if (x >= TS * KB) break;
+            const rsrc_t src = make_rsrc(pieces + min(t + x / KB, t1 - 1) * step, KB * 1024);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)&ops[buf][x / KB][x % KB][0],
+                                                     16, 16 * lane, (x % KB) * 1024, 0, 0);
         }
+    };
+    if (t0 < t1) bring(t0, 0);
+    h8_t kf[PAGES][4][KS];
+    bool ok[PAGES];
+    float sum[PAGES][4][4];
+#pragma unroll
+    for (int n = 0; n < PAGES; ++n) {
+        const int p = c0 + wave * PAGES + n;
+        const int page = __builtin_amdgcn_readfirstlane(p * KV_PAGE < seq.len ? table[p] : -1);
+        PageKeys<D, BITS> keys;
+        keys.fetch(page_record(a, page, h, bytes, ok[n]), lane);
+#pragma unroll
+        for (int s = 0; s < KS / 2; ++s)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) keys.widen(q, s, kf[n][q][2 * s], kf[n][q][2 * s + 1]);
+        scales[wave][n][lane] = keys.scale;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[n][q][e] = 0.0f;
+    }
+    for (int t = t0, buf = 0; t < t1; t += TS, buf ^= 1) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        for (int i = 0; i < WAVES && t + i < t1; ++i) {
-            const RowInfo row = info[i][col];
-            const bool sees = ok && row.first < j0 + KV_PAGE && row.last >= j0;
-            if (!__any(sees)) continue;
-            f4_t s4[4];
+        if (t + TS < t1) bring(t + TS, buf ^ 1);
+        for (int i = 0; i < TS && t + i < t1; ++i) {
+            const RowInfo row = __builtin_bit_cast(RowInfo, ops[buf][i][KB - 1][lane]);
+            f4_t s4[PAGES][4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s4[q] = f4_t{0, 0, 0, 0};
+            for (int n = 0; n < PAGES; ++n)
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
+                for (int q = 0; q < 4; ++q) s4[n][q] = f4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    const h8_t qf = __builtin_bit_cast(h8_t, op[i][n][s][lane]);
+            for (int m = 0; m < NQ; ++m)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q][s], qf, s4[q], 0, 0, 0);
+                for (int s = 0; s < KS; ++s) {
+                    const h8_t x = __builtin_bit_cast(h8_t, ops[buf][i][m * KS + s][lane]);
+#pragma unroll
+                    for (int n = 0; n < PAGES; ++n)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            s4[n][q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[n][q][s], x, s4[n][q], 0, 0, 0);
                 }
-            const bool whole = !__any(row.first > j0 || row.last < j0 + KV_PAGE - 1);
+            __builtin_amdgcn_sched_barrier(0);  // keeps to two waves' registers
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[q][e] * ks[q][e], row.unit, -row.lse));
-                    const int j = j0 + 16 * q + 4 * g + e;
-                    sum[q][e] += whole || (j >= row.first && j <= row.last) ? x : 0.0f;
-                }
+            for (int n = 0; n < PAGES; ++n)
+                if (ok[n]) add_row(s4[n], scales[wave][n], row, (c0 + wave * PAGES + n) * KV_PAGE, g, sum[n]);
         }
-        __syncthreads();
     }
-    if (j0 >= seq.len) return;
-    // over the sixteen rows' lanes, then lane (col, g) keeps token 16 (col / 4) + 4 g + col % 4
-    float mine = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float v = sum[q][e];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v += dpp_f(v, k);
-            mine = col == 4 * q + e ? v : mine;
+    for (int n = 0; n < PAGES; ++n) {
+        const float got = rows_sum(sum[n], col);
+        const int j = (c0 + wave * PAGES + n) * KV_PAGE + token_of(col, g);
+        if (j >= seq.len) continue;
+        if (w.splits > 1) {
+            w.part[(split * a.B * a.heads + b * a.heads + h) * (int64_t)w.groups * (WAVES * PAGES * KV_PAGE) + j] = got;
+        } else {
+            const int64_t at = (b * a.heads + h) * w.stride + j;
+            w.weights[at] = __builtin_fmaf(w.old && j < past ? w.old[at] : 0.0f, w.keep, got);
         }
-    const int j = j0 + 16 * (col >> 2) + 4 * g + (col & 3);
-    if (j >= seq.len) return;
-    if (w.splits > 1) {
-        w.part[((split * a.B + b) * a.heads + h) * (int64_t)w.page_groups * (WAVES * KV_PAGE) + j] = mine;
-        return;
     }
-    const int64_t at = (b * a.heads + h) * w.stride + j;
-    w.weights[at] = w.old && j < seq.len - seq.n ? __builtin_fmaf(w.old[at], w.keep, mine) : mine;
 }
 
-template <int D, int BITS>
-hipError_t weights_d(const AttendWeights& w, unsigned grid, hipStream_t s) {
-    if (w.a.dtype == DT_BF16 && !w.a.rope.table)
-        Q8K_LAUNCH((attend_weights_kernel<D, BITS, 1>), dim3(grid), dim3(64 * WAVES), 0, s, w);
-    else
-        Q8K_LAUNCH((attend_weights_kernel<D, BITS, 2>), dim3(grid), dim3(64 * WAVES), 0, s, w);
+// Adds up the shares of the rows, in order.
+__global__ __launch_bounds__(256) void weights_join_kernel(AttendWeights w, int64_t len) {
+    const Attend& a = w.a;
+    const int64_t per = (len + 255) / 256, bh = blockIdx.x / per, b = bh / a.heads;
+    const int j = (int)(blockIdx.x % per) * 256 + threadIdx.x;
+    const Sequence seq = sequence_of(a, b);
+    if (j >= seq.len) return;
+    const float* part = w.part + bh * len + j;
+    float got = 0.0f;
+    for (int s = 0; s < w.splits; ++s) got += part[s * a.B * a.heads * len];
+    const int64_t at = bh * w.stride + j;
+    w.weights[at] = __builtin_fmaf(w.old && j < seq.len - seq.n ? w.old[at] : 0.0f, w.keep, got);
+}
+
+template <int D, int BITS, int NQ>
+hipError_t weights_n(const WeightsPlan& p, const AttendWeights& w, hipStream_t s) {
+    const dim3 grid((unsigned)p.workgroups), block(64 * WAVES);
+    if (!p.many) {
+        if (p.rows <= ROWS)
+            Q8K_LAUNCH((weights_few_kernel<D, BITS, NQ, true>), grid, block, 0, s, w);
+        else
+            Q8K_LAUNCH((weights_few_kernel<D, BITS, NQ, false>), grid, block, 0, s, w);
+        return hipGetLastError();
+    }
+    const int64_t waves = w.a.B * w.a.heads * w.a.tiles_max;
+    Q8K_LAUNCH((weights_rows_kernel<D, NQ>), dim3((unsigned)((waves + WAVES - 1) / WAVES)), block, 0, s, w);
+    Q8K_LAUNCH((weights_many_kernel<D, BITS, NQ>), grid, block, 0, s, w);
+    if (p.splits > 1) {
+        const int64_t len = p.groups * p.group_pages * KV_PAGE;
+        Q8K_LAUNCH(weights_join_kernel, dim3((unsigned)(w.a.B * w.a.heads * ((len + 255) / 256))), dim3(256), 0, s, w, len);
+    }
     return hipGetLastError();
+}
+template <int D, int BITS>
+hipError_t weights_d(const WeightsPlan& p, const AttendWeights& w, hipStream_t s) {
+    return w.a.dtype == DT_BF16 && !w.a.rope.table ? weights_n<D, BITS, 1>(p, w, s) : weights_n<D, BITS, 2>(p, w, s);
 }
 
 }  // namespace
 
-WeightsPlan weights_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {
-    WeightsPlan p;
-    p.page_groups = (max_len + WAVES * KV_PAGE - 1) / (WAVES * KV_PAGE);
+// Up to FEW_ROWS rows a head: one launch, a workgroup for each group of pages, as many
+// as make about FEW_WGS workgroups at the limits.  More: the rows' operands in the
+// workspace, groups of WAVES * 2 pages (of 256 values WAVES), and the rows in as many
+// shares as make MANY_WGS workgroups.
+constexpr int64_t FEW_ROWS = 64, FEW_WGS = 2048, MANY_WGS = 1024;
+
+WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {
+    WeightsPlan p{};
+    const int64_t group = q_heads / heads, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
+    p.rows = max_q * group;
+    p.many = p.rows > FEW_ROWS;
     p.splits = 1;
-    p.workgroups = B * heads * p.page_groups * p.splits;
     p.threads = 64 * WAVES;
-    p.ws_bytes = 0;
+    p.tiles_max = (p.rows + ROWS - 1) / ROWS;
+    if (!p.many) {
+        p.group_pages = (B * heads * pages + FEW_WGS - 1) / FEW_WGS;
+        p.group_pages = p.group_pages < WAVES ? WAVES : (p.group_pages + WAVES - 1) / WAVES * WAVES;
+    } else {
+        p.group_pages = WAVES * (D == 256 ? 1 : 2);
+    }
+    p.groups = (pages + p.group_pages - 1) / p.group_pages;
+    p.workgroups = B * heads * p.groups;
+    if (p.many) {
+        int64_t splits = (MANY_WGS + p.workgroups - 1) / p.workgroups;
+        const int64_t most = (p.tiles_max + 15) / 16;  // sixteen tiles a share at least
+        splits = splits > most ? most : splits;
+        p.splits = (int)splits;
+        p.workgroups *= splits;
+        p.rows_bytes = (Tq * group / ROWS + B + 1) * heads * (2 * (D / 32) + 1) * 1024;
+        p.ws_bytes = p.rows_bytes;
+        if (splits > 1) p.ws_bytes += splits * B * heads * p.groups * p.group_pages * KV_PAGE * 4;
+    }
     return p;
 }
 
 hipError_t launch_attend_weights(int bits, int D, const WeightsPlan& p, AttendWeights w, void* ws, hipStream_t s) {
     w.a.tile_rows = ROWS;
+    w.a.tiles_max = (int)p.tiles_max;
     w.a.inv_group = 1.0f / (float)w.a.group;
-    w.page_groups = (int)p.page_groups;
+    w.groups = (int)p.groups;
+    w.group_pages = (int)p.group_pages;
     w.splits = p.splits;
-    w.part = static_cast<float*>(ws);
-    const unsigned grid = (unsigned)p.workgroups;
-    if (bits == 8)
-        return D == 64 ? weights_d<64, 8>(w, grid, s) : D == 128 ? weights_d<128, 8>(w, grid, s) : weights_d<256, 8>(w, grid, s);
-    return D == 64 ? weights_d<64, 4>(w, grid, s) : D == 128 ? weights_d<128, 4>(w, grid, s) : weights_d<256, 4>(w, grid, s);
+    w.rows = static_cast<uint4*>(ws);
+    w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.rows_bytes);
+    if (bits == 8) return D == 64 ? weights_d<64, 8>(p, w, s) : D == 128 ? weights_d<128, 8>(p, w, s) : weights_d<256, 8>(p, w, s);
+    return D == 64 ? weights_d<64, 4>(p, w, s) : D == 128 ? weights_d<128, 4>(p, w, s) : weights_d<256, 4>(p, w, s);
 }
 
 }  // namespace q8k

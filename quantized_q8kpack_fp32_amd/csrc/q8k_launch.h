@@ -245,14 +245,17 @@ struct AttendWeights {
     float keep;
     float* weights;
     int64_t stride;
-    int page_groups, splits;  // of the pages, of the rows
-    float* part;              // [splits][B][heads][page_groups * 256] where splits > 1
+    int groups, group_pages;  // groups of pages of a sequence, at most, and their pages
+    int splits;               // shares of the rows
+    uint4* rows;              // workspace: the rows' operands
+    float* part;              // [splits][B][heads][groups * group_pages * 64] where splits > 1
 };
 struct WeightsPlan {
-    int64_t page_groups, workgroups, ws_bytes;
+    bool many;  // rows: their operands go to the workspace
+    int64_t rows, tiles_max, groups, group_pages, workgroups, rows_bytes, ws_bytes;
     int splits, threads;
 };
-WeightsPlan weights_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D);
+WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D);
 hipError_t launch_attend_weights(int bits, int D, const WeightsPlan& p, AttendWeights w, void* ws, hipStream_t s);
 
 // Eviction.

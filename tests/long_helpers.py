@@ -281,7 +281,8 @@ def weights(bits, q, cu_q, cache, table_of_pages, kv_len, scale, window, rope, p
         L, n = int(kv_len[b]), int(cu_q[b + 1] - cu_q[b])
         got[b, :, :L] = 0
         if old is not None and L > n:
-            got[b, :, : L - n] = keep * old[b, :, : L - n].astype(np.float64)
+            # (keep is a float at the interface: 0.9 is 2.6e-8 of itself off, which no rounding of the kernel's is)
+            got[b, :, : L - n] = np.float64(np.float32(keep)) * old[b, :, : L - n].astype(np.float64)
     for b, q0, n, L, seen, k, v, x in _sequences(q, cu_q, bits, cache, table_of_pages, kv_len, scale, window, rope, pos,
                                                  pairs, D):
         rows = min(n, served) if served is not None else n
