@@ -89,17 +89,26 @@ __device__ __forceinline__ RowInfo stage_rows(const AttendWeights& w, const Sequ
 // 16 q + 4 g + e.
 __device__ __forceinline__ void add_row(const f4_t (&s4)[4], const float* scales, const RowInfo& row, int j0, int g,
                                         float (&sum)[4][4]) {
-    const bool whole = !__any(row.first > j0 || row.last < j0 + KV_PAGE - 1);
+    float t[4][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const f4_t ks = *reinterpret_cast<const f4_t*>(scales + 16 * q + 4 * g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s4[q][e] * ks[e], row.unit, -row.lse));
-            const int j = j0 + 16 * q + 4 * g + e;
-            sum[q][e] += whole || (j >= row.first && j <= row.last) ? x : 0.0f;
-        }
+        for (int e = 0; e < 4; ++e) t[q][e] = __builtin_fmaf(s4[q][e] * ks[e], row.unit, -row.lse);
     }
+    if (__any(row.first > j0 || row.last < j0 + KV_PAGE - 1)) {
+        // pages that some row sees only in part (what lies in unseen places may be anything)
+        const uint32_t from = j0 + 4 * g - row.first, most = row.last - row.first;
+        const bool none = row.last < row.first;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[q][e] = !none && from + (16 * q + e) <= most ? t[q][e] : -INFINITY;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[q][e] += __builtin_amdgcn_exp2f(t[q][e]);
 }
 // Over the sixteen lanes of a row, halving what a lane holds at each step: lane (col, g)
 // is left with token 16 q + 4 g + e, q = 2 (col / 4 % 2) + col / 8, e = col % 4.
