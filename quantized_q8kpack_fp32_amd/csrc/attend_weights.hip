@@ -50,8 +50,20 @@ struct RowInfo {
     int first, last;
 };
 
-// Sixteen rows of a head as the product's operand, by way of LDS, and their RowInfo
-// (in lane group 0).
+// Row `col` of a tile.
+__device__ __forceinline__ RowInfo info_of(const AttendWeights& w, const Sequence& seq, const Tile& tile, int h, int col) {
+    RowInfo o{1.0f, INFINITY, 0, -1};
+    if (tile.row0 + col < tile.rows) {
+        const TileRow tr = row_of_tile(w.a, tile, col);
+        const Span sp = span_of(w.a, seq, tr.tok);
+        const float lse = w.lse[q_row_of(w.a, seq, h, tr)];
+        // (a row of -inf sees nothing that counts)
+        o = RowInfo{1.0f, lse == -INFINITY ? INFINITY : lse * LOG2E, sp.first, sp.last};
+    }
+    return o;
+}
+
+// Sixteen rows of a head as the product's operand, by way of LDS, and their RowInfo.
 template <int D, int NQ>
 __device__ __forceinline__ RowInfo stage_rows(const AttendWeights& w, const Sequence& seq, int h, int t, int lane,
                                               float (*q_s)[D + 4], h8_t (&qf)[NQ][D / 32]) {
@@ -64,14 +76,7 @@ __device__ __forceinline__ RowInfo stage_rows(const AttendWeights& w, const Sequ
         const int i = lane + 64 * n;
         fetch_q<D>(a, seq, h, row_of_tile(a, tile, min(i / (D / 8), rows - 1 - tile.row0)), i % (D / 8), qi[n]);
     }
-    RowInfo o{1.0f, INFINITY, 0, -1};
-    if (tile.row0 + col < rows) {
-        const TileRow tr = row_of_tile(a, tile, col);
-        const Span sp = span_of(a, seq, tr.tok);
-        const float lse = w.lse[q_row_of(a, seq, h, tr)];
-        // (a row of -inf sees nothing that counts)
-        o = RowInfo{1.0f, lse == -INFINITY ? INFINITY : lse * LOG2E, sp.first, sp.last};
-    }
+    RowInfo o = info_of(w, seq, tile, h, col);
 #pragma unroll
     for (int n = 0; n < D / 32; ++n) fetch_turn(a, (lane + 64 * n) % (D / 8), qi[n]);
 #pragma unroll
@@ -146,7 +151,7 @@ template <int D, int BITS, int NQ, bool ONE>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kernel(AttendWeights w) {
     constexpr int KS = D / 32, TILES = ONE ? 1 : 4;
     const Attend& a = w.a;
-    __shared__ float qs[WAVES][ROWS][D + 4];
+    __shared__ float qs[ONE ? 1 : WAVES][ROWS][D + 4];
     __shared__ uint4 op[TILES][NQ][ONE ? 1 : KS][64];
     __shared__ RowInfo info[TILES][ROWS];
     __shared__ float scales[WAVES][KV_PAGE];
@@ -155,36 +160,58 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
     const int h = (int)(blockIdx.x % a.heads);
     const int64_t id = blockIdx.x / a.heads, b = id / w.groups;
     const int c0 = (int)(id % w.groups) * w.group_pages;
+    const int32_t* table = a.table + b * a.max_pages;
+    // (of the table's, whatever the length: it then needs not be waited for)
+    const int first_page = __builtin_amdgcn_readfirstlane(table[min((int64_t)c0 + wave, a.max_pages - 1)]);
     const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
     const int pages = (seq.len + KV_PAGE - 1) / KV_PAGE, c1 = min(pages, c0 + w.group_pages);
     if (c0 >= c1) return;
     constexpr int bytes = kv_record_of(BITS, D);
-    const int32_t* table = a.table + b * a.max_pages;
     PageKeys<D, BITS> keys;
     bool ok = false, next_ok;
     int p = c0 + wave;
     const auto page_at = [&](int p) { return __builtin_amdgcn_readfirstlane(p < c1 ? table[p] : -1); };
-    keys.fetch(page_record(a, page_at(p), h, bytes, ok), lane);
-    const int tiles = (seq.nq * a.group + ROWS - 1) / ROWS;
+    // a row's values and the first page set out together
+    const int rows = seq.nq * a.group, tiles = (rows + ROWS - 1) / ROWS;
     h8_t qf[NQ][KS];
     RowInfo mine{1.0f, INFINITY, 0, -1};
     if constexpr (ONE) {
-        if (tiles > 0) mine = stage_rows<D, NQ>(w, seq, h, 0, lane, qs[wave], qf);
-        if (tiles == 0)
+        constexpr int NI = (ROWS * (D / 8) + 64 * WAVES - 1) / (64 * WAVES);
+        const Tile tile = item_tile(a, seq, 0);
+        QueryItem qi[NI];
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const int i = threadIdx.x + 64 * WAVES * n, r = i / (D / 8);
+            if (r < rows && r < ROWS) fetch_q<D>(a, seq, h, row_of_tile(a, tile, r), i % (D / 8), qi[n]);
+        }
+        keys.fetch(page_record(a, p < c1 ? first_page : -1, h, bytes, ok), lane);
+        mine = info_of(w, seq, tile, h, col);
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+            const int i = threadIdx.x + 64 * WAVES * n, r = i / (D / 8), q = i % (D / 8);
+            if (r >= ROWS) continue;
+            if (r < rows) {
+                fetch_turn(a, q, qi[n]);
+                put_q(a, q, qi[n], qs[0][r]);
+            } else {
+                *reinterpret_cast<float4*>(&qs[0][r][8 * q]) = make_float4(0, 0, 0, 0);
+                *reinterpret_cast<float4*>(&qs[0][r][8 * q + 4]) = make_float4(0, 0, 0, 0);
+            }
+        }
+        __syncthreads();
+        mine.unit = query_operand<D, NQ>(a, qs[0][col], g, qf);
+    } else {
+        keys.fetch(page_record(a, p < c1 ? first_page : -1, h, bytes, ok), lane);
+        if (wave < tiles) {
+            mine = stage_rows<D, NQ>(w, seq, h, wave, lane, qs[wave], qf);
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int s = 0; s < KS; ++s) qf[n][s] = h8_t{};
-        if (g == 0 && wave == 0) info[0][col] = mine;
-    } else if (wave < tiles) {
-        mine = stage_rows<D, NQ>(w, seq, h, wave, lane, qs[wave], qf);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int s = 0; s < KS; ++s) op[wave][n][s][lane] = __builtin_bit_cast(uint4, qf[n][s]);
-        if (g == 0) info[wave][col] = mine;
+                for (int s = 0; s < KS; ++s) op[wave][n][s][lane] = __builtin_bit_cast(uint4, qf[n][s]);
+            if (g == 0) info[wave][col] = mine;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const int64_t row = (b * a.heads + h) * w.stride;
     for (; p < c1; p += WAVES) {
         const int j0 = p * KV_PAGE, j = j0 + token_of(col, g);
@@ -214,7 +241,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
                             s4[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q][t], qf[n][2 * s + t], s4[q], 0, 0, 0);
             }
             keys.fetch(rec, lane);
-            if (ok) add_row(s4, scales[wave], info[0][col], j0, g, sum);
+            if (ok) add_row(s4, scales[wave], mine, j0, g, sum);
         } else {
             h8_t kf[4][KS];
 #pragma unroll
@@ -292,10 +319,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
     id /= w.splits;
     const int64_t b = id / w.groups;
     const int c0 = (int)(id % w.groups) * (WAVES * PAGES);
+    const int32_t* table = a.table + b * a.max_pages;
+    int page[PAGES];  // of the table's, whatever the length: it then needs not be waited for
+#pragma unroll
+    for (int n = 0; n < PAGES; ++n)
+        page[n] = __builtin_amdgcn_readfirstlane(table[min((int64_t)c0 + wave * PAGES + n, a.max_pages - 1)]);
     const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
     if (c0 * KV_PAGE >= seq.len) return;
     constexpr int bytes = kv_record_of(BITS, D);
-    const int32_t* table = a.table + b * a.max_pages;
     // rows that may see one of these pages
     const int past = seq.len - seq.n, i0 = max(0, c0 * KV_PAGE - past);
     int64_t i1 = seq.nq;
@@ -314,16 +345,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
                                                      16, 16 * lane, (x % KB) * 1024, 0, 0);
         }
     };
-    if (t0 < t1) bring(t0, 0);
     h8_t kf[PAGES][4][KS];
     bool ok[PAGES];
     float sum[PAGES][4][4];
 #pragma unroll
     for (int n = 0; n < PAGES; ++n) {
         const int p = c0 + wave * PAGES + n;
-        const int page = __builtin_amdgcn_readfirstlane(p * KV_PAGE < seq.len ? table[p] : -1);
         PageKeys<D, BITS> keys;
-        keys.fetch(page_record(a, page, h, bytes, ok[n]), lane);
+        keys.fetch(page_record(a, p * KV_PAGE < seq.len ? page[n] : -1, h, bytes, ok[n]), lane);
+        if (n == 0 && t0 < t1) bring(t0, 0);
 #pragma unroll
         for (int s = 0; s < KS / 2; ++s)
 #pragma unroll
@@ -417,10 +447,13 @@ hipError_t weights_d(const WeightsPlan& p, const AttendWeights& w, hipStream_t s
 }  // namespace
 
 // Up to FEW_ROWS rows a head: one launch, a workgroup for each group of pages, as many
-// as make about FEW_WGS workgroups at the limits.  More: the rows' operands in the
+// as make about FEW_WGS workgroups at the limits (16 sequences of up to 8191 tokens, 32
+// heads over 8: 21.7 us, 512 of them 23.9, 4096 24.5).  More rows: their operands in the
 // workspace, groups of WAVES * 2 pages (of 256 values WAVES), and the rows in as many
-// shares as make MANY_WGS workgroups.
-constexpr int64_t FEW_ROWS = 64, FEW_WGS = 2048, MANY_WGS = 1024;
+// shares as make MANY_WGS workgroups (2 x 1000 tokens over 8001, 32 heads over 4: 234 us,
+// 1024 of them 249, 4096 236), each of LEAST_TILES tiles at least (the last 64 of 4 x up to
+// 16001, 32 over 8, 16 tiles: 44.8 us, by 8 48.5, by 4 59).
+constexpr int64_t FEW_ROWS = 64, FEW_WGS = 2048, MANY_WGS = 2048, LEAST_TILES = 16;
 
 WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {
     WeightsPlan p{};
@@ -440,7 +473,7 @@ WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, 
     p.workgroups = B * heads * p.groups;
     if (p.many) {
         int64_t splits = (MANY_WGS + p.workgroups - 1) / p.workgroups;
-        const int64_t most = (p.tiles_max + 15) / 16;  // sixteen tiles a share at least
+        const int64_t most = (p.tiles_max + LEAST_TILES - 1) / LEAST_TILES;
         splits = splits > most ? most : splits;
         p.splits = (int)splits;
         p.workgroups *= splits;
