@@ -3,17 +3,16 @@
 // others, those of the largest weights (equal ones by ascending index), in order;
 // what the cache holds of these moves to the front of the sequence's new pages.
 //
-// Two launches: the choice (one workgroup a sequence and head: the least weight kept
-// by its digits, eight bits a pass over the weights, then one pass in order), and
-// the move.  A page's places beyond the kept tokens are left as they were.
-#include "kv4_cache.h"
+// Two launches: the choice (one workgroup a sequence and head) and the move.  A page's
+// places beyond the kept tokens are left as they were.
+#include "attend.h"
 #include "q8k_launch.h"
 
 namespace q8k {
 
 namespace {
 
-constexpr int THREADS = 1024;
+constexpr int THREADS = 1024, WAVES = THREADS / 64;
 
 // Weights as whole numbers of the same order; NaN below all, -0 as 0.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -21,13 +20,21 @@ __device__ __forceinline__ uint32_t key_of(float v) {
     return v != v ? 0u : b >> 31 ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ int lanes_below(uint64_t mask, int lane) { return __popcll(mask & ((1ull << lane) - 1)); }
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
 
+// The least key that is kept, digit by digit from the top (11, 11 and 10 bits, each with
+// the counts of all its values), then one pass in order.  The weights are read once:
+// EACH a thread stay in registers (longer rows are read again, 1024 EACH at a time).
+template <int EACH>
 __global__ __launch_bounds__(THREADS) void kv_evict_choose_kernel(KvEvict a) {
-    __shared__ int hist[256], found[2], counts[2][2][THREADS / 64];
+    constexpr int CHUNK = THREADS * EACH;
+    __shared__ int hist[2048], sums[WAVES], found[2];
+    __shared__ uint32_t counts[EACH * WAVES + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x, b = row / a.heads;
-    int64_t l = a.kv_len[b];
+    const int64_t l = a.kv_len[b];
     const int len = (int)(l < 0 ? 0 : l > a.max_len ? a.max_len : l), budget = (int)a.budget;
     const float* in = a.weights + row * a.w_stride;
     float* out = a.out_weights ? a.out_weights + row * a.out_stride : nullptr;
@@ -41,56 +48,98 @@ __global__ __launch_bounds__(THREADS) void kv_evict_choose_kernel(KvEvict a) {
         return;
     }
     const int c0 = (int)a.first, c1 = len - (int)a.last, want = budget - (int)(a.first + a.last);
-    // the want-th largest key among the candidates, digit by digit
+    const int chunks = (len + CHUNK - 1) / CHUNK;
+    float v[EACH];
+    const auto load = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < EACH; ++r) {
+            const int i = c * CHUNK + r * THREADS + (int)threadIdx.x;
+            v[r] = i < len ? in[i] : 0.0f;
+        }
+    };
+    load(0);
     uint32_t prefix = 0, mask = 0;
     int rest = want;
     if (want > 0)
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = threadIdx.x; i < 256; i += THREADS) hist[i] = 0;
+        for (int digit = 0; digit < 3; ++digit) {
+            const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+            const uint32_t most = digit == 2 ? 1023u : 2047u;
+            hist[threadIdx.x] = hist[threadIdx.x + THREADS] = 0;
             __syncthreads();
-            for (int i = c0 + threadIdx.x; i < c1; i += THREADS) {
-                const uint32_t k = key_of(in[i]);
-                if ((k & mask) == prefix) atomicAdd(&hist[k >> shift & 255u], 1);
+            for (int c = 0; c < chunks; ++c) {
+                if (chunks > 1) load(c);
+#pragma unroll
+                for (int r = 0; r < EACH; ++r) {
+                    const int i = c * CHUNK + r * THREADS + (int)threadIdx.x;
+                    const uint32_t k = key_of(v[r]);
+                    if (i >= c0 && i < c1 && (k & mask) == prefix) atomicAdd(&hist[k >> shift & most], 1);
+                }
             }
             __syncthreads();
-            if (threadIdx.x == 0) {
-                int above = 0, d = 255;
-                while (above + hist[d] < rest) above += hist[d--];
-                found[0] = d;
-                found[1] = rest - above;
+            // thread t: the counts of values 2047 - 2 t and 2046 - 2 t, and of all above them
+            const int x = hist[2047 - 2 * threadIdx.x], y = hist[2046 - 2 * threadIdx.x], upto = wave_scan(x + y);
+            if (lane == 63) sums[wave] = upto;
+            __syncthreads();
+            int above = upto - x - y;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) above += w < wave ? sums[w] : 0;
+            if (above < rest && rest <= above + x + y) {
+                const bool second = rest > above + x;
+                found[0] = 2047 - 2 * (int)threadIdx.x - (second ? 1 : 0);
+                found[1] = rest - above - (second ? x : 0);
             }
             __syncthreads();
             prefix |= (uint32_t)found[0] << shift;
-            mask |= 255u << shift;
+            mask |= most << shift;
             rest = found[1];
-            __syncthreads();
         }
     // in order: all above it, and the first `rest` of those equal to it
     int done = 0, ties = 0;
-    for (int i0 = 0, turn = 0; i0 < len; i0 += THREADS, turn ^= 1) {
-        const int i = i0 + threadIdx.x;
-        const bool inside = i < len, fixed = inside && (i < c0 || i >= c1);
-        const float v = inside ? in[i] : 0.0f;
-        const uint32_t k = key_of(v);
-        const bool above = inside && (fixed || (want > 0 && k > prefix)), tie = inside && !fixed && want > 0 && k == prefix;
-        const uint64_t ma = __ballot(above), mt = __ballot(tie);
-        if (lane == 0) counts[turn][0][wave] = __popcll(ma), counts[turn][1][wave] = __popcll(mt);
+    for (int c = 0; c < chunks; ++c) {
+        if (chunks > 1) load(c);
+        uint64_t ma[EACH], mt[EACH];
+#pragma unroll
+        for (int r = 0; r < EACH; ++r) {
+            const int i = c * CHUNK + r * THREADS + (int)threadIdx.x;
+            const uint32_t k = key_of(v[r]);
+            const bool inside = i < len, fixed = i < c0 || i >= c1;
+            ma[r] = __ballot(inside && (fixed || (want > 0 && k > prefix)));
+            mt[r] = __ballot(inside && !fixed && want > 0 && k == prefix);
+            if (lane == 0) counts[r * WAVES + wave] = (uint32_t)__popcll(ma[r]) | (uint32_t)__popcll(mt[r]) << 16;
+        }
         __syncthreads();
-        int before = 0, tied = 0, all = 0, all_tied = 0;
-        for (int w = 0; w < THREADS / 64; ++w) {
-            const int x = counts[turn][0][w], y = counts[turn][1][w];
-            before += w < wave ? x : 0, tied += w < wave ? y : 0;
-            all += x, all_tied += y;
+        if (wave == 0) {
+            constexpr int N = EACH * WAVES / 64;
+            uint32_t n[N], sum = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) n[i] = counts[N * lane + i], sum += n[i];
+            uint32_t before = (uint32_t)wave_scan((int)sum) - sum;
+#pragma unroll
+            for (int i = 0; i < N; ++i) counts[N * lane + i] = before, before += n[i];
+            if (lane == 63) counts[EACH * WAVES] = before;
         }
-        const int t = ties + tied + lanes_below(mt, lane);  // ties before this one
-        const int at = done + before + lanes_below(ma, lane) + min(t, rest) - 0;
-        if (above || (tie && t < rest)) {
-            kept[at] = i;
-            if (out) out[at] = v;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < EACH; ++r) {
+            const int i = c * CHUNK + r * THREADS + (int)threadIdx.x;
+            const uint32_t before = counts[r * WAVES + wave];
+            const int t = ties + (int)(before >> 16) + lanes_below(mt[r]);
+            const int at = done + (int)(before & 0xffffu) + lanes_below(ma[r]) + min(t, rest);
+            if ((ma[r] >> lane & 1) || ((mt[r] >> lane & 1) && t < rest)) {
+                kept[at] = i;
+                if (out) out[at] = v[r];
+            }
         }
-        done += all;
-        ties += all_tied;
+        const uint32_t all = counts[EACH * WAVES];
+        done += (int)(all & 0xffffu);
+        ties += (int)(all >> 16);
+        __syncthreads();
     }
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad(uint32_t w) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, CTRL, 0xF, 0xF, false);
 }
 
 // The move.  What a page holds of its tokens is cut into parts, a wave each: lane t
@@ -98,8 +147,10 @@ __global__ __launch_bounds__(THREADS) void kv_evict_choose_kernel(KvEvict a) {
 // another: a kept token's new place is never behind its old one, so that a page's
 // tokens, all loaded before any is stored, come from places that no earlier page
 // was stored to.
-//   parts of 64 bytes a token of the keys' codes, of 32 rows of places (the values' codes
-//   and, in 4 bits, their factors), and one of the scales and the keys' factors
+//   parts of 64 bytes a token of the keys' codes, of 32 rows of places of the values'
+//   codes, and one of the scales and, in 4 bits, the factors
+// Four tokens of one group of four change places within the wave, so that their bytes of
+// a row leave as a word.
 template <int D, int BITS, bool IN_PLACE>
 __global__ __launch_bounds__(64) void kv_evict_move_kernel(KvEvict a) {
     constexpr int bytes = kv_record_of(BITS, D);
@@ -117,57 +168,83 @@ __global__ __launch_bounds__(64) void kv_evict_move_kernel(KvEvict a) {
     const int len = (int)(l < 0 ? 0 : l > a.max_len ? a.max_len : l), n = min(len, (int)a.budget);
     const int* kept = a.kept + (b * a.heads + h) * a.budget;
     const int P0 = IN_PLACE ? 0 : (int)(id % pages), P1 = IN_PLACE ? (n + KV_PAGE - 1) / KV_PAGE : P0 + 1;
+    const int place = BITS == 8 ? kv_place(lane) : kv4_place(lane);
     for (int P = P0; P < P1; ++P) {
         const int i = P * KV_PAGE + lane;
         const bool there = i < n;
-        const int from = there ? kept[i] : 0;
+        if (P * KV_PAGE >= n) return;
+        const int from = there ? kept[i] : 0, to_page = a.out_table[b * a.out_pages + P];
         if (IN_PLACE && __all(!there || from == i)) continue;
-        const int to_page = a.out_table[b * a.out_pages + P];
-        if (P * KV_PAGE >= n || to_page < 0 || to_page >= a.pages) continue;
+        if (to_page < 0 || to_page >= a.pages) continue;
         const int src_page = a.table[b * a.max_pages + from / KV_PAGE], token = from % KV_PAGE;
         const bool good = there && src_page >= 0 && src_page < a.pages;
-        const uint8_t* src = a.cache + ((int64_t)(good ? src_page : 0) * a.heads + h) * bytes;
+        const int64_t rec = good ? ((int64_t)src_page * a.heads + h) * bytes : -1;
         uint8_t* dst = a.cache + ((int64_t)to_page * a.heads + h) * bytes;
         if (part < KEYS) {
-            // four pieces of 16 bytes; in 4 bits and 64 values of 8
+            // four lanes a token, sixteen tokens at a time; 16 bytes a lane, in 4 bits and 64 values 8
             constexpr bool small = BITS == 4 && D == 64;
-            const auto at = [&](int t, int c) {
-                if (BITS == 8) return part * 4096 + t * 64 + c * 16;
-                if (small) return (t >> 5) * 1024 + (t & 15) * 64 + c * 16 + ((t >> 4) & 1) * 8;
-                return ((t >> 4) * (D / 128) + part) * 1024 + (t & 15) * 64 + c * 16;
+            const int piece = lane & 3;
+            const auto at = [&](int t) {
+                if (BITS == 8) return part * 4096 + t * 64 + piece * 16;
+                if (small) return (t >> 5) * 1024 + (t & 15) * 64 + piece * 16 + ((t >> 4) & 1) * 8;
+                return ((t >> 4) * (D / 128) + part) * 1024 + (t & 15) * 64 + piece * 16;
             };
             uint4 v[4];
+            int64_t r[4];
+            int t[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int who = 16 * c + (lane >> 2);
+                r[c] = __shfl(rec, who, 64);
+                t[c] = __shfl(token, who, 64);
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 v[c] = make_uint4(0, 0, 0, 0);
-                if (!good) continue;
+                if (r[c] < 0) continue;
                 if constexpr (small) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(src + at(token, c));
+                    const uint2 x = *reinterpret_cast<const uint2*>(a.cache + r[c] + at(t[c]));
                     v[c].x = x.x, v[c].y = x.y;
                 } else {
-                    v[c] = *reinterpret_cast<const uint4*>(src + at(token, c));
+                    v[c] = *reinterpret_cast<const uint4*>(a.cache + r[c] + at(t[c]));
                 }
             }
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (there)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if constexpr (small)
-                        *reinterpret_cast<uint2*>(dst + at(lane, c)) = make_uint2(v[c].x, v[c].y);
-                    else
-                        *reinterpret_cast<uint4*>(dst + at(lane, c)) = v[c];
-                }
+            for (int c = 0; c < 4; ++c) {
+                const int who = 16 * c + (lane >> 2);
+                if (P * KV_PAGE + who >= n) continue;
+                if constexpr (small)
+                    *reinterpret_cast<uint2*>(dst + at(who)) = make_uint2(v[c].x, v[c].y);
+                else
+                    *reinterpret_cast<uint4*>(dst + at(who)) = v[c];
+            }
         } else if (part < KEYS + VALUES) {
             const int base = (BITS == 8 ? KV_PAGE * D : KV4_V(D)) + (part - KEYS) * ROWS * KV_PAGE;
-            const int p = BITS == 8 ? kv_place(token) : kv4_place(token), to = BITS == 8 ? kv_place(lane) : kv4_place(lane);
+            const uint8_t* src = a.cache + (good ? rec : 0) + base + (BITS == 8 ? kv_place(token) : kv4_place(token));
             uint32_t v[ROWS];
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) v[r] = good ? src[base + r * KV_PAGE + p] : 0;
+            for (int r = 0; r < ROWS; ++r) v[r] = good ? src[r * KV_PAGE] : 0;
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (there)
+            if (P * KV_PAGE + KV_PAGE <= n) {
+                // the four lanes of a group hold the bytes of places p .. p + 3, in their order 0, 1, 2, 3 or (4 bits)
+                // 0, 2, 1, 3: lane k of places' order is left with the word of row 4 r + k
+                const bool odd = place & 1, upper = place & 2;
+                const uint32_t one = odd ? 0x03070105u : 0x06020400u, two = upper ? 0x03020706u : 0x05040100u;
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r) dst[base + r * KV_PAGE + to] = (uint8_t)v[r];
+                for (int r = 0; r < ROWS / 4; ++r) {
+                    uint32_t w = v[4 * r] | v[4 * r + 1] << 8 | v[4 * r + 2] << 16 | v[4 * r + 3] << 24;
+                    // with the neighbour in the places' lowest bit: bytes (mine, its) of rows 0 and 2, or 1 and 3
+                    w = __builtin_amdgcn_perm(BITS == 8 ? quad<0xB1>(w) : quad<0x4E>(w), w, one);
+                    w = __builtin_amdgcn_perm(BITS == 8 ? quad<0x4E>(w) : quad<0xB1>(w), w, two);
+                    *reinterpret_cast<uint32_t*>(dst + base + (4 * r + (place & 3)) * KV_PAGE + (place & ~3)) = w;
+                }
+            } else if (there) {
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) dst[base + r * KV_PAGE + place] = (uint8_t)v[r];
+            }
         } else {
+            const uint8_t* src = a.cache + (good ? rec : 0);
             const float* s = reinterpret_cast<const float*>(src + bytes - 8 * KV_PAGE) + token;
             const float k = good ? s[0] : 0.0f, v = good ? s[KV_PAGE] : 0.0f;
             uint32_t kf[BITS == 4 ? D / 32 : 1], vf[BITS == 4 ? D / 32 : 1];
@@ -186,7 +263,7 @@ __global__ __launch_bounds__(64) void kv_evict_move_kernel(KvEvict a) {
 #pragma unroll
                     for (int y = 0; y < D / 32; ++y) {
                         dst[kv4_key_factor<D>(lane, y)] = (uint8_t)kf[y];
-                        dst[KV4_VF(D) + y * KV_PAGE + kv4_place(lane)] = (uint8_t)vf[y];
+                        dst[KV4_VF(D) + y * KV_PAGE + place] = (uint8_t)vf[y];
                     }
             }
         }
@@ -215,7 +292,10 @@ int64_t evict_workgroups(int bits, int D, int64_t B, int64_t heads, int64_t budg
 int evict_threads() { return THREADS; }
 
 hipError_t launch_kv_evict(int bits, int D, const KvEvict& a, bool in_place, hipStream_t s) {
-    Q8K_LAUNCH(kv_evict_choose_kernel, dim3((unsigned)(a.B * a.heads)), dim3(THREADS), 0, s, a);
+    if (a.max_len <= 4 * THREADS)
+        Q8K_LAUNCH((kv_evict_choose_kernel<4>), dim3((unsigned)(a.B * a.heads)), dim3(THREADS), 0, s, a);
+    else
+        Q8K_LAUNCH((kv_evict_choose_kernel<16>), dim3((unsigned)(a.B * a.heads)), dim3(THREADS), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (bits == 8) return D == 64 ? move_d<64, 8>(a, in_place, s) : D == 128 ? move_d<128, 8>(a, in_place, s) : move_d<256, 8>(a, in_place, s);
