@@ -19,6 +19,11 @@ namespace {
 
 constexpr int ROWS = 16;
 
+__device__ __forceinline__ h2_t h2(uint32_t w) { return __builtin_bit_cast(h2_t, w); }
+__device__ __forceinline__ uint2 pair_of(h2_t a, h2_t b) {
+    return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+}
+
 // Probabilities enter the second product as fp16 pieces of p * vscale / R *
 // 2^15, R a power of two at least the largest vscale that the row has seen in
 // this wave: at most 2^15 (fp16 ends at 65504), and what fp16's smallest step
@@ -46,7 +51,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     __shared__ float red[WAVES][ROWS][2];
     __shared__ float acc_s[WAVES][ROWS][DV + 4];
     __shared__ float scales[WAVES][2 * KV_PAGE];
-    __shared__ __attribute__((aligned(16))) uint32_t factors[WAVES][BITS == 4 ? DV / 2 : 4];  // of a page's values
+    // of a page's values, for each word of codes two pairs; and what comes off (kv4_cache.h)
+    __shared__ __attribute__((aligned(16))) uint2 factors[WAVES][3][BITS == 4 ? DV / 2 : 2];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int h = (int)(blockIdx.x % a.heads);
@@ -70,6 +76,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
         if (i < ROWS * (D / 8) && tile.row0 + r < tile.rows)
             fetch_q<D>(a, seq, h, row_of_tile(a, tile, r), i % (D / 8), qi[n]);
     }
+    const Widen masks;
     const int32_t* pages = a.table + it.b * a.max_pages;
     const int lane_off = col * 64 + g * 16;
     // A page's codes and scales on their way, one page ahead of the arithmetic:
@@ -80,7 +87,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
     // Reads go through a buffer descriptor of one record; a page that selects
     // nothing has an empty one, whose reads return zeros and touch no memory.
     // 4 bits: KB blocks of two pieces of the keys, one of two row blocks of the values; the
-    // factors of a lane's pieces, and those of the values, a word or two a lane, by LDS.
+    // factors of a lane's pieces, and those of the values, a word or two a lane, which become
+    // pairs with what comes off once for the wave, by LDS (8 x 65537 tokens 101 us; by every
+    // lane for itself 120, the pairs alone by LDS 104).
     constexpr int KB = D / 32, VF = DV / 128 < 1 ? 1 : DV / 128;
     uint4 kraw[4][KS / 2], vraw[DB];
     uint4 kraw4[KB], vraw4[DB / 2];
@@ -166,8 +175,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
                         const int e = q * (D / 64) + s;
                         const uint4 c = kraw4[e >> 1];
                         const Factors f = kv4_key_factors(kfac[e >> 2] >> (8 * (e & 3)) & 255u);
-                        kf[q][0] = kv4_widen_keys(e & 1 ? c.z : c.x, f);
-                        kf[q][1] = kv4_widen_keys(e & 1 ? c.w : c.y, f);
+                        kf[q][0] = kv4_widen_keys(masks, e & 1 ? c.z : c.x, f);
+                        kf[q][1] = kv4_widen_keys(masks, e & 1 ? c.w : c.y, f);
                     }
                 }
 #pragma unroll
@@ -192,7 +201,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
         sc[KV_PAGE + lane] = vsc;
         if constexpr (BITS == 4) {
 #pragma unroll
-            for (int i = 0; i < VF; ++i) factors[wave][VF * (lane % (DV / 2 / VF)) + i] = vfac[i];
+            for (int i = 0; i < VF; ++i) {
+                const FactorPairs f = kv4_value_factors(vfac[i]);
+                const int at = VF * (lane % (DV / 2 / VF)) + i;
+                factors[wave][0][at] = pair_of(f.first.f, f.second.f);
+                factors[wave][1][at] = pair_of(f.first.low, f.second.low);
+                factors[wave][2][at] = pair_of(f.first.high, f.second.high);
+            }
         }
         float vs[4][4];
 #pragma unroll
@@ -272,9 +287,18 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void attend_decode_ke
                     vf[d][1] = codes_f16(vraw[d0 + d].z, vraw[d0 + d].w);
                 } else if (d % 2 == 0) {
                     const uint4 c = vraw4[(d0 + d) / 2];
-                    const uint4 f = *reinterpret_cast<const uint4*>(&factors[wave][(d0 + d) * 8 + 4 * g]);
-                    kv4_widen_values(c.x, c.y, f.x, f.y, vf[d][0], vf[d + 1][0]);
-                    kv4_widen_values(c.z, c.w, f.z, f.w, vf[d][1], vf[d + 1][1]);
+                    const int at = (d0 + d) * 8 + 4 * g;
+                    FactorPairs f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(&factors[wave][0][at + i]);
+                        const uint4 y = *reinterpret_cast<const uint4*>(&factors[wave][1][at + i]);
+                        const uint4 z = *reinterpret_cast<const uint4*>(&factors[wave][2][at + i]);
+                        f[i] = {{h2(x.x), h2(y.x), h2(z.x)}, {h2(x.y), h2(y.y), h2(z.y)}};
+                        f[i + 1] = {{h2(x.z), h2(y.z), h2(z.z)}, {h2(x.w), h2(y.w), h2(z.w)}};
+                    }
+                    kv4_widen_values(masks, c.x, c.y, f[0], f[1], vf[d][0], vf[d + 1][0]);
+                    kv4_widen_values(masks, c.z, c.w, f[2], f[3], vf[d][1], vf[d + 1][1]);
                 }
             }
 #pragma unroll

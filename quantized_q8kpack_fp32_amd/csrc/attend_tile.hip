@@ -116,6 +116,7 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
     // 0 the keys' scales and wave 1 the values'.  Reads go through a buffer
     // descriptor of one record, an empty one where the page selects nothing.
     // Page numbers come 64 at a time, one a lane.
+    const Widen masks;
     const int32_t* pages = a.table + it.b * a.max_pages;
     int ids = p0 + lane < p1 ? pages[p0 + lane] : -1;
     const int lane_off = col * 64 + g * 16;
@@ -166,16 +167,16 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
                     for (int b = 0; b < 2; ++b) {
                         const int p = 2 * i + b, q = p / (D / 64), s = p % (D / 64);
                         const Factors x = kv4_key_factors(b ? f.x >> 8 : f.x & 255u);
-                        o.k[q][2 * s][lane] = __builtin_bit_cast(uint4, kv4_widen_keys(b ? r.z : r.x, x));
-                        o.k[q][2 * s + 1][lane] = __builtin_bit_cast(uint4, kv4_widen_keys(b ? r.w : r.y, x));
+                        o.k[q][2 * s][lane] = __builtin_bit_cast(uint4, kv4_widen_keys(masks, b ? r.z : r.x, x));
+                        o.k[q][2 * s + 1][lane] = __builtin_bit_cast(uint4, kv4_widen_keys(masks, b ? r.w : r.y, x));
                     }
                 } else {
                     const int e = i - D / 32;
                     h8_t va, vb;
-                    kv4_widen_values(r.x, r.y, f.x, f.y, va, vb);
+                    kv4_widen_values(masks, r.x, r.y, kv4_value_factors(f.x), kv4_value_factors(f.y), va, vb);
                     o.v[2 * e][0][lane] = __builtin_bit_cast(uint4, va);
                     o.v[2 * e + 1][0][lane] = __builtin_bit_cast(uint4, vb);
-                    kv4_widen_values(r.z, r.w, f.z, f.w, va, vb);
+                    kv4_widen_values(masks, r.z, r.w, kv4_value_factors(f.z), kv4_value_factors(f.w), va, vb);
                     o.v[2 * e][1][lane] = __builtin_bit_cast(uint4, va);
                     o.v[2 * e + 1][1][lane] = __builtin_bit_cast(uint4, vb);
                 }

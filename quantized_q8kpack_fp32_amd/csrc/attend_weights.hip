@@ -28,7 +28,7 @@ struct PageKeys {
         scale = __builtin_bit_cast(float, load4(rec, kv_record_of(BITS, D) - 8 * KV_PAGE + 4 * lane));
     }
     // of 16 tokens 16 q and on, steps 2 s and 2 s + 1
-    __device__ __forceinline__ void widen(int q, int s, h8_t& a, h8_t& b) const {
+    __device__ __forceinline__ void widen(const Widen& masks, int q, int s, h8_t& a, h8_t& b) const {
         if constexpr (BITS == 8) {
             const uint4 c = raw[4 * s + q];
             a = codes_f16(c.x, c.y);
@@ -37,8 +37,8 @@ struct PageKeys {
             const int p = q * (D / 64) + s;
             const uint4 c = raw[p >> 1];
             const Factors f = kv4_key_factors(fac[p >> 2] >> (8 * (p & 3)) & 255u);
-            a = kv4_widen_keys(p & 1 ? c.z : c.x, f);
-            b = kv4_widen_keys(p & 1 ? c.w : c.y, f);
+            a = kv4_widen_keys(masks, p & 1 ? c.z : c.x, f);
+            b = kv4_widen_keys(masks, p & 1 ? c.w : c.y, f);
         }
     }
 };
@@ -167,6 +167,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
     const int pages = (seq.len + KV_PAGE - 1) / KV_PAGE, c1 = min(pages, c0 + w.group_pages);
     if (c0 >= c1) return;
     constexpr int bytes = kv_record_of(BITS, D);
+    const Widen masks;
     PageKeys<D, BITS> keys;
     bool ok = false, next_ok;
     int p = c0 + wave;
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
             for (int s = 0; s < KS / 2; ++s) {
                 h8_t kf[4][2];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) keys.widen(q, s, kf[q][0], kf[q][1]);
+                for (int q = 0; q < 4; ++q) keys.widen(masks, q, s, kf[q][0], kf[q][1]);
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
 #pragma unroll
             for (int s = 0; s < KS / 2; ++s)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) keys.widen(q, s, kf[q][2 * s], kf[q][2 * s + 1]);
+                for (int q = 0; q < 4; ++q) keys.widen(masks, q, s, kf[q][2 * s], kf[q][2 * s + 1]);
             keys.fetch(rec, lane);
             if (ok)
                 for (int i = 0; i < tiles; ++i) {
@@ -345,6 +346,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
                                                      16, 16 * lane, (x % KB) * 1024, 0, 0);
         }
     };
+    const Widen masks;
     h8_t kf[PAGES][4][KS];
     bool ok[PAGES];
     float sum[PAGES][4][4];
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
 #pragma unroll
         for (int s = 0; s < KS / 2; ++s)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) keys.widen(q, s, kf[n][q][2 * s], kf[n][q][2 * s + 1]);
+            for (int q = 0; q < 4; ++q) keys.widen(masks, q, s, kf[n][q][2 * s], kf[n][q][2 * s + 1]);
         scales[wave][n][lane] = keys.scale;
 #pragma unroll
         for (int q = 0; q < 4; ++q)

@@ -124,32 +124,49 @@ __device__ __forceinline__ Factors kv4_factors(uint32_t two) {
     r.high = r.f * (_Float16)-24.0f;
     return r;
 }
-__device__ __forceinline__ uint32_t kv4_low(uint32_t w, const Factors& f) {
-    const h2_t a = __builtin_bit_cast(h2_t, (w & 0x003c003cu) | 0x5c005c00u);
+// The masks and exponents from registers: a mask and an exponent then take one
+// instruction, with literals two (no instruction takes two of them).
+struct Widen {
+    uint32_t low_mask = 0x003c003cu, low = 0x5c005c00u, high_mask = 0x03c003c0u, high = 0x4c004c00u;
+    __device__ __forceinline__ Widen() {
+        asm("" : "+s"(low_mask), "+s"(high_mask));
+        asm("" : "+v"(low), "+v"(high));
+    }
+};
+__device__ __forceinline__ uint32_t kv4_low(const Widen& m, uint32_t w, const Factors& f) {
+    const h2_t a = __builtin_bit_cast(h2_t, (w & m.low_mask) | m.low);
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(a, f.f, f.low));
 }
-__device__ __forceinline__ uint32_t kv4_high(uint32_t w, const Factors& f) {
-    const h2_t a = __builtin_bit_cast(h2_t, (w & 0x03c003c0u) | 0x4c004c00u);
+__device__ __forceinline__ uint32_t kv4_high(const Widen& m, uint32_t w, const Factors& f) {
+    const h2_t a = __builtin_bit_cast(h2_t, (w & m.high_mask) | m.high);
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(a, f.f, f.high));
 }
 // A key's word: eight values of one group.  `factor`: the factor's byte.
 __device__ __forceinline__ Factors kv4_key_factors(uint32_t factor) { return kv4_factors(factor * 0x00400040u); }
-__device__ __forceinline__ h8_t kv4_widen_keys(uint32_t w, const Factors& f) {
+__device__ __forceinline__ h8_t kv4_widen_keys(const Widen& m, uint32_t w, const Factors& f) {
     const uint32_t r = __builtin_amdgcn_alignbit(w, w, 8);
-    return __builtin_bit_cast(h8_t, make_uint4(kv4_low(w, f), kv4_high(w, f), kv4_low(r, f), kv4_high(r, f)));
+    return __builtin_bit_cast(h8_t, make_uint4(kv4_low(m, w, f), kv4_high(m, w, f), kv4_low(m, r, f), kv4_high(m, r, f)));
 }
-// Two words of values (eight tokens) and of their factors: the operands of values c and
+// A word of the values' factors (four tokens): those of its pairs (0, 1) and (2, 3).
+struct FactorPairs {
+    Factors first, second;
+};
+__device__ __forceinline__ FactorPairs kv4_value_factors(uint32_t f) {
+    return {kv4_factors((f << 6) & 0x3fc03fc0u), kv4_factors((f >> 2) & 0x3fc03fc0u)};
+}
+// Two words of values (eight tokens) and their factors: the operands of values c and
 // 16 + c of a group.
-__device__ __forceinline__ void kv4_widen_values(uint32_t w0, uint32_t w1, uint32_t f0, uint32_t f1, h8_t& a, h8_t& b) {
+__device__ __forceinline__ void kv4_widen_values(const Widen& m, uint32_t w0, uint32_t w1, const FactorPairs& f0,
+                                                 const FactorPairs& f1, h8_t& a, h8_t& b) {
     uint32_t x[4], y[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t w = i ? w1 : w0, f = i ? f1 : f0;
-        const Factors p = kv4_factors((f << 6) & 0x3fc03fc0u), q = kv4_factors((f >> 2) & 0x3fc03fc0u);
-        x[2 * i] = kv4_low(w << 2, p);
-        y[2 * i] = kv4_high(w << 2, p);
-        x[2 * i + 1] = kv4_low(w >> 6, q);
-        y[2 * i + 1] = kv4_high(w >> 6, q);
+        const uint32_t w = i ? w1 : w0;
+        const Factors &p = i ? f1.first : f0.first, &q = i ? f1.second : f0.second;
+        x[2 * i] = kv4_low(m, w << 2, p);
+        y[2 * i] = kv4_high(m, w << 2, p);
+        x[2 * i + 1] = kv4_low(m, w >> 6, q);
+        y[2 * i + 1] = kv4_high(m, w >> 6, q);
     }
     a = __builtin_bit_cast(h8_t, make_uint4(x[0], x[1], x[2], x[3]));
     b = __builtin_bit_cast(h8_t, make_uint4(y[0], y[1], y[2], y[3]));
