@@ -74,7 +74,7 @@ def test_append_odd_rows(q, D, T):
     row[4] = 0
     row[5] *= np.float32(1e-42)
     row[6, :, 32:] *= np.float32(1e-6)
-    row[7, :, :32] *= np.float32(2e38)
+    row[7, :, :32] = np.sign(row[7, :, :32]) * g.uniform(0, 3e38, (2, 32)).astype(np.float32)
     row[8, :, 33:] = 0
     row[9] = np.float32(-3.0)
     row[10, :, ::2] = 0.5  # ties
@@ -186,7 +186,7 @@ KINDS = [(64, "f32", 64), (64, "bf16", 16), (64, "bf16", 0), (128, "f16", 128), 
     ([70, 200], [1, 2], 150, 200, 0), ([1200, 700], [1, 2], 8, 2200, 0), ([1025, 300], [1, 3], 80, 1025, 500),
     # tiles of 64 rows, whole and in chunks; of 128 rows, whole and in chunks
     ([200, 140], [150, 70], 32, 200, 0), ([900, 300], [65, 33], 16, 2200, 100), ([129, 140], [129, 70], 64, 140, 100),
-    ([900, 300], [128, 100], 32, 3200, 0),
+    ([900, 300], [128, 100], 32, 3200, 0), ([2300, 300], [100, 20], 36, 2300, 0),
 ])
 def test_attend_every_kernel(q, D, dtype, rot, lens, news, H, max_len, window):
     compare(q, D, dtype, H if news[0] > 3 else 3 * H, H, lens, news, window, rot, max_len=max_len, more_pages=55)

@@ -115,7 +115,7 @@ def test_weights(q, bits, D, dtype, Hq, H, lens, news, window, rot, pairs, keep)
 @pytest.mark.parametrize("D,dtype,rot", [(64, "f32", 64), (64, "bf16", 0), (128, "f16", 64), (128, "bf16", 0),
                                          (256, "f32", 0), (256, "bf16", 0)])
 @pytest.mark.parametrize("lens,news,H,G,max_len", [
-    ([70, 200], [1, 2], 2, 4, 2000), ([2500, 90, 700], [1, 1, 1], 2, 1, 2500), ([600, 300], [17, 40], 1, 4, 900),
+    ([70, 200], [1, 2], 2, 4, 2000), ([2500, 90, 700], [1, 1, 1], 2, 1, 2500), ([600, 300], [17, 40], 1, 4, 900), ([600, 300], [3, 12], 2, 4, 900),
     ([1000], [200], 1, 8, 1000), ([130, 250, 77], [130, 70, 77], 4, 2, 300),
 ])
 def test_weights_few_and_many_rows(q, bits, D, dtype, rot, lens, news, H, G, max_len):
