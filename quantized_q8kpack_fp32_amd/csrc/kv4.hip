@@ -53,10 +53,8 @@ __device__ __forceinline__ void natural_order(float* row_s, int oa, int ob, int 
 // values, 2 and 3 the others, which lie beside them.  Lane i makes the bytes of values
 // 8 (i % 2) + 4 (i / 2) and on of the first sixteen.
 __device__ __forceinline__ uint32_t value_bytes(float4 x, float4 y, float inverse, int item) {
-    const uint32_t lo = kv4_code(x.x, inverse) | kv4_code(x.y, inverse) << 8 | kv4_code(x.z, inverse) << 16 |
-                        kv4_code(x.w, inverse) << 24;
-    const uint32_t hi = kv4_code(y.x, inverse) | kv4_code(y.y, inverse) << 8 | kv4_code(y.z, inverse) << 16 |
-                        kv4_code(y.w, inverse) << 24;
+    const uint64_t codes = kv4_codes8<0, 8, 16, 24, 32, 40, 48, 56>(x, y, inverse);
+    const uint32_t lo = (uint32_t)codes, hi = (uint32_t)(codes >> 32);
     const uint32_t lo2 = other_half(lo), hi2 = other_half(hi);
     return item & 2 ? hi2 | hi << 4 : lo | lo2 << 4;
 }

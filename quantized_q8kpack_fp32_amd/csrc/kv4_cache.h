@@ -71,18 +71,40 @@ __device__ __forceinline__ float kv4_inverse(uint32_t f, float scale) {
     const float step = kv4_factor_value(f) * scale;
     return f == 0 || !(scale < INFINITY) ? 0.0f : 1.0f / step;
 }
-// code + 8 of one value: kv_codes4's rule with 7 in the place of 127.
-__device__ __forceinline__ uint32_t kv4_code(float x, float inverse) {
+// code + 8 of eight values (x and y: 0-3 and 4-7), value i's at bit SHIFT_i: kv_codes4's
+// rule with 7 in the place of 127.  1.5 * 2^23 + 8 rounds a product to a whole number,
+// half to even, and leaves code + 8 in the low bits of the sum, above constant ones, which
+// come off all at once.
+constexpr float KV4_ROUND = 12582920.0f;
+template <int S0, int S1, int S2, int S3, int S4, int S5, int S6, int S7>
+__device__ __forceinline__ uint64_t kv4_codes8(float4 a, float4 b, float inverse) {
 #pragma clang fp contract(off)
-    if (!(inverse < INFINITY)) return x > 0.0f ? 15u : x < 0.0f ? 1u : 8u;
-    // 1.5 * 2^23 leaves the rounded product in the low bits of the sum; a NaN has code 0
-    return (__builtin_bit_cast(uint32_t, fmaxf(x * inverse + 12582912.0f, 0.0f)) + 8u) & 15u;
+    float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    constexpr int at[8] = {S0, S1, S2, S3, S4, S5, S6, S7};
+    constexpr uint32_t top = 0x4b400000u;
+    uint32_t w[2] = {0, 0}, off[2] = {0, 0};
+    // a NaN has code 0, and so has an infinity (whose row's inverse is 0)
+    const auto odd = [](float x, float y) { return !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY); };
+    if (__any(odd(v[0], v[1]) || odd(v[2], v[3]) || odd(v[4], v[5]) || odd(v[6], v[7])))
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        w[at[i] / 32] += __builtin_bit_cast(uint32_t, v[i] * inverse + KV4_ROUND) << (at[i] % 32);
+        off[at[i] / 32] += top << (at[i] % 32);
+    }
+    w[0] -= off[0];
+    w[1] -= off[1];
+    if (!(inverse < INFINITY)) {
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[at[i] / 32] |= (v[i] > 0.0f ? 15u : v[i] < 0.0f ? 1u : 8u) << (at[i] % 32);
+    }
+    return (uint64_t)w[1] << 32 | w[0];
 }
-// The word of eight values (x and y: 0-3 and 4-7).
+// The word of eight values of a key.
 __device__ __forceinline__ uint32_t kv4_key_codes(float4 x, float4 y, float inverse) {
-    const uint32_t w = kv4_code(x.x, inverse) | kv4_code(x.y, inverse) << 16 | kv4_code(x.z, inverse) << 4 |
-                       kv4_code(x.w, inverse) << 20 | kv4_code(y.x, inverse) << 8 | kv4_code(y.y, inverse) << 24 |
-                       kv4_code(y.z, inverse) << 12 | kv4_code(y.w, inverse) << 28;
+    const uint32_t w = (uint32_t)kv4_codes8<0, 16, 4, 20, 8, 24, 12, 28>(x, y, inverse);
     return w << 2 | w >> 30;
 }
 // The codes (as numbers) of a key's word.

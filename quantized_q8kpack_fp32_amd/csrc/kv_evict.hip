@@ -30,15 +30,24 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 template <int EACH>
 __global__ __launch_bounds__(THREADS) void kv_evict_choose_kernel(KvEvict a) {
     constexpr int CHUNK = THREADS * EACH;
-    __shared__ int hist[2048], sums[WAVES], found[2];
+    __shared__ int hist[2048], sums[WAVES], found[3];
     __shared__ uint32_t counts[EACH * WAVES + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x, b = row / a.heads;
     const int64_t l = a.kv_len[b];
-    const int len = (int)(l < 0 ? 0 : l > a.max_len ? a.max_len : l), budget = (int)a.budget;
     const float* in = a.weights + row * a.w_stride;
     float* out = a.out_weights ? a.out_weights + row * a.out_stride : nullptr;
     int* kept = a.kept + row * a.budget;
+    float v[EACH];
+    const auto load = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < EACH; ++r) {
+            const int64_t i = (int64_t)c * CHUNK + r * THREADS + (int)threadIdx.x;
+            v[r] = i < a.max_len ? in[i] : 0.0f;  // (whatever the length, which needs not be waited for)
+        }
+    };
+    load(0);
+    const int len = (int)(l < 0 ? 0 : l > a.max_len ? a.max_len : l), budget = (int)a.budget;
     if (row % a.heads == 0 && threadIdx.x == 0) a.new_len[b] = min(len, budget);
     if (len <= budget) {
         for (int i = threadIdx.x; i < budget; i += THREADS) {
@@ -49,15 +58,6 @@ __global__ __launch_bounds__(THREADS) void kv_evict_choose_kernel(KvEvict a) {
     }
     const int c0 = (int)a.first, c1 = len - (int)a.last, want = budget - (int)(a.first + a.last);
     const int chunks = (len + CHUNK - 1) / CHUNK;
-    float v[EACH];
-    const auto load = [&](int c) {
-#pragma unroll
-        for (int r = 0; r < EACH; ++r) {
-            const int i = c * CHUNK + r * THREADS + (int)threadIdx.x;
-            v[r] = i < len ? in[i] : 0.0f;
-        }
-    };
-    load(0);
     uint32_t prefix = 0, mask = 0;
     int rest = want;
     if (want > 0)
@@ -87,11 +87,18 @@ __global__ __launch_bounds__(THREADS) void kv_evict_choose_kernel(KvEvict a) {
                 const bool second = rest > above + x;
                 found[0] = 2047 - 2 * (int)threadIdx.x - (second ? 1 : 0);
                 found[1] = rest - above - (second ? x : 0);
+                found[2] = second ? y : x;
             }
             __syncthreads();
             prefix |= (uint32_t)found[0] << shift;
             mask |= most << shift;
             rest = found[1];
+            if (found[2] == rest) {
+                // all of them are kept: those above what is just below
+                prefix -= 1;
+                rest = 0;
+                break;
+            }
         }
     // in order: all above it, and the first `rest` of those equal to it
     int done = 0, ties = 0;
@@ -164,17 +171,16 @@ __global__ __launch_bounds__(64) void kv_evict_move_kernel(KvEvict a) {
     id /= a.heads;
     const int64_t pages = (a.budget + KV_PAGE - 1) / KV_PAGE;
     const int64_t b = IN_PLACE ? id : id / pages;
-    const int64_t l = a.kv_len[b];
-    const int len = (int)(l < 0 ? 0 : l > a.max_len ? a.max_len : l), n = min(len, (int)a.budget);
     const int* kept = a.kept + (b * a.heads + h) * a.budget;
-    const int P0 = IN_PLACE ? 0 : (int)(id % pages), P1 = IN_PLACE ? (n + KV_PAGE - 1) / KV_PAGE : P0 + 1;
+    const int P0 = IN_PLACE ? 0 : (int)(id % pages), P1 = IN_PLACE ? (int)pages : P0 + 1;
     const int place = BITS == 8 ? kv_place(lane) : kv4_place(lane);
     for (int P = P0; P < P1; ++P) {
-        const int i = P * KV_PAGE + lane;
-        const bool there = i < n;
-        if (P * KV_PAGE >= n) return;
-        const int from = there ? kept[i] : 0, to_page = a.out_table[b * a.out_pages + P];
-        if (IN_PLACE && __all(!there || from == i)) continue;
+        const int i = P * KV_PAGE + lane, old = i < a.budget ? kept[i] : -1;
+        const int to_page = a.out_table[b * a.out_pages + P];
+        const bool there = old >= 0, whole = __all(there);
+        if (!__any(there)) return;
+        if (IN_PLACE && __all(!there || old == i)) continue;
+        const int from = there ? old : 0, n = __popcll(__ballot(there));  // the first n places
         if (to_page < 0 || to_page >= a.pages) continue;
         const int src_page = a.table[b * a.max_pages + from / KV_PAGE], token = from % KV_PAGE;
         const bool good = there && src_page >= 0 && src_page < a.pages;
@@ -213,7 +219,7 @@ __global__ __launch_bounds__(64) void kv_evict_move_kernel(KvEvict a) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int who = 16 * c + (lane >> 2);
-                if (P * KV_PAGE + who >= n) continue;
+                if (who >= n) continue;
                 if constexpr (small)
                     *reinterpret_cast<uint2*>(dst + at(who)) = make_uint2(v[c].x, v[c].y);
                 else
@@ -226,7 +232,7 @@ __global__ __launch_bounds__(64) void kv_evict_move_kernel(KvEvict a) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) v[r] = good ? src[r * KV_PAGE] : 0;
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (P * KV_PAGE + KV_PAGE <= n) {
+            if (whole) {
                 // the four lanes of a group hold the bytes of places p .. p + 3, in their order 0, 1, 2, 3 or (4 bits)
                 // 0, 2, 1, 3: lane k of places' order is left with the word of row 4 r + k
                 const bool odd = place & 1, upper = place & 2;
