@@ -596,22 +596,22 @@ static int check_attend_sizes(const char* fn, const q8k_kv_cache* kv, int64_t q_
     return check_count(fn, "max_len", max_len, MAX_LEN);
 }
 
-static size_t attend_workspace_bytes(const char* fn, const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq,
+static size_t attend_workspace_bytes(const char* fn, int bits, const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq,
                                      int64_t max_q, int64_t max_len) {
     if (!kv || !kv_dim(kv->head_dim) || kv->kv_heads < 1 || kv->kv_heads > MAX_HEADS ||
         check_attend_sizes(fn, kv, q_heads, B, Tq, max_q, max_len) != Q8K_OK || B == 0 || max_q == 0)
         return 0;
-    return (size_t)attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, 0).ws_bytes;
+    return (size_t)attend_plan(bits, B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, 0).ws_bytes;
 }
 
 size_t qattend_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
                                int64_t max_len) {
-    return attend_workspace_bytes("qattend_workspace_bytes", kv, q_heads, B, Tq, max_q, max_len);
+    return attend_workspace_bytes("qattend_workspace_bytes", 8, kv, q_heads, B, Tq, max_q, max_len);
 }
 
 size_t qattend_kv4_workspace_bytes(const q8k_kv_cache* kv, int64_t q_heads, int64_t B, int64_t Tq, int64_t max_q,
                                    int64_t max_len) {
-    return attend_workspace_bytes("qattend_kv4_workspace_bytes", kv, q_heads, B, Tq, max_q, max_len);
+    return attend_workspace_bytes("qattend_kv4_workspace_bytes", 4, kv, q_heads, B, Tq, max_q, max_len);
 }
 
 // What attention and its weights are asked of queries, pages and lengths: the
@@ -668,12 +668,12 @@ static int attend(const char* fn, int bits, int dtype, const void* q, int64_t q_
                          max_len, scale, window, pos, rope, &a));
     Q8K_TRY(check_ptr(fn, "out", out, 16));
     if (lse) Q8K_TRY(check_ptr(fn, "lse", lse, 4));
-    const size_t need = attend_workspace_bytes(fn, kv, q_heads, B, Tq, max_q, max_len);
+    const size_t need = attend_workspace_bytes(fn, bits, kv, q_heads, B, Tq, max_q, max_len);
     if (ws_bytes < need)
         return fail(Q8K_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     if (need > 0) Q8K_TRY(check_ptr(fn, "ws", ws, 16));
     if (B == 0 || max_q == 0) return Q8K_OK;
-    const AttendPlan p = attend_plan(B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, window);
+    const AttendPlan p = attend_plan(bits, B, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim, window);
     Q8K_TRY(check_grid(fn, p.items * kv->kv_heads));
     Q8K_TRY(check_threads(fn, p.items * kv->kv_heads * p.slices, p.threads));
     a.out = out;

@@ -495,6 +495,10 @@ hipError_t join_d(const Attend& a, bool tiles, hipStream_t s) {
 // rest: 65537 tokens among 255 of up to 2000 take 50 us, among 256 of them, whole,
 // 412 (in chunks 52).
 constexpr int64_t TARGET_WGS = 512;
+// Heads of 256 values in 4 bits: a compute unit takes one workgroup of them at a time, so
+// that 512 come in two turns (32 query heads over 8, bf16: 16 x 2000 tokens 25.4 us, with 512
+// 32.7, with 384 36.3; 16 x 8191 57.4, 66.2 and 78.2; 2 x 60000 55.2, 66.5 and 78.2).
+constexpr int64_t TARGET_WGS_256 = 256;
 constexpr int64_t SPLIT_MAX_BATCH = 256;
 // A chunk has at least this many pages (4096 tokens of one sequence: 15.6 us;
 // with 16 pages 17.2, with 4 15.3, but 16000 tokens then 22.6 and not 20.8).
@@ -537,7 +541,8 @@ constexpr int64_t SHORT_PAGES = 16, SIXTEENS = 512, SIXTEENS_PAGES = 16384;
 // 256 values 1244 and 729).
 constexpr int64_t SMALL_TILES_BELOW = 256, SMALL_TILES_PAGES = 48;
 
-static AttendPlan plan_for(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
+static AttendPlan plan_for(int bits, int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
+                           int64_t window) {
     AttendPlan p;
     const int64_t group = q_heads / heads, rows = max_q * group, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
     // what a tile reads at most
@@ -558,7 +563,8 @@ static AttendPlan plan_for(int64_t B, int64_t max_q, int64_t max_len, int q_head
     const int64_t tiles = B * p.tiles_max, live = live_of(p.tile_rows);
     p.split = live > (D == 256 && !p.tiles ? UNSPLIT_PAGES_256 : UNSPLIT_PAGES) && B <= SPLIT_MAX_BATCH &&
               tiles * heads < (p.tiles ? 1 : 4) * TARGET_WGS;
-    p.target = p.split ? (int)((TARGET_WGS + heads - 1) / heads) : 0;
+    const int64_t wgs_wanted = bits == 4 && D == 256 && !p.tiles ? TARGET_WGS_256 : TARGET_WGS;
+    p.target = p.split ? (int)((wgs_wanted + heads - 1) / heads) : 0;
     p.items = tiles;
     if (p.split) {
         const int64_t most = tiles * (1 + pages / p.least);
@@ -582,10 +588,10 @@ static AttendPlan plan_for(int64_t B, int64_t max_q, int64_t max_len, int q_head
 
 // Callers size the workspace without a window: a plan that a window changes to
 // one of a larger workspace is not taken (either serves any window).
-AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
-    const AttendPlan all = plan_for(B, max_q, max_len, q_heads, heads, D, 0);
+AttendPlan attend_plan(int bits, int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D, int64_t window) {
+    const AttendPlan all = plan_for(bits, B, max_q, max_len, q_heads, heads, D, 0);
     if (window == 0) return all;
-    const AttendPlan p = plan_for(B, max_q, max_len, q_heads, heads, D, window);
+    const AttendPlan p = plan_for(bits, B, max_q, max_len, q_heads, heads, D, window);
     return p.ws_bytes > all.ws_bytes ? all : p;
 }
 

@@ -73,23 +73,21 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(KvAppend a) {
     const int hv = (int)(row % (2 * a.heads));
     const bool is_v = hv >= a.heads;
     const int h = is_v ? hv - a.heads : hv;
-    const int slot = a.slots[t];
-    if (slot < 0 || slot >= a.pages * KV_PAGE) return;
-    const int64_t page = slot / KV_PAGE;
-    const int token = slot % KV_PAGE;
     RopeView r = a.rope;
-    const float* turn = nullptr;
-    if (r.table) {
-        const int p = a.pos[t];
-        if (p < 0 || p >= r.len) return;  // neither key nor value: the token selects nothing
-        turn = r.table + (int64_t)p * r.dim;
-    }
-    if (is_v) r.table = turn = nullptr;
+    if (is_v) r.table = nullptr;
     int oa, ob;
     kv_item(r, item, oa, ob);
+    // the slot, the position and the row set out together
+    const int slot = a.slots[t], p = a.rope.table ? a.pos[t] : 0;
     const void* src = is_v ? a.v : a.k;
     const int64_t base = t * (is_v ? a.v_stride : a.k_stride) + (int64_t)h * D;
-    float4 x = load4f(src, base + oa, a.dtype), y = load4f(src, base + ob, a.dtype);
+    const uint4 raw_x = load4raw(src, base + oa, a.dtype == DT_F32), raw_y = load4raw(src, base + ob, a.dtype == DT_F32);
+    if (slot < 0 || slot >= a.pages * KV_PAGE) return;
+    if (a.rope.table && (p < 0 || p >= a.rope.len)) return;  // neither key nor value: the token selects nothing
+    const int64_t page = slot / KV_PAGE;
+    const int token = slot % KV_PAGE;
+    const float* turn = r.table ? r.table + (int64_t)p * r.dim : nullptr;
+    float4 x = raw4f(raw_x, a.dtype), y = raw4f(raw_y, a.dtype);
     if (turn && 8 * item < r.dim) {
         kv_turn(r, *reinterpret_cast<const float4*>(turn + 4 * item),
                 *reinterpret_cast<const float4*>(turn + r.dim / 2 + 4 * item), x, y);
@@ -349,8 +347,13 @@ __global__ __launch_bounds__(256) void kv4_read_tile_kernel(KvRead a) {
     }
 }
 
-// Tokens times heads from which on tiles are taken.
-constexpr int64_t TILE_FROM_ROWS = 4096;
+// Tokens times heads from which on the tiles take less time where slots run on: appends
+// of 512 tokens of 8 heads of 128, fp32, take 7.1 us and 5.2 in the simple form, 1024 7.3
+// and 7.2, 2048 8.6 and 11.4 (reads 5.4 and 4.6, 6.4 and 6.4, 8.9 and 10.1); heads of 64,
+// bf16, 1024: 4.8 and 5.0; heads of 256, fp32, 512: 11.2 and 8.7, 1024: 12.0 and 14.6.
+// Slots apart, one a page, cost either form its single bytes: 1024 of 8 heads of 128, fp32,
+// 13.6 and 10.8, 2048 21.5 and 18.6.
+constexpr int64_t TILE_FROM_ROWS = 8192;
 
 template <int D>
 hipError_t append_d(const KvAppend& a, hipStream_t s) {

@@ -231,7 +231,7 @@ struct AttendPlan {
     int threads;        // of a workgroup
     int64_t items, ws_bytes;
 };
-AttendPlan attend_plan(int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
+AttendPlan attend_plan(int bits, int64_t B, int64_t max_q, int64_t max_len, int q_heads, int heads, int D,
                        int64_t window);
 constexpr int ATTEND_TILE_ROWS = 128, ATTEND_TILE_FEW = 64;
 hipError_t launch_attend_tiles(int bits, int D, const Attend& a, hipStream_t s);  // attend_tile.hip
