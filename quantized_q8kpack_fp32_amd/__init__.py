@@ -332,6 +332,16 @@ def _rows(dev, what, t, dtype, T, stride, row):
     return t.data_ptr()
 
 
+def _grid(dev, what, t, T, stride, row):
+    """_rows of fp32 rows that most often are a contiguous tensor's, ``stride`` its last axis."""
+    if t.__class__ is int or t is None:
+        return t
+    if t.is_contiguous() and t.dtype is torch.float32 and t.get_device() == dev and t.shape[-1:] == (stride,) \
+            and stride >= row and t.numel() >= T * stride:
+        return t.data_ptr()
+    return _rows(dev, what, t, torch.float32, T, stride, row)
+
+
 def _check_rows(what, t, T, stride, row):
     """Any tensor's rows: a row lies in the last axes whose elements follow each other, and rows begin where one of
     the axes before has its next element (or a whole number of them on).  Axes of one element, the rows of a flat
@@ -514,8 +524,8 @@ def qattend_weights(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q
         _kv(dev, kv, kv.bits), B, _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
         _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages, _flat(dev, "kv_len", kv_len, i32, B),
         max_len, scale, window, _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
-        _flat(dev, "lse", lse, f32, Tq * q_heads), _rows(dev, "old", old, f32, rows, w_stride, max_len), keep,
-        _rows(dev, "weights", weights, f32, rows, w_stride, max_len), w_stride, _bytes(dev, "ws", ws, ws_bytes), ws_bytes,
+        _flat(dev, "lse", lse, f32, Tq * q_heads), _grid(dev, "old", old, rows, w_stride, max_len), keep,
+        _grid(dev, "weights", weights, rows, w_stride, max_len), w_stride, _bytes(dev, "ws", ws, ws_bytes), ws_bytes,
         _stream_of(dev, stream)))
 
 
@@ -523,14 +533,13 @@ def q8k_kv_evict(kv, B: int, page_table, max_pages: int, kv_len, max_len: int, w
                  first: int, last: int, out_table, out_pages: int, out_weights, out_stride: int, kept, new_len,
                  stream=None) -> None:
     """The C call without ``bits``, which ``kv`` knows."""
-    dev = _device()
-    i32, f32 = torch.int32, torch.float32
+    dev, i32 = _device(), torch.int32
     rows = B * kv.kv_heads
     _check(lib.q8k_kv_evict(
         kv.bits, _kv(dev, kv, kv.bits), B, _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
-        _flat(dev, "kv_len", kv_len, i32, B), max_len, _rows(dev, "weights", weights, f32, rows, w_stride, max_len),
+        _flat(dev, "kv_len", kv_len, i32, B), max_len, _grid(dev, "weights", weights, rows, w_stride, max_len),
         w_stride, budget, first, last, _flat(dev, "out_table", out_table, i32, B * out_pages), out_pages,
-        _rows(dev, "out_weights", out_weights, f32, rows, out_stride, budget), out_stride,
+        _grid(dev, "out_weights", out_weights, rows, out_stride, budget), out_stride,
         _flat(dev, "kept", kept, i32, rows * budget), _flat(dev, "new_len", new_len, i32, B), _stream_of(dev, stream)))
 
 

@@ -13,6 +13,7 @@ namespace q8k {
 namespace {
 
 constexpr int WAVES = 4, ROWS = 16;
+constexpr int LEAST_TILES = 16;  // a share of the rows has so many at least
 
 // A page's keys of one head: on their way, and as the product's operand.
 template <int D, int BITS>
@@ -146,7 +147,9 @@ __device__ __forceinline__ rsrc_t page_record(const Attend& a, int page, int h, 
 
 // Few rows, up to 16 or 64 (ONE: their operand stays in registers, else in LDS): each
 // workgroup brings them once and then streams its share of a sequence's pages, a
-// page a wave, the next one's codes on their way.
+// page a wave, the next one's codes on their way.  Workgroup n of a sequence takes
+// pages 4 n .. 4 n + 3 and those `groups` workgroups further on: an even share of whatever
+// length it has, below whatever limit.
 template <int D, int BITS, int NQ, bool ONE>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kernel(AttendWeights w) {
     constexpr int KS = D / 32, TILES = ONE ? 1 : 4;
@@ -159,19 +162,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
     const int col = lane & 15, g = lane >> 4;
     const int h = (int)(blockIdx.x % a.heads);
     const int64_t id = blockIdx.x / a.heads, b = id / w.groups;
-    const int c0 = (int)(id % w.groups) * w.group_pages;
+    const int c0 = (int)(id % w.groups) * WAVES, step = w.groups * WAVES;
     const int32_t* table = a.table + b * a.max_pages;
     // (of the table's, whatever the length: it then needs not be waited for)
     const int first_page = __builtin_amdgcn_readfirstlane(table[min((int64_t)c0 + wave, a.max_pages - 1)]);
     const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
-    const int pages = (seq.len + KV_PAGE - 1) / KV_PAGE, c1 = min(pages, c0 + w.group_pages);
-    if (c0 >= c1) return;
+    const int pages = (seq.len + KV_PAGE - 1) / KV_PAGE;
+    if (c0 >= pages) return;
     constexpr int bytes = kv_record_of(BITS, D);
     const Widen masks;
     PageKeys<D, BITS> keys;
     bool ok = false, next_ok;
     int p = c0 + wave;
-    const auto page_at = [&](int p) { return __builtin_amdgcn_readfirstlane(p < c1 ? table[p] : -1); };
+    const auto page_at = [&](int64_t p) { return __builtin_amdgcn_readfirstlane(p < pages ? table[p] : -1); };
     // a row's values and the first page set out together
     const int rows = seq.nq * a.group, tiles = (rows + ROWS - 1) / ROWS;
     h8_t qf[NQ][KS];
@@ -185,7 +188,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
             const int i = threadIdx.x + 64 * WAVES * n, r = i / (D / 8);
             if (r < rows && r < ROWS) fetch_q<D>(a, seq, h, row_of_tile(a, tile, r), i % (D / 8), qi[n]);
         }
-        keys.fetch(page_record(a, p < c1 ? first_page : -1, h, bytes, ok), lane);
+        keys.fetch(page_record(a, p < pages ? first_page : -1, h, bytes, ok), lane);
         mine = info_of(w, seq, tile, h, col);
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
         __syncthreads();
         mine.unit = query_operand<D, NQ>(a, qs[0][col], g, qf);
     } else {
-        keys.fetch(page_record(a, p < c1 ? first_page : -1, h, bytes, ok), lane);
+        keys.fetch(page_record(a, p < pages ? first_page : -1, h, bytes, ok), lane);
         if (wave < tiles) {
             mine = stage_rows<D, NQ>(w, seq, h, wave, lane, qs[wave], qf);
 #pragma unroll
@@ -214,7 +217,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
         __syncthreads();
     }
     const int64_t row = (b * a.heads + h) * w.stride;
-    for (; p < c1; p += WAVES) {
+    for (; p < pages; p += step) {
         const int j0 = p * KV_PAGE, j = j0 + token_of(col, g);
         const float before = w.old && j < seq.len - seq.n ? w.old[row + j] : 0.0f;
         scales[wave][lane] = keys.scale;
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[q][i] = 0.0f;
-        const rsrc_t rec = page_record(a, page_at(p + WAVES), h, bytes, next_ok);
+        const rsrc_t rec = page_record(a, page_at((int64_t)p + step), h, bytes, next_ok);
         if constexpr (ONE) {
             f4_t s4[4];
 #pragma unroll
@@ -273,6 +276,21 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void weights_few_kern
     }
 }
 
+// How many of a sequence's `groups` workgroups there are groups of pages for, and
+// shares of the rows that leave the others something to do: by the lengths on the
+// device, not by the limits that the grid was made for.
+struct Shares {
+    int groups, splits;
+};
+__device__ __forceinline__ Shares shares_of(const AttendWeights& w, const Sequence& seq, int group_pages) {
+    const int64_t tokens = (int64_t)group_pages * KV_PAGE;
+    Shares s;
+    s.groups = (int)((seq.len + tokens - 1) / tokens);
+    const int tiles = (seq.nq * w.a.group + ROWS - 1) / ROWS, most = max(1, (tiles + LEAST_TILES - 1) / LEAST_TILES);
+    s.splits = s.groups > 0 ? max(1, min(w.groups / s.groups, most)) : 1;
+    return s;
+}
+
 // Many rows: they become operands once, in the workspace, sixteen to a piece of
 // NQ D/32 + 1 KB (the last: their RowInfo, four times over).
 template <int D, int NQ>
@@ -316,24 +334,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
     int64_t id = blockIdx.x;
     const int h = (int)(id % a.heads);
     id /= a.heads;
-    const int split = (int)(id % w.splits);
-    id /= w.splits;
     const int64_t b = id / w.groups;
-    const int c0 = (int)(id % w.groups) * (WAVES * PAGES);
-    const int32_t* table = a.table + b * a.max_pages;
-    int page[PAGES];  // of the table's, whatever the length: it then needs not be waited for
-#pragma unroll
-    for (int n = 0; n < PAGES; ++n)
-        page[n] = __builtin_amdgcn_readfirstlane(table[min((int64_t)c0 + wave * PAGES + n, a.max_pages - 1)]);
     const Sequence seq = sequence_of_lane(sequence_of(a, b), 0);
-    if (c0 * KV_PAGE >= seq.len) return;
+    const Shares sh = shares_of(w, seq, WAVES * PAGES);
+    const int place = uni((int)(id % w.groups)), split = uni(sh.groups > 0 ? place / sh.groups : 1);
+    if (split >= sh.splits) return;
+    const int c0 = (place - split * sh.groups) * (WAVES * PAGES);
+    const int32_t* table = a.table + b * a.max_pages;
     constexpr int bytes = kv_record_of(BITS, D);
     // rows that may see one of these pages
     const int past = seq.len - seq.n, i0 = max(0, c0 * KV_PAGE - past);
     int64_t i1 = seq.nq;
     if (a.window > 0) i1 = min(i1, (int64_t)(c0 + WAVES * PAGES) * KV_PAGE - 1 + a.window - past);
     const int r0 = uni(i0 * a.group / ROWS), r1 = uni(i1 > i0 ? (int)((i1 * a.group + ROWS - 1) / ROWS) : r0);
-    const int each = (r1 - r0 + w.splits - 1) / w.splits, t0 = r0 + split * each, t1 = min(r1, t0 + each);
+    const int each = (r1 - r0 + sh.splits - 1) / sh.splits, t0 = r0 + split * each, t1 = min(r1, t0 + each);
     const uint4* pieces = w.rows + (first_piece(a, seq, b) * a.heads + h) * (64 * KB);
     const int64_t step = (int64_t)a.heads * (64 * KB);
     const auto bring = [&](int t, int buf) {
@@ -354,7 +368,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
     for (int n = 0; n < PAGES; ++n) {
         const int p = c0 + wave * PAGES + n;
         PageKeys<D, BITS> keys;
-        keys.fetch(page_record(a, p * KV_PAGE < seq.len ? page[n] : -1, h, bytes, ok[n]), lane);
+        const int page = __builtin_amdgcn_readfirstlane(p * KV_PAGE < seq.len ? table[p] : -1);
+        keys.fetch(page_record(a, page, h, bytes, ok[n]), lane);
         if (n == 0 && t0 < t1) bring(t0, 0);
 #pragma unroll
         for (int s = 0; s < KS / 2; ++s)
@@ -399,8 +414,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
         const float got = rows_sum(sum[n], col);
         const int j = (c0 + wave * PAGES + n) * KV_PAGE + token_of(col, g);
         if (j >= seq.len) continue;
-        if (w.splits > 1) {
-            w.part[(split * a.B * a.heads + b * a.heads + h) * (int64_t)w.groups * (WAVES * PAGES * KV_PAGE) + j] = got;
+        if (sh.splits > 1) {
+            w.part[((b * a.heads + h) * w.groups + place) * (WAVES * PAGES * KV_PAGE) + (j - c0 * KV_PAGE)] = got;
         } else {
             const int64_t at = (b * a.heads + h) * w.stride + j;
             w.weights[at] = __builtin_fmaf(w.old && j < past ? w.old[at] : 0.0f, w.keep, got);
@@ -409,15 +424,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
 }
 
 // Adds up the shares of the rows, in order.
-__global__ __launch_bounds__(256) void weights_join_kernel(AttendWeights w, int64_t len) {
+__global__ __launch_bounds__(256) void weights_join_kernel(AttendWeights w) {
     const Attend& a = w.a;
-    const int64_t per = (len + 255) / 256, bh = blockIdx.x / per, b = bh / a.heads;
-    const int j = (int)(blockIdx.x % per) * 256 + threadIdx.x;
+    const int64_t per = (a.max_len + 255) / 256, bh = blockIdx.x / per, b = bh / a.heads;
+    const int64_t j = (blockIdx.x % per) * 256 + threadIdx.x;
     const Sequence seq = sequence_of(a, b);
-    if (j >= seq.len) return;
-    const float* part = w.part + bh * len + j;
+    const Shares sh = shares_of(w, seq, w.group_pages);
+    if (j >= seq.len || sh.splits == 1) return;
+    const int64_t tokens = (int64_t)w.group_pages * KV_PAGE;
+    const float* part = w.part + (bh * w.groups + j / tokens) * tokens + j % tokens;
     float got = 0.0f;
-    for (int s = 0; s < w.splits; ++s) got += part[s * a.B * a.heads * len];
+    for (int s = 0; s < sh.splits; ++s) got += part[s * sh.groups * tokens];
     const int64_t at = bh * w.stride + j;
     w.weights[at] = __builtin_fmaf(w.old && j < seq.len - seq.n ? w.old[at] : 0.0f, w.keep, got);
 }
@@ -435,10 +452,7 @@ hipError_t weights_n(const WeightsPlan& p, const AttendWeights& w, hipStream_t s
     const int64_t waves = w.a.B * w.a.heads * w.a.tiles_max;
     Q8K_LAUNCH((weights_rows_kernel<D, NQ>), dim3((unsigned)((waves + WAVES - 1) / WAVES)), block, 0, s, w);
     Q8K_LAUNCH((weights_many_kernel<D, BITS, NQ>), grid, block, 0, s, w);
-    if (p.splits > 1) {
-        const int64_t len = p.groups * p.group_pages * KV_PAGE;
-        Q8K_LAUNCH(weights_join_kernel, dim3((unsigned)(w.a.B * w.a.heads * ((len + 255) / 256))), dim3(256), 0, s, w, len);
-    }
+    if (p.split) Q8K_LAUNCH(weights_join_kernel, dim3((unsigned)p.join_workgroups), dim3(256), 0, s, w);
     return hipGetLastError();
 }
 template <int D, int BITS>
@@ -448,41 +462,36 @@ hipError_t weights_d(const WeightsPlan& p, const AttendWeights& w, hipStream_t s
 
 }  // namespace
 
-// Up to FEW_ROWS rows a head: one launch, a workgroup for each group of pages, as many
-// as make about FEW_WGS workgroups at the limits (16 sequences of up to 8191 tokens, 32
-// heads over 8: 21.7 us, 512 of them 23.9, 4096 24.5).  More rows: their operands in the
-// workspace, groups of WAVES * 2 pages (of 256 values WAVES), and the rows in as many
-// shares as make MANY_WGS workgroups (2 x 1000 tokens over 8001, 32 heads over 4: 234 us,
-// 1024 of them 249, 4096 236), each of LEAST_TILES tiles at least (the last 64 of 4 x up to
-// 16001, 32 over 8, 16 tiles: 44.8 us, by 8 48.5, by 4 59).
-constexpr int64_t FEW_ROWS = 64, FEW_WGS = 2048, MANY_WGS = 2048, LEAST_TILES = 16;
+// Up to FEW_ROWS rows a head: one launch, as many workgroups a sequence and head as make
+// FEW_WGS (16 sequences of up to 8191 tokens, 32 heads over 8: 20.2 us, 512 of them 24.4,
+// 1536 22.6, 2048 23.1; 1 x 65537 12.5, 12.7, 14.2 and 14.4; 8 x 65537 64, 73, 64.5 and
+// 63).  More rows: their operands in the workspace, groups of 2 WAVES pages (of 256 values
+// WAVES), and the rows in as many shares as make MANY_WGS workgroups (2 x 1000 tokens over
+// 8001, 32 heads over 4: 228 us, 1024 of them 249, 4096 241), each of LEAST_TILES tiles at
+// least (the last 64 of 4 x up to 16001, 32 over 8, 16 tiles: 44 us, by 8 48.5, by 4 59).
+constexpr int64_t FEW_ROWS = 64, FEW_WGS = 1024, MANY_WGS = 2048;
 
 WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {
     WeightsPlan p{};
     const int64_t group = q_heads / heads, pages = (max_len + KV_PAGE - 1) / KV_PAGE;
     p.rows = max_q * group;
     p.many = p.rows > FEW_ROWS;
-    p.splits = 1;
     p.threads = 64 * WAVES;
     p.tiles_max = (p.rows + ROWS - 1) / ROWS;
+    // workgroups that a sequence and head has pages for, and those that fill the device
+    p.group_pages = p.many && D < 256 ? 2 * WAVES : WAVES;
+    const int64_t most = (pages + p.group_pages - 1) / p.group_pages;
+    const int64_t fill = ((p.many ? MANY_WGS : FEW_WGS) + B * heads - 1) / (B * heads);
     if (!p.many) {
-        p.group_pages = (B * heads * pages + FEW_WGS - 1) / FEW_WGS;
-        p.group_pages = p.group_pages < WAVES ? WAVES : (p.group_pages + WAVES - 1) / WAVES * WAVES;
+        p.groups = most < fill ? most : fill;
     } else {
-        p.group_pages = WAVES * (D == 256 ? 1 : 2);
-    }
-    p.groups = (pages + p.group_pages - 1) / p.group_pages;
-    p.workgroups = B * heads * p.groups;
-    if (p.many) {
-        int64_t splits = (MANY_WGS + p.workgroups - 1) / p.workgroups;
-        const int64_t most = (p.tiles_max + LEAST_TILES - 1) / LEAST_TILES;
-        splits = splits > most ? most : splits;
-        p.splits = (int)splits;
-        p.workgroups *= splits;
+        p.split = p.tiles_max > LEAST_TILES;
+        p.groups = p.split && fill > most ? fill : most;
         p.rows_bytes = (Tq * group / ROWS + B + 1) * heads * (2 * (D / 32) + 1) * 1024;
-        p.ws_bytes = p.rows_bytes;
-        if (splits > 1) p.ws_bytes += splits * B * heads * p.groups * p.group_pages * KV_PAGE * 4;
+        p.join_workgroups = B * heads * ((max_len + 255) / 256);
+        p.ws_bytes = p.rows_bytes + (p.split ? B * heads * p.groups * p.group_pages * KV_PAGE * 4 : 0);
     }
+    p.workgroups = B * heads * p.groups;
     return p;
 }
 
@@ -492,7 +501,6 @@ hipError_t launch_attend_weights(int bits, int D, const WeightsPlan& p, AttendWe
     w.a.inv_group = 1.0f / (float)w.a.group;
     w.groups = (int)p.groups;
     w.group_pages = (int)p.group_pages;
-    w.splits = p.splits;
     w.rows = static_cast<uint4*>(ws);
     w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.rows_bytes);
     if (bits == 8) return D == 64 ? weights_d<64, 8>(p, w, s) : D == 128 ? weights_d<128, 8>(p, w, s) : weights_d<256, 8>(p, w, s);

@@ -245,15 +245,15 @@ struct AttendWeights {
     float keep;
     float* weights;
     int64_t stride;
-    int groups, group_pages;  // groups of pages of a sequence, at most, and their pages
-    int splits;               // shares of the rows
+    int groups, group_pages;  // workgroups of a sequence and head; pages that one holds at a time
     uint4* rows;              // workspace: the rows' operands
-    float* part;              // [splits][B][heads][groups * group_pages * 64] where splits > 1
+    float* part;              // [B][heads][groups][group_pages * 64]: of shares of the rows
 };
 struct WeightsPlan {
     bool many;  // rows: their operands go to the workspace
-    int64_t rows, tiles_max, groups, group_pages, workgroups, rows_bytes, ws_bytes;
-    int splits, threads;
+    bool split;  // some sequence's rows may be cut into shares
+    int64_t rows, tiles_max, groups, group_pages, workgroups, join_workgroups, rows_bytes, ws_bytes;
+    int threads;
 };
 WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D);
 hipError_t launch_attend_weights(int bits, int D, const WeightsPlan& p, AttendWeights w, void* ws, hipStream_t s);
