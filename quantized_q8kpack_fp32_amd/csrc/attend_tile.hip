@@ -3,16 +3,17 @@
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
 // Chunks of up to 1000 tokens of three prompts over up to 16001 (32 heads of 128
-// over 4, bf16, turned): 802 us, 575 TFLOP/s of the formula's, where a large matrix
-// product reaches 1140.  A query of two fp16 pieces makes the first product twice as
-// long as the formula's, so that the matrix work alone would take 607 us at that
-// rate; matrix instructions are busy for 36% of the cycles and vector ones (some
-// twelve a score) for 41%, and little of the two overlaps: each wave does a page's
-// scores, probabilities and values in turn, and the waves of a unit are in the same
-// phase behind one barrier a page (scheduling groups that put the instructions
-// between each other, and wave priorities, gained nothing).  The 1000, 443 and 787
-// tokens make 564 tiles with work, of unequal length, on 512 places, the longest
-// first; four of 1024 over 8192, 1024 tiles of nearly one length, reach 695.
+// over 4, bf16, turned): 740 us, 623 TFLOP/s of the formula's, where a large matrix
+// product reaches 1143 (from the 4-bit cache, whose codes take more to widen, 759).  A query
+// of two fp16 pieces makes the first product twice as long as the formula's, so that the
+// matrix work alone would take 605 us at that rate; matrix instructions are busy for some
+// 36% of the cycles and vector ones (some twelve a score) for 41%, and little of the two
+// overlaps: each wave does a page's scores, probabilities and values in turn, and the waves
+// of a unit are in the same phase behind one barrier a page (scheduling groups that put the
+// instructions between each other, and priorities by phase, gained nothing).  The 1000, 443
+// and 787 tokens make 564 tiles with work, of unequal length, on 512 places, the longest
+// first; four of 1024 over 8192, 1024 tiles of nearly one length, reached 695 before the two
+// workgroups of a unit were told apart.
 #include "attend.h"
 
 namespace q8k {
@@ -75,6 +76,10 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
     const int rows = tile.rows;
     if (tile.row0 >= rows) return;
     const int p0 = uni(tile.p0 + it.split * it.c), p1 = uni(min(tile.p1, p0 + it.c));
+    // Of the two workgroups that a compute unit starts with, one goes first wherever both could
+    // issue, so that they do not stay in the same phase of a page (the chunks above 740 us,
+    // alike 783; from the 4-bit cache 759 and 796).
+    if (blockIdx.x >> 8 & 1) __builtin_amdgcn_s_setprio(1);
     if (it.splits > 1 && p0 >= p1) return;  // the join reads only chunks that some row's span meets
 
     // The wave's queries: all on their way at once, then 16 rows at a time

@@ -339,6 +339,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
     const Shares sh = shares_of(w, seq, WAVES * PAGES);
     const int place = uni((int)(id % w.groups)), split = uni(sh.groups > 0 ? place / sh.groups : 1);
     if (split >= sh.splits) return;
+    // (the two workgroups that a compute unit starts with: not in the same phase, attend_tile.hip)
+    if (blockIdx.x >> 8 & 1) __builtin_amdgcn_s_setprio(1);
     const int c0 = (place - split * sh.groups) * (WAVES * PAGES);
     const int32_t* table = a.table + b * a.max_pages;
     constexpr int bytes = kv_record_of(BITS, D);
