@@ -345,7 +345,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void weights_many_kernel(AttendWeigh
     const int32_t* table = a.table + b * a.max_pages;
     constexpr int bytes = kv_record_of(BITS, D);
     // rows that may see one of these pages
-    const int past = seq.len - seq.n, i0 = max(0, c0 * KV_PAGE - past);
+    const int past = seq.len - seq.n, i0 = min(max(0, c0 * KV_PAGE - past), seq.nq);
     int64_t i1 = seq.nq;
     if (a.window > 0) i1 = min(i1, (int64_t)(c0 + WAVES * PAGES) * KV_PAGE - 1 + a.window - past);
     const int r0 = uni(i0 * a.group / ROWS), r1 = uni(i1 > i0 ? (int)((i1 * a.group + ROWS - 1) / ROWS) : r0);
