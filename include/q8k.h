@@ -258,7 +258,8 @@ int qmatmul_prefill_moe_noalloc(int qtype, const void* w, int64_t E, int64_t row
  * probability as two pieces, within 2^-21 of the value (a bf16 query that is not
  * turned exactly); where results are bf16 a probability is one piece, within
  * 2^-11, an eighth of the result's own half step.  lse comes from the
- * probabilities before that.
+ * probabilities before that.  (In the 4-bit cache of "long contexts" below: codes
+ * times factors, exactly.)
  *
  * The cache (the page layout is the library's; other code reads it with
  * q8k_kv_read): `pages` pages of Q8K_KV_PAGE tokens, q8k_kv_bytes(...) bytes.
@@ -410,7 +411,7 @@ int qattend_kv4(int dtype, const void* q, int64_t q_stride, int64_t q_heads, con
  *                      heads a of key head h of e^(s_j - lse[i][a])
  * for the tokens j < len, s_j as in qattend.  Arguments up to rope: qattend's, over a
  * cache of `bits` 8 or 4.  lse fp32 [Tq][q_heads]: what attention returned for these
- * rows (a row of -inf adds nothing).
+ * rows (a row of -inf adds nothing, one of NaN makes what it sees NaN).
  * old, weights: rows of at least max_len fp32, one for each sequence and key head [B]
  * [kv_heads], w_stride elements apart; they may be the same.  old NULL: none.  old is
  * not read for the new tokens, which have got nothing before, nor from len on; weights

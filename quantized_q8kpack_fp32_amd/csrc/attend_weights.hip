@@ -4,6 +4,12 @@
 // as attention left them.  With lse known no row needs its other tokens, so the
 // sum over rows stays where the tokens are: a wave holds the keys of one page, widened
 // once, and adds up its 64 tokens while the rows go by.  No atomics: one order always.
+//
+// Few rows are bound by the keys' bytes: 16 sequences of up to 8191 tokens, 32 heads of
+// 128 over 8, 8 bits, 20 us, 4.4 TB/s.  Many are bound by matrix instructions and the
+// exponentials, which hardly overlap: 2 x 1000 tokens over 8001, 32 heads over 4, 4 bits,
+// bf16 and turned, 228 us, 205 of them the products: 600 TFLOP/s of the formula's, 1200 with
+// the queries' two pieces.
 #include <type_traits>
 
 #include "attend.h"

@@ -4,7 +4,10 @@
 // value each become D codes of 4 bits, D/32 factors and one scale:
 //   scale = amax/7,  factor_y = the least 8-bit float >= max|x_y| / amax,
 //   code = round(x / (factor_y scale)).
-// Bound by bytes: 4 D or 8 D a token and head in, D + D/16 + 8 out.
+// 4 D or 8 D bytes a token and head in, D + D/16 + 8 out: 8191 tokens of 8 heads of 128,
+// bf16, 53 MB, take 18.7 us, 13 of them vector instructions (divisions and codes); the
+// read back 13.9 (3.7 TB/s).  Few tokens are bound by the launch and two chained loads
+// (61 tokens 3.6 us, the read back 4.0).
 #include "kv4_cache.h"
 #include "kv_tile.h"
 #include "q8k_launch.h"

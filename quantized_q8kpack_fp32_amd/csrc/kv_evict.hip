@@ -3,8 +3,11 @@
 // others, those of the largest weights (equal ones by ascending index), in order;
 // what the cache holds of these moves to the front of the sequence's new pages.
 //
-// Two launches: the choice (one workgroup a sequence and head) and the move.  A page's
-// places beyond the kept tokens are left as they were.
+// Two launches: the choice (one workgroup a sequence and head; 8 rows of 2111 weights 6.9
+// us, a chain of barriers, 128 of up to 16001 16.9) and the move (4000 of up to 16001
+// tokens of 128 rows, 8 bits, heads of 128: 96 us, 4.2 TB/s of what it touches, since a
+// page's values lie row by row and a line of 64 tokens is read for one).  A page's places
+// beyond the kept tokens are left as they were.
 #include "attend.h"
 #include "q8k_launch.h"
 
