@@ -5,8 +5,8 @@
 //   scale = amax/7,  factor_y = the least 8-bit float >= max|x_y| / amax,
 //   code = round(x / (factor_y scale)).
 // 4 D or 8 D bytes a token and head in, D + D/16 + 8 out: 8191 tokens of 8 heads of 128,
-// bf16, 53 MB, take 18.7 us, 13 of them vector instructions (divisions and codes); the
-// read back 13.9 (3.7 TB/s).  Few tokens are bound by the launch and two chained loads
+// bf16, 53 MB, take 17 us, 10 of them vector instructions (divisions and codes); the
+// read back 12 (4.3 TB/s).  Few tokens are bound by the launch and two chained loads
 // (61 tokens 3.6 us, the read back 4.0).
 #include "kv4_cache.h"
 #include "kv_tile.h"
@@ -116,7 +116,8 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(KvAppend a) {
 // consecutive bytes a token.  The values' bytes meet in LDS: those of four tokens
 // that follow each other from a multiple of four on lie side by side in each row of
 // places and leave as words, the others' (a run's ends, slots in no order) as bytes.
-template <int D>
+// Made for each type: where the type was looked at for every value, 19.2 us for 17.0.
+template <int D, int DT>
 __global__ __launch_bounds__(256) void kv4_append_tile_kernel(KvAppend a) {
     constexpr int L = D / 8, ROWS = 256 / L, N = TILE / ROWS, W = D / 8;  // words of a token's values
     __shared__ float turned[ROWS][D + 4];
@@ -131,27 +132,17 @@ __global__ __launch_bounds__(256) void kv4_append_tile_kernel(KvAppend a) {
     // all rows of the tile (the last one's again behind the last)
     uint4 raw[N][4];
     int slot_of[N], pos[N];
-    const auto fetch = [&](bool f32) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int64_t t = t0 + min(i * ROWS + (int)threadIdx.x / L, n - 1);
-            const int64_t kb = t * a.k_stride + (int64_t)h * D, vb = t * a.v_stride + (int64_t)h * D;
-            raw[i][0] = load4raw(a.k, kb + oa, f32);
-            raw[i][1] = load4raw(a.k, kb + ob, f32);
-            raw[i][2] = load4raw(a.v, vb + 8 * item, f32);
-            raw[i][3] = load4raw(a.v, vb + 8 * item + 4, f32);
-        }
-    };
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int64_t t = t0 + min(i * ROWS + (int)threadIdx.x / L, n - 1);
         slot_of[i] = a.slots[t];
         pos[i] = a.rope.table ? a.pos[t] : 0;
+        const int64_t kb = t * a.k_stride + (int64_t)h * D, vb = t * a.v_stride + (int64_t)h * D;
+        raw[i][0] = load4raw(a.k, kb + oa, DT == DT_F32);
+        raw[i][1] = load4raw(a.k, kb + ob, DT == DT_F32);
+        raw[i][2] = load4raw(a.v, vb + 8 * item, DT == DT_F32);
+        raw[i][3] = load4raw(a.v, vb + 8 * item + 4, DT == DT_F32);
     }
-    if (a.dtype == DT_F32)
-        fetch(true);
-    else
-        fetch(false);
     float4 c[N], s[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -174,8 +165,8 @@ __global__ __launch_bounds__(256) void kv4_append_tile_kernel(KvAppend a) {
         if (slot < 0) continue;  // uniform over the row's lanes
         uint8_t* rec = a.cache + ((int64_t)(slot / KV_PAGE) * a.heads + h) * kv4_record(D);
         const int token = slot % KV_PAGE;
-        float4 x = raw4f(raw[i][0], a.dtype), y = raw4f(raw[i][1], a.dtype);
-        const float4 u = raw4f(raw[i][2], a.dtype), w = raw4f(raw[i][3], a.dtype);
+        float4 x = raw4f(raw[i][0], DT), y = raw4f(raw[i][1], DT);
+        const float4 u = raw4f(raw[i][2], DT), w = raw4f(raw[i][3], DT);
         if (a.rope.table && 8 * item < a.rope.dim) kv_turn(a.rope, c[i], s[i], x, y);
         if (a.rope.table && !a.rope.adjacent) natural_order<D>(turned[threadIdx.x / L], oa, ob, item, x, y);
         const Row4 k = quantise_row<L>(x, y), v = quantise_row<L>(u, w);
@@ -220,8 +211,12 @@ __global__ __launch_bounds__(256) void kv4_append_tile_kernel(KvAppend a) {
     }
 }
 
+// Rounded to fp32 and then to the type.  (The compiler would take a product and its
+// conversion to fp16 as one instruction, which rounds once.)
 __device__ __forceinline__ float4 scaled(float4 c, float factor, float s) {
-    return make_float4(c.x * factor * s, c.y * factor * s, c.z * factor * s, c.w * factor * s);
+    float4 v = make_float4(c.x * factor * s, c.y * factor * s, c.z * factor * s, c.w * factor * s);
+    asm("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+    return v;
 }
 
 // The codes of four bytes' low (at 0) or high (at 4) halves.
@@ -264,7 +259,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(KvRead a) {
 }
 
 // Many tokens, as kv4_append_tile_kernel's: 32 tokens of one head.
-template <int D>
+template <int D, int DT>
 __global__ __launch_bounds__(256) void kv4_read_tile_kernel(KvRead a) {
     constexpr int L = D / 8, ROWS = 256 / L, W = D / 8;
     __shared__ uint32_t codes[TILE][W + 1];
@@ -343,37 +338,45 @@ __global__ __launch_bounds__(256) void kv4_read_tile_kernel(KvRead a) {
             v1 = scaled(value_codes(codes[t][4 * group + 2 * (item & 1) + 1], at), e, vs[i]);
         }
         const int64_t o = ((t0 + t) * a.heads + h) * D + 8 * item;
-        store4f(a.k, o, a.dtype, k0);
-        store4f(a.k, o + 4, a.dtype, k1);
-        store4f(a.v, o, a.dtype, v0);
-        store4f(a.v, o + 4, a.dtype, v1);
+        store4f(a.k, o, DT, k0);
+        store4f(a.k, o + 4, DT, k1);
+        store4f(a.v, o, DT, v0);
+        store4f(a.v, o + 4, DT, v1);
     }
 }
 
 // Tokens times heads from which on the tiles take less time where slots run on: appends
-// of 512 tokens of 8 heads of 128, fp32, take 7.1 us and 5.2 in the simple form, 1024 7.3
-// and 7.2, 2048 8.6 and 11.4 (reads 5.4 and 4.6, 6.4 and 6.4, 8.9 and 10.1); heads of 64,
-// bf16, 1024: 4.8 and 5.0; heads of 256, fp32, 512: 11.2 and 8.7, 1024: 12.0 and 14.6.
+// of 512 tokens of 8 heads of 128, fp32, take 5.9 us and 5.0 in the simple form, 1024 6.3
+// and 6.9, 2048 7.5 and 11.0 (reads 5.3 and 4.4, 6.3 and 6.4, 9.1 and 9.6); heads of 64,
+// bf16, 1024: 4.7 and 5.0; heads of 256, fp32, 512: 9.3 and 8.7, 1024: 10.0 and 14.4.
 // Slots apart, one a page, cost either form its single bytes: 1024 of 8 heads of 128, fp32,
-// 13.6 and 10.8, 2048 21.5 and 18.6.
+// 12.7 and 10.8, 2048 20.6 and 18.7.
 constexpr int64_t TILE_FROM_ROWS = 8192;
 
+template <int D, int DT>
+hipError_t append_tiles(const KvAppend& a, hipStream_t s) {
+    Q8K_LAUNCH((kv4_append_tile_kernel<D, DT>), dim3((unsigned)kv_workgroups(a.T, a.heads)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
 template <int D>
 hipError_t append_d(const KvAppend& a, hipStream_t s) {
-    if (a.T * a.heads >= TILE_FROM_ROWS) {
-        Q8K_LAUNCH((kv4_append_tile_kernel<D>), dim3((unsigned)kv_workgroups(a.T, a.heads)), dim3(256), 0, s, a);
-        return hipGetLastError();
-    }
+    if (a.T * a.heads >= TILE_FROM_ROWS)
+        return a.dtype == DT_F32 ? append_tiles<D, DT_F32>(a, s)
+               : a.dtype == DT_BF16 ? append_tiles<D, DT_BF16>(a, s) : append_tiles<D, DT_F16>(a, s);
     const int64_t rows = a.T * 2 * a.heads, per = 256 / (D / 8);
     Q8K_LAUNCH((kv4_append_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
+template <int D, int DT>
+hipError_t read_tiles(const KvRead& a, hipStream_t s) {
+    Q8K_LAUNCH((kv4_read_tile_kernel<D, DT>), dim3((unsigned)kv_workgroups(a.T, a.heads)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
 template <int D>
 hipError_t read_d(const KvRead& a, hipStream_t s) {
-    if (a.T * a.heads >= TILE_FROM_ROWS) {
-        Q8K_LAUNCH((kv4_read_tile_kernel<D>), dim3((unsigned)kv_workgroups(a.T, a.heads)), dim3(256), 0, s, a);
-        return hipGetLastError();
-    }
+    if (a.T * a.heads >= TILE_FROM_ROWS)
+        return a.dtype == DT_F32 ? read_tiles<D, DT_F32>(a, s)
+               : a.dtype == DT_BF16 ? read_tiles<D, DT_BF16>(a, s) : read_tiles<D, DT_F16>(a, s);
     const int64_t rows = a.T * a.heads, per = 256 / (D / 8);
     Q8K_LAUNCH((kv4_read_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a);
     return hipGetLastError();

@@ -59,17 +59,17 @@ __device__ __forceinline__ int kv4_key_factor(int token, int y) {
 // The least factor that is not below r in [0, 1] (0 for NaN): above 2^-14 the top bits of
 // r, rounded up; below, r in steps of 2^-18.
 __device__ __forceinline__ uint32_t kv4_factor(float r) {
-    if (!(r > 0.0f)) return 0;
-    if (r < 6.103515625e-05f) return (uint32_t)(int)ceilf(r * 262144.0f);
-    return ((__builtin_bit_cast(uint32_t, r) + 0x7ffffu) >> 19) - (112u << 4);
+    r = fmaxf(r, 0.0f);
+    const uint32_t small = (uint32_t)(int)ceilf(r * 262144.0f);
+    return r < 6.103515625e-05f ? small : ((__builtin_bit_cast(uint32_t, r) + 0x7ffffu) >> 19) - (112u << 4);
 }
 __device__ __forceinline__ float kv4_factor_value(uint32_t f) { return half_bits_to_float(f << 6); }
 // 1 / step of a group, or 0 where all codes are 0 (nothing but zeros, or too small beside
 // the row's largest for any factor; an infinity among the row's values).
 __device__ __forceinline__ float kv4_inverse(uint32_t f, float scale) {
 #pragma clang fp contract(off)
-    const float step = kv4_factor_value(f) * scale;
-    return f == 0 || !(scale < INFINITY) ? 0.0f : 1.0f / step;
+    // (a step, not a quotient, is chosen: a division is too much for the compiler to take both ways)
+    return 1.0f / (f == 0 || !(scale < INFINITY) ? INFINITY : kv4_factor_value(f) * scale);
 }
 // code + 8 of eight values (x and y: 0-3 and 4-7), value i's at bit SHIFT_i: kv_codes4's
 // rule with 7 in the place of 127.  1.5 * 2^23 + 8 rounds a product to a whole number,
@@ -84,8 +84,10 @@ __device__ __forceinline__ uint64_t kv4_codes8(float4 a, float4 b, float inverse
     constexpr uint32_t top = 0x4b400000u;
     uint32_t w[2] = {0, 0}, off[2] = {0, 0};
     // a NaN has code 0, and so has an infinity (whose row's inverse is 0)
-    const auto odd = [](float x, float y) { return !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY); };
-    if (__any(odd(v[0], v[1]) || odd(v[2], v[3]) || odd(v[4], v[5]) || odd(v[6], v[7])))
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd |= !(fabsf(v[i]) < INFINITY);
+    if (__any(odd))
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
 #pragma unroll

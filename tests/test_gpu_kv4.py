@@ -62,6 +62,13 @@ def test_append(q, D, dtype, pairs, rot, heads, T, scattered):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", sh.DTYPES)
+def test_append_tiles(q, D, dtype):
+    """The kernel for many tokens, of every type: its last tile of three tokens."""
+    test_append(q, D, dtype, "half", D // 2, 32, 259, False)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("T", [12, 8300])
 def test_append_odd_rows(q, D, T):
     """NaN, infinities, zeros, values whose step's reciprocal overflows, groups far below the row's largest."""
