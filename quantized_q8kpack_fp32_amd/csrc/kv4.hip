@@ -7,7 +7,7 @@
 // 4 D or 8 D bytes a token and head in, D + D/16 + 8 out: 8191 tokens of 8 heads of 128,
 // bf16, 53 MB, take 17 us, 10 of them vector instructions (divisions and codes); the
 // read back 12 (4.3 TB/s).  Few tokens are bound by the launch and two chained loads
-// (61 tokens 3.6 us, the read back 4.0).
+// (61 tokens 3.4 us, the read back 3.9).
 #include "kv4_cache.h"
 #include "kv_tile.h"
 #include "q8k_launch.h"
@@ -16,12 +16,6 @@ namespace q8k {
 
 namespace {
 
-// Maximum over aligned groups of four lanes, of magnitudes (group_max's rule).
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, dpp_f(v, 0));
-    v = fmaxf(v, dpp_f(v, 1));
-    return fmaxf(v, 0.0f);
-}
 // Codes of lanes two apart in a group of four.
 __device__ __forceinline__ uint32_t other_half(uint32_t w) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x4E, 0xF, 0xF, false);  // quad_perm 2,3,0,1
@@ -32,12 +26,42 @@ struct Row4 {
     float scale, inverse;
     uint32_t factor;
 };
+// Magnitudes compare as whole numbers do: an infinity or a NaN shows in the largest one,
+// and no maximum has to quieten its operands.
+constexpr uint32_t INF_BITS = 0x7f800000u;
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t most_of(float4 x, float4 y) {
+    const uint32_t a = max(max(magnitude(x.x), magnitude(x.y)), magnitude(x.z));
+    const uint32_t b = max(max(magnitude(x.w), magnitude(y.x)), magnitude(y.y));
+    return max(max(a, b), max(magnitude(y.z), magnitude(y.w)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+// (passes NaN over, as group_max does; leaves 0 in the place of what has code 0: a NaN, and
+// an infinity, whose row's scale is infinite)
 template <int L>
-__device__ __forceinline__ Row4 quantise_row(float4 x, float4 y) {
-    const float most = fmaxf(max4(x), max4(y)), top = quad_max(most), amax = group_max<L>(most);
+__device__ __forceinline__ Row4 quantise_row(float4& x, float4& y) {
+    float* const v[8] = {&x.x, &x.y, &x.z, &x.w, &y.x, &y.y, &y.z, &y.w};
+    uint32_t most = most_of(x, y);
+    const bool odd = __any(most >= INF_BITS);
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *v[i] = magnitude(*v[i]) > INF_BITS ? 0.0f : *v[i];
+        most = most_of(x, y);
+    }
+    const uint32_t top = max_dpp<0x4E>(max_dpp<0xB1>(most));  // of the group: quad_perm 1,0,3,2 and 2,3,0,1
+    uint32_t all = max_dpp<0x141>(top);                       // row_half_mirror
+    if (L >= 16) all = max_dpp<0x128>(all);                   // row_ror:8
+    if (L == 32) all = max(all, (uint32_t)__shfl_xor((int)all, 16, WAVE));
+    if (odd)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *v[i] = magnitude(*v[i]) == INF_BITS ? 0.0f : *v[i];
+    const float amax = __builtin_bit_cast(float, all);
     Row4 r;
     r.scale = amax / 7.0f;
-    r.factor = kv4_factor(top / amax);
+    r.factor = kv4_factor(__builtin_bit_cast(float, top) / amax);
     r.inverse = kv4_inverse(r.factor, r.scale);
     return r;
 }
@@ -166,7 +190,7 @@ __global__ __launch_bounds__(256) void kv4_append_tile_kernel(KvAppend a) {
         uint8_t* rec = a.cache + ((int64_t)(slot / KV_PAGE) * a.heads + h) * kv4_record(D);
         const int token = slot % KV_PAGE;
         float4 x = raw4f(raw[i][0], DT), y = raw4f(raw[i][1], DT);
-        const float4 u = raw4f(raw[i][2], DT), w = raw4f(raw[i][3], DT);
+        float4 u = raw4f(raw[i][2], DT), w = raw4f(raw[i][3], DT);
         if (a.rope.table && 8 * item < a.rope.dim) kv_turn(a.rope, c[i], s[i], x, y);
         if (a.rope.table && !a.rope.adjacent) natural_order<D>(turned[threadIdx.x / L], oa, ob, item, x, y);
         const Row4 k = quantise_row<L>(x, y), v = quantise_row<L>(u, w);

@@ -71,7 +71,7 @@ __device__ __forceinline__ float kv4_inverse(uint32_t f, float scale) {
     // (a step, not a quotient, is chosen: a division is too much for the compiler to take both ways)
     return 1.0f / (f == 0 || !(scale < INFINITY) ? INFINITY : kv4_factor_value(f) * scale);
 }
-// code + 8 of eight values (x and y: 0-3 and 4-7), value i's at bit SHIFT_i: kv_codes4's
+// code + 8 of eight finite values (a and b: 0-3 and 4-7), value i's at bit S_i: kv_codes4's
 // rule with 7 in the place of 127.  1.5 * 2^23 + 8 rounds a product to a whole number,
 // half to even, and leaves code + 8 in the low bits of the sum, above constant ones, which
 // come off all at once.
@@ -79,17 +79,10 @@ constexpr float KV4_ROUND = 12582920.0f;
 template <int S0, int S1, int S2, int S3, int S4, int S5, int S6, int S7>
 __device__ __forceinline__ uint64_t kv4_codes8(float4 a, float4 b, float inverse) {
 #pragma clang fp contract(off)
-    float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     constexpr int at[8] = {S0, S1, S2, S3, S4, S5, S6, S7};
     constexpr uint32_t top = 0x4b400000u;
     uint32_t w[2] = {0, 0}, off[2] = {0, 0};
-    // a NaN has code 0, and so has an infinity (whose row's inverse is 0)
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) odd |= !(fabsf(v[i]) < INFINITY);
-    if (__any(odd))
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         w[at[i] / 32] += __builtin_bit_cast(uint32_t, v[i] * inverse + KV4_ROUND) << (at[i] % 32);
