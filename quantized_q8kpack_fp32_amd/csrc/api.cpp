@@ -737,7 +737,7 @@ int qattend_weights(int dtype, int bits, const void* q, int64_t q_stride, int64_
     const WeightsPlan p = weights_plan(B, Tq, max_q, max_len, (int)q_heads, kv->kv_heads, kv->head_dim);
     Q8K_TRY(check_grid(fn, p.workgroups));
     Q8K_TRY(check_threads(fn, p.workgroups, p.threads));
-    Q8K_TRY(check_threads(fn, p.join_workgroups, p.threads));
+    if (p.split) Q8K_TRY(check_threads(fn, p.join_workgroups, p.threads));
     Q8K_TRY(check_threads(fn, B * kv->kv_heads * p.tiles_max, 64));
     w.lse = lse;
     w.old = old;
