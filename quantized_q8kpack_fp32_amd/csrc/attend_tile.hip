@@ -40,6 +40,18 @@ struct PageOps {
     uint32_t odd[2], pad;
 };
 
+// Tiles of 128 rows of heads of 64 or 128 values share a compute unit.  From so many pages
+// on, every second of the workgroups that it starts with goes first wherever several could
+// issue, so that they do not stay in the same phase of a page (8 bits, bf16, 32 heads over 4:
+// four of 1024 tokens over 8192 712 us, alike 730, of 64 values 441 and 473; the ragged
+// chunks above 752 and 798, from the 4-bit cache 758 and 798; three of 700 over 12000, hardly
+// more than one turn of workgroups, 837 and 832).  Over fewer pages it is as often a loss
+// (over 4096 371 and 366, of 64 values 222 and 249; over 2048 185.6 and 183.6, fp32 221 and
+// 218; over 1024 88.6 and 90.7; eight prompts of 500 68.9 and 68.3), in tiles of 64 rows
+// (1000 over 2000: 83.2 and 82.9) and of heads of 256 (1000 over 8000: 703 and 699) it gains
+// nothing.
+constexpr int PRIORITY_PAGES = 96;
+
 // One workgroup: 64 RT rows of one key head over its split's pages, 16 RT rows
 // a wave.  While a page is multiplied, the next one's codes, in registers since
 // the page before, become fp16 in the other buffer, and the one after that is
@@ -76,10 +88,7 @@ __global__ __launch_bounds__(64 * WAVES * HALVES, D == 64 && RT == 2 ? 3 : 2) vo
     const int rows = tile.rows;
     if (tile.row0 >= rows) return;
     const int p0 = uni(tile.p0 + it.split * it.c), p1 = uni(min(tile.p1, p0 + it.c));
-    // Of the two workgroups that a compute unit starts with, one goes first wherever both could
-    // issue, so that they do not stay in the same phase of a page (the chunks above 740 us,
-    // alike 783; from the 4-bit cache 759 and 796).
-    if (blockIdx.x >> 8 & 1) __builtin_amdgcn_s_setprio(1);
+    if (RT == 2 && p1 - p0 >= PRIORITY_PAGES && (blockIdx.x >> 8 & 1)) __builtin_amdgcn_s_setprio(1);
     if (it.splits > 1 && p0 >= p1) return;  // the join reads only chunks that some row's span meets
 
     // The wave's queries: all on their way at once, then 16 rows at a time
