@@ -438,13 +438,16 @@ int qattend_weights(int dtype, int bits, const void* q, int64_t q_stride, int64_
  * out_table int32 [B][out_pages], budget <= 64 * out_pages: the new pages.  The same
  * table (the same address): the move is in place, and the pages of the sequences must
  * be theirs alone; else no new page may be a page that page_table names or another new
- * page.  A token on a page outside [0, pages) of page_table arrives as zeros; one for
+ * page (a copy of page_table is another table: its pages would be written before they
+ * are read).  A token on a page outside [0, pages) of page_table arrives as zeros; one for
  * such a page of out_table is not written.  Nothing else of the cache changes.
  * out_weights: NULL, or rows of at least budget fp32, out_stride apart, for the kept
  * tokens' weights; may be weights with its stride, else apart from it.
  * kept int32 [B][kv_heads][budget]: the kept tokens' old indices, ascending, then -1.
  * new_len int32 [B]: min(kv_len, budget); apart from kv_len.
- * out_weights is not written behind a sequence's kept tokens. */
+ * out_weights is not written behind a sequence's kept tokens.
+ * What a new token sees goes by places in the cache, then as before: a window of
+ * qattend* counts the kept tokens, not the positions they were appended with. */
 int q8k_kv_evict(int bits, const q8k_kv_cache* kv, int64_t B, const int32_t* page_table, int64_t max_pages,
                  const int32_t* kv_len, int64_t max_len, const float* weights, int64_t w_stride, int64_t budget,
                  int64_t first, int64_t last, const int32_t* out_table, int64_t out_pages, float* out_weights,

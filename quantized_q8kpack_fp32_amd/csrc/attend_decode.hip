@@ -9,7 +9,7 @@
 // (2 D + 8 a token and head), which go from memory to the registers that the
 // matrix instructions read: 8 x 65537 tokens of 8 heads of 128 in 171 us, 6.4
 // TB/s (a streaming read of as many bytes reaches 6.7), 16 of up to 8191 in 37.9,
-// 4.4 TB/s, 5 us of it the join; from the 4-bit cache 101 us (6.0 TB/s, near what its
+// 4.4 TB/s, 5 us of it the join; from the 4-bit cache 103 us (5.9 TB/s, near what its
 // vector instructions take) and 30.  Short sequences are bound by the chain of loads
 // before the first product and by what one compute unit draws: 513 tokens 8.8 us.
 #include "attend.h"

@@ -3,17 +3,16 @@
 // codes become fp16 once for 64 or 128 rows and are read by all waves from LDS.
 //
 // Chunks of up to 1000 tokens of three prompts over up to 16001 (32 heads of 128
-// over 4, bf16, turned): 740 us, 623 TFLOP/s of the formula's, where a large matrix
-// product reaches 1143 (from the 4-bit cache, whose codes take more to widen, 759).  A query
+// over 4, bf16, turned): 753 us, 613 TFLOP/s of the formula's, where a large matrix
+// product reaches 1143 (from the 4-bit cache, whose codes take more to widen, 761).  A query
 // of two fp16 pieces makes the first product twice as long as the formula's, so that the
-// matrix work alone would take 605 us at that rate; matrix instructions are busy for some
+// matrix work alone would take 606 us at that rate; matrix instructions are busy for some
 // 36% of the cycles and vector ones (some twelve a score) for 41%, and little of the two
 // overlaps: each wave does a page's scores, probabilities and values in turn, and the waves
 // of a unit are in the same phase behind one barrier a page (scheduling groups that put the
 // instructions between each other, and priorities by phase, gained nothing).  The 1000, 443
 // and 787 tokens make 564 tiles with work, of unequal length, on 512 places, the longest
-// first; four of 1024 over 8192, 1024 tiles of nearly one length, reached 695 before the two
-// workgroups of a unit were told apart.
+// first; four of 1024 over 8192, 1024 tiles of nearly one length, reach 724.
 #include "attend.h"
 
 namespace q8k {

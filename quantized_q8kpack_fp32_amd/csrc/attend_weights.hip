@@ -6,10 +6,11 @@
 // once, and adds up its 64 tokens while the rows go by.  No atomics: one order always.
 //
 // Few rows are bound by the keys' bytes: 16 sequences of up to 8191 tokens, 32 heads of
-// 128 over 8, 8 bits, 20 us, 4.4 TB/s.  Many are bound by matrix instructions and the
-// exponentials, which hardly overlap: 2 x 1000 tokens over 8001, 32 heads over 4, 4 bits,
-// bf16 and turned, 228 us, 205 of them the products: 600 TFLOP/s of the formula's, 1200 with
-// the queries' two pieces.
+// 128 over 8, 8 bits, 20 us, 4.4 TB/s, 4 bits 17.5 us.  Many are bound by matrix instructions
+// and the exponentials, which hardly overlap: 2 x 1000 tokens over 8001, 32 heads over 4, 4
+// bits, bf16 and turned, 225 us, 205 of them the products: 600 TFLOP/s of the formula's, 1200
+// with the queries' two pieces.  A window takes no page's reading off: its unseen tokens are
+// masked (a window of 1000 over 2 x 65537, 4 bits, 22 us, as without one).
 #include <type_traits>
 
 #include "attend.h"
@@ -19,7 +20,14 @@ namespace q8k {
 namespace {
 
 constexpr int WAVES = 4, ROWS = 16;
-constexpr int LEAST_TILES = 16;  // a share of the rows has so many at least
+// A share of the rows has so many tiles at least.  It is right where the workgroups without
+// shares fill the device (the last 64 tokens of 4 x up to 16001, 32 heads over 8, 632
+// workgroups: 43 us, by 8 52, by 4 47).  Where they are fewer it leaves compute units idle,
+// and smaller shares, which are not made, would be faster (64 tokens of one sequence over
+// 1000, 16 workgroups: 32 us, by 8 25, by 4 20, by 2 18; over 4000, 64: 29, 24, 20, 22; of
+// heads of 64 23, 20, 17, 17, of 256 32, 26, 25, 28; over 16001, 256: 31, 29, 32, 43; 300
+// over 500 with one key head 38, 29, 27, 32, with eight 40, 30, 26, 29).
+constexpr int LEAST_TILES = 16;
 
 // A page's keys of one head: on their way, and as the product's operand.
 template <int D, int BITS>
@@ -470,13 +478,19 @@ hipError_t weights_d(const WeightsPlan& p, const AttendWeights& w, hipStream_t s
 
 }  // namespace
 
-// Up to FEW_ROWS rows a head: one launch, as many workgroups a sequence and head as make
-// FEW_WGS (16 sequences of up to 8191 tokens, 32 heads over 8: 20.2 us, 512 of them 24.4,
-// 1536 22.6, 2048 23.1; 1 x 65537 12.5, 12.7, 14.2 and 14.4; 8 x 65537 64, 73, 64.5 and
-// 63).  More rows: their operands in the workspace, groups of 2 WAVES pages (of 256 values
-// WAVES), and the rows in as many shares as make MANY_WGS workgroups (2 x 1000 tokens over
-// 8001, 32 heads over 4: 228 us, 1024 of them 249, 4096 241), each of LEAST_TILES tiles at
-// least (the last 64 of 4 x up to 16001, 32 over 8, 16 tiles: 44 us, by 8 48.5, by 4 59).
+// Up to FEW_ROWS rows a head, what four tiles in LDS hold: one launch (16 sequences of up to
+// 8191 tokens, 32 heads over 8, 4 bits: of 5 new tokens, 20 rows, 24.7 us, as operands in the
+// workspace 30.8; of 8 28.9 and 33.4; of 16, 64 rows, 35.6 and 38.2; one sequence of 16 over
+// 8191 9.0 and 15.9), as many workgroups a sequence and head as make FEW_WGS (16 sequences of
+// up to 8191 tokens, 8 bits: 20.2 us, 512 of them 24.4, 1536 22.6, 2048 23.1; 1 x 65537 12.5,
+// 12.7, 14.2 and 14.4; 8 x 65537 64, 73, 64.5 and 63; 4 bits, 16 x up to 8191 17.5, by 512
+// 21.3, by 2048 19.4, five new tokens each 24.7, 22.8 and 29.3; 16 x 16001 of heads of 64 26.5,
+// 30.6 and 26.5, of 256 66.9, 65.8 and 72.3).  More rows: their operands in the workspace,
+// groups of 2 WAVES pages (of 256 values WAVES), and the rows in as many shares as make
+// MANY_WGS workgroups (2 x 1000 tokens over 8001, 32 heads over 4: 225 us, by 1024 230, by 4096
+// 240, under a window of 1000 153, 150 and 160; of heads of 64 151, 149 and 154, of 256 409, 419
+// and 419; up to 700 of three over up to 6000, 32 over 8: 129, 147 and 131; 1000 over 16001,
+// fp32: 223, 230 and 229), each of LEAST_TILES tiles at least.
 constexpr int64_t FEW_ROWS = 64, FEW_WGS = 1024, MANY_WGS = 2048;
 
 WeightsPlan weights_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int q_heads, int heads, int D) {

@@ -5,9 +5,10 @@
 //   scale = amax/7,  factor_y = the least 8-bit float >= max|x_y| / amax,
 //   code = round(x / (factor_y scale)).
 // 4 D or 8 D bytes a token and head in, D + D/16 + 8 out: 8191 tokens of 8 heads of 128,
-// bf16, 53 MB, take 17 us, 10 of them vector instructions (divisions and codes); the
-// read back 12 (4.3 TB/s).  Few tokens are bound by the launch and two chained loads
-// (61 tokens 3.4 us, the read back 3.9).
+// bf16, half turned, 45 MB, take 16 us, about 11 of them vector instructions (twelve
+// divisions a lane, which the four lanes of a group repeat, and the codes); the read back,
+// 43 MB, 11 (3.8 TB/s).  Few tokens are bound by the launch and two chained loads (61
+// tokens 3.4 us, the read back 3.9).
 #include "kv4_cache.h"
 #include "kv_tile.h"
 #include "q8k_launch.h"

@@ -3,11 +3,14 @@
 // others, those of the largest weights (equal ones by ascending index), in order;
 // what the cache holds of these moves to the front of the sequence's new pages.
 //
-// Two launches: the choice (one workgroup a sequence and head; 8 rows of 2111 weights 6.3
-// us, a chain of barriers, 128 of up to 16001 15.0) and the move (4000 of up to 16001
-// tokens of 128 rows, 8 bits, heads of 128: 96 us, 4.2 TB/s of what it touches, since a
-// page's values lie row by row and a line of 64 tokens is read for one).  A page's places
-// beyond the kept tokens are left as they were.
+// Two launches: the choice (one workgroup a sequence and head; 8 rows of 2111 weights 6.1
+// us, a chain of barriers, 128 of up to 16001 14.9, 8 of 65537, read again for each digit,
+// 68) and the move (4000 of up to 16001 tokens of 128 rows, 8 bits, heads of 128: 96 us, 4.2
+// TB/s of what it touches, since a page's values lie row by row and a line of 64 tokens is
+// read for one; 2048 of 2111 tokens of 8 rows, 4 bits, 4.4).  In place the pages of a head go
+// one after another, each behind a chain of loads and stores: 47 us for the 2048 of 2111,
+// 184 for the 4000 of up to 16001.  A page's places beyond the kept tokens are left as they
+// were.
 #include "attend.h"
 #include "q8k_launch.h"
 
@@ -307,6 +310,10 @@ int64_t evict_workgroups(int bits, int D, int64_t B, int64_t heads, int64_t budg
 }
 int evict_threads() { return THREADS; }
 
+// Four weights a thread for rows that they hold, else sixteen (both launches, 200 kept, 8
+// heads of 128, 4 bits: 8 rows of 2111 9.6 us, of sixteen a thread 13.3, 8 of 4096 10.0 and
+// 13.7, 128 18.8 and 23.3; 8 of 5000 14.4, of four a thread, in two turns, 14.2, 8 of 16000
+// 15.4 and 21.8, 128 33.8 and 40.2, 8 of 65537 66.5 and 63.9).
 hipError_t launch_kv_evict(int bits, int D, const KvEvict& a, bool in_place, hipStream_t s) {
     if (a.max_len <= 4 * THREADS)
         Q8K_LAUNCH((kv_evict_choose_kernel<4>), dim3((unsigned)(a.B * a.heads)), dim3(THREADS), 0, s, a);
