@@ -411,7 +411,8 @@ int qattend_kv4(int dtype, const void* q, int64_t q_stride, int64_t q_heads, con
  *                      heads a of key head h of e^(s_j - lse[i][a])
  * for the tokens j < len, s_j as in qattend.  Arguments up to rope: qattend's, over a
  * cache of `bits` 8 or 4.  lse fp32 [Tq][q_heads]: what attention returned for these
- * rows (a row of -inf adds nothing, one of NaN makes what it sees NaN).
+ * rows (a row of -inf adds nothing, whatever it and what it sees hold; one of NaN
+ * makes what it sees NaN).
  * old, weights: rows of at least max_len fp32, one for each sequence and key head [B]
  * [kv_heads], w_stride elements apart; they may be the same.  old NULL: none.  old is
  * not read for the new tokens, which have got nothing before, nor from len on; weights

@@ -72,8 +72,8 @@ __device__ __forceinline__ RowInfo info_of(const AttendWeights& w, const Sequenc
         const TileRow tr = row_of_tile(w.a, tile, col);
         const Span sp = span_of(w.a, seq, tr.tok);
         const float lse = w.lse[q_row_of(w.a, seq, h, tr)];
-        // (a row of -inf sees nothing that counts)
-        o = RowInfo{1.0f, lse == -INFINITY ? INFINITY : lse * LOG2E, sp.first, sp.last};
+        // (a row of -inf sees nothing: what it would meet may be NaN)
+        if (lse != -INFINITY) o = RowInfo{1.0f, lse * LOG2E, sp.first, sp.last};
     }
     return o;
 }
