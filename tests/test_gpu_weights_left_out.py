@@ -46,3 +46,22 @@ def test_rows_of_minus_infinity_add_nothing(q, bits, odd, D, G, news):
         qx[last[0]], qx[last[1], :, 3] = np.nan, np.inf
     got = run(q, bits, raw, table, cu, lens, qx, D, "f32", lse, old, 0.5)
     check(got, want, bound, lens)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D,G,news,window", [(64, 4, [3, 2], 100), (128, 8, [5, 3], 70), (256, 2, [90, 70], 65), (64, 1, [1, 1], 1)])
+def test_rows_of_nan_reach_what_they_see_alone(q, bits, D, G, news, window):
+    """The lse of one query head of the first new token is NaN: so are, for its key head, the tokens of its window."""
+    g = np.random.default_rng(D + window)
+    lens = [300, 200]
+    raw, table, cu = lh.paged(g, bits, D, 2, lens, news)
+    qx = g.standard_normal((int(cu[-1]), 2 * G, D)).astype(np.float32)
+    args = (qx, cu, raw, table, lens, D ** -0.5, window, None, None, "half", D)
+    lse = lh.attend(bits, *args, "f32")[1].astype(np.float32)
+    lse[cu[:2], G] = np.nan  # the second key head's first
+    want, bound = lh.weights(bits, *args, np.nan_to_num(lse, nan=-np.inf), None, 1.0)
+    for b in range(2):
+        p = lens[b] - news[b]
+        want[b, 1, max(0, p - window + 1): p + 1] = np.nan
+    got = run(q, bits, raw, table, cu, lens, qx, D, "f32", lse, window=window)
+    check(got, want, bound, lens)
