@@ -447,36 +447,61 @@ def q8k_kv4_bytes(pages: int, kv_heads: int, head_dim: int) -> int:
     return int(lib.q8k_kv4_bytes(pages, kv_heads, head_dim))
 
 
-def _append(call, bits, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream):
-    dev, t = _device(), _TYPES.get(dtype)
-    row = kv.kv_heads * kv.head_dim
-    _check(call(dtype, _rows(dev, "k", k, t, T, k_stride, row), k_stride,
-                _rows(dev, "v", v, t, T, v_stride, row), v_stride, T,
-                _flat(dev, "pos", pos, torch.int32, 0 if rope is None else T), _rope(dev, rope),
-                _flat(dev, "slots", slots, torch.int32, T), _kv(dev, kv, bits), _stream_of(dev, stream)))
+# The calls of the caches of 8 and of 4 bits differ in the C function alone: made twice, so that a call is one frame.
+def _named(name, f):
+    f.__name__ = f.__qualname__ = name
+    return f
 
 
-def q8k_kv_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
-    _append(lib.q8k_kv_append, 8, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream)
+def _append(name, bits):
+    call = getattr(lib, name)
+
+    def append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
+        dev, t = _device(), _TYPES.get(dtype)
+        row = kv.kv_heads * kv.head_dim
+        _check(call(dtype, _rows(dev, "k", k, t, T, k_stride, row), k_stride,
+                    _rows(dev, "v", v, t, T, v_stride, row), v_stride, T,
+                    _flat(dev, "pos", pos, torch.int32, 0 if rope is None else T), _rope(dev, rope),
+                    _flat(dev, "slots", slots, torch.int32, T), _kv(dev, kv, bits), _stream_of(dev, stream)))
+
+    return _named(name, append)
 
 
-def q8k_kv4_append(dtype: int, k, k_stride: int, v, v_stride: int, T: int, pos, rope, slots, kv, stream=None) -> None:
-    _append(lib.q8k_kv4_append, 4, dtype, k, k_stride, v, v_stride, T, pos, rope, slots, kv, stream)
+def _read(name, bits):
+    call = getattr(lib, name)
+
+    def read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
+        dev, t = _device(), _TYPES.get(dtype)
+        n = T * kv.kv_heads * kv.head_dim
+        _check(call(dtype, _kv(dev, kv, bits), _flat(dev, "slots", slots, torch.int32, T), T, _flat(dev, "k", k, t, n),
+                    _flat(dev, "v", v, t, n), _stream_of(dev, stream)))
+
+    return _named(name, read)
 
 
-def _read(call, bits, dtype, kv, slots, T, k, v, stream):
-    dev, t = _device(), _TYPES.get(dtype)
-    n = T * kv.kv_heads * kv.head_dim
-    _check(call(dtype, _kv(dev, kv, bits), _flat(dev, "slots", slots, torch.int32, T), T, _flat(dev, "k", k, t, n),
-                _flat(dev, "v", v, t, n), _stream_of(dev, stream)))
+def _attend(name, bits):
+    call = getattr(lib, name)
+
+    def attend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
+               max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
+               ws_bytes: int = 0, stream=None) -> None:
+        dev, t = _device(), _TYPES.get(dtype)
+        i32 = torch.int32
+        row = q_heads * kv.head_dim
+        _check(call(dtype, _rows(dev, "q", q, t, Tq, q_stride, row), q_stride, q_heads, _kv(dev, kv, bits), B,
+                    _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
+                    _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+                    _flat(dev, "kv_len", kv_len, i32, B), max_len, scale, window,
+                    _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
+                    _flat(dev, "out", out, t, Tq * row), _flat(dev, "lse", lse, torch.float32, Tq * q_heads),
+                    _bytes(dev, "ws", ws, ws_bytes), ws_bytes, _stream_of(dev, stream)))
+
+    return _named(name, attend)
 
 
-def q8k_kv_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
-    _read(lib.q8k_kv_read, 8, dtype, kv, slots, T, k, v, stream)
-
-
-def q8k_kv4_read(dtype: int, kv, slots, T: int, k, v, stream=None) -> None:
-    _read(lib.q8k_kv4_read, 4, dtype, kv, slots, T, k, v, stream)
+q8k_kv_append, q8k_kv4_append = _append("q8k_kv_append", 8), _append("q8k_kv4_append", 4)
+q8k_kv_read, q8k_kv4_read = _read("q8k_kv_read", 8), _read("q8k_kv4_read", 4)
+qattend, qattend_kv4 = _attend("qattend", 8), _attend("qattend_kv4", 4)
 
 
 def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
@@ -485,27 +510,6 @@ def qattend_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_l
 
 def qattend_kv4_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
     return int(lib.qattend_kv4_workspace_bytes(kv.ref, q_heads, B, Tq, max_q, max_len))
-
-
-def _attend(call, bits, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len, max_len,
-            scale, window, pos, rope, out, lse, ws, ws_bytes, stream):
-    dev, t = _device(), _TYPES.get(dtype)
-    i32 = torch.int32
-    row = q_heads * kv.head_dim
-    _check(call(dtype, _rows(dev, "q", q, t, Tq, q_stride, row), q_stride, q_heads, _kv(dev, kv, bits), B,
-                _flat(dev, "cu_q", cu_q, i32, B + 1), Tq, max_q,
-                _flat(dev, "page_table", page_table, i32, B * max_pages), max_pages,
-                _flat(dev, "kv_len", kv_len, i32, B), max_len, scale, window,
-                _flat(dev, "pos", pos, i32, 0 if rope is None else Tq), _rope(dev, rope),
-                _flat(dev, "out", out, t, Tq * row), _flat(dev, "lse", lse, torch.float32, Tq * q_heads),
-                _bytes(dev, "ws", ws, ws_bytes), ws_bytes, _stream_of(dev, stream)))
-
-
-def qattend_kv4(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
-                max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
-                ws_bytes: int = 0, stream=None) -> None:
-    _attend(lib.qattend_kv4, 4, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len, max_len,
-            scale, window, pos, rope, out, lse, ws, ws_bytes, stream)
 
 
 def qattend_weights_workspace_bytes(kv, q_heads: int, B: int, Tq: int, max_q: int, max_len: int) -> int:
@@ -541,13 +545,6 @@ def q8k_kv_evict(kv, B: int, page_table, max_pages: int, kv_len, max_len: int, w
         w_stride, budget, first, last, _flat(dev, "out_table", out_table, i32, B * out_pages), out_pages,
         _grid(dev, "out_weights", out_weights, rows, out_stride, budget), out_stride,
         _flat(dev, "kept", kept, i32, rows * budget), _flat(dev, "new_len", new_len, i32, B), _stream_of(dev, stream)))
-
-
-def qattend(dtype: int, q, q_stride: int, q_heads: int, kv, B: int, cu_q, Tq: int, max_q: int, page_table,
-            max_pages: int, kv_len, max_len: int, scale: float, window: int, pos, rope, out, lse=None, ws=None,
-            ws_bytes: int = 0, stream=None) -> None:
-    _attend(lib.qattend, 8, dtype, q, q_stride, q_heads, kv, B, cu_q, Tq, max_q, page_table, max_pages, kv_len, max_len,
-            scale, window, pos, rope, out, lse, ws, ws_bytes, stream)
 
 
 def qlogprobs_workspace_bytes(T: int, V: int, topn: int) -> int:
